@@ -92,6 +92,12 @@ def lib() -> ctypes.CDLL:
             L.kvevict_check.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
             L.kvevict_strerror.argtypes = [I]
             L.kvevict_strerror.restype = ctypes.c_char_p
+            for n in ("kvevict_window_attention", "kvevict_shared_prefix_attention", "kvevict_rotary"):
+                getattr(L, n).argtypes = [ctypes.c_char_p, P]
+                getattr(L, n).restype = I
+            for n in ("kvevict_window_attention_workspace_bytes", "kvevict_shared_prefix_attention_workspace_bytes"):
+                getattr(L, n).argtypes = [ctypes.c_char_p, ctypes.POINTER(SZ)]
+                getattr(L, n).restype = I
             L.kvevict_destroy.argtypes = [P]
             L.kvevict_destroy.restype = None
             for n in ("kvevict_state_bytes", "kvevict_create", "kvevict_prefill", "kvevict_prefill_scored_workspace_bytes",

@@ -1,0 +1,294 @@
+// api_ops.cu -- host side of the attention operators (include/kvevict_ops.h):
+// argument checks, how the work is cut into items, and the launches.
+#include <algorithm>
+#include <cmath>
+
+#include "kvevict_ops.h"
+#include "window_attn.h"
+
+using namespace kvevict;
+
+namespace {
+
+constexpr int kSMs = 152;
+constexpr int64_t kMaxRows = int64_t{1} << 30;
+constexpr int kMaxGroup = 64;
+constexpr int kMaxParts = 64;  // parts a unit's keys are split into at most
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// The stride of an axis of one entry is not looked at; any other is a positive
+// multiple of 16 bytes.
+bool strides_ok(const int64_t *s, const int64_t *sizes, int n, int elem)
+{
+    for (int i = 0; i < n; ++i)
+        if (sizes[i] > 1 && (s[i] <= 0 || s[i] >= (int64_t{1} << 38) || (s[i] * elem) % 16)) return false;
+    return true;
+}
+
+int check_shape(const kvevict_attention_args *a)
+{
+    if (!a) return KVEVICT_ERR_INVALID_ARG;
+    if (a->dtype != KVEVICT_F32 && a->dtype != KVEVICT_BF16) return KVEVICT_ERR_INVALID_ARG;
+    if (a->head_dim != 64 && a->head_dim != 128) return KVEVICT_ERR_INVALID_ARG;
+    if (a->n_kv_heads < 1 || a->n_kv_heads > 65535 || a->n_q_heads < 1 || a->n_q_heads % a->n_kv_heads ||
+        a->n_q_heads / a->n_kv_heads > kMaxGroup)
+        return KVEVICT_ERR_INVALID_ARG;
+    if (a->batch < 0 || a->batch > (1 << 24) || a->n_sink < 0 || a->window < 0) return KVEVICT_ERR_INVALID_ARG;
+    if (a->q_rows < 0 || a->k_rows < 0 || a->q_rows >= kMaxRows || a->k_rows >= kMaxRows) return KVEVICT_ERR_INVALID_ARG;
+    if (!(a->scale >= 0.f) || !std::isfinite(a->scale)) return KVEVICT_ERR_INVALID_ARG;
+    if (!a->q_starts != !a->k_starts) return KVEVICT_ERR_INVALID_ARG;
+    if (a->q_starts) {
+        if (a->q_lens || a->kv_lens || a->max_q < 0 || a->max_k < 0) return KVEVICT_ERR_INVALID_ARG;
+        if (!aligned(a->q_starts, 4) || !aligned(a->k_starts, 4)) return KVEVICT_ERR_INVALID_ARG;
+    }
+    const int64_t per = a->q_starts ? 1 : a->batch;
+    if (per * a->n_q_heads * a->q_rows >= (int64_t{1} << 40)) return KVEVICT_ERR_INVALID_ARG;
+    return KVEVICT_OK;
+}
+
+// The keys a tile of rows can see at most, as tiles of `keys`.
+int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens, int keys)
+{
+    const int64_t all = (max_k + keys - 1) / keys;
+    if (!window) return all;
+    return std::min(all, (static_cast<int64_t>(n_sink) + keys - 1) / keys + (window + tokens - 1 + keys - 1) / keys + 1);
+}
+
+// Cuts a problem into items: tiles of `rows` rows, and parts of the key range
+// where the tiles alone would leave SMs idle. Four items an SM keep the end of
+// the launch short (a quarter of an item's time idle on average), two key tiles
+// a part at least pay for the part's own output.
+void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int64_t max_k, int64_t other_items, bool may_split)
+{
+    const int per = rows / G;
+    p.q_tiles = (p.max_q + per - 1) / per;
+    const int64_t items = static_cast<int64_t>(p.batch) * Hkv * p.q_tiles;
+    p.splits = 1;
+    if (may_split && items + other_items < 2 * kSMs) {
+        const int64_t tiles = key_tiles(max_k, p.n_sink, p.causal ? p.window : 0, std::min(per, p.max_q), keys);
+        const int64_t want = (4 * kSMs + items - 1) / std::max<int64_t>(1, items);
+        p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, (tiles + 1) / 2, kMaxParts})));
+    }
+}
+
+struct Plan {
+    AttnParams p{};
+    bool few = false;
+    int64_t items = 0;
+    size_t bytes = 0;  // workspace
+};
+
+// rows a tile holds: 16 where a unit has no more, else 64
+bool few_rows(int G, int64_t max_q) { return G * max_q <= kAttnF32FewRows; }
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Slots and workspace of a cut plan; the second problem's slots follow the first's.
+int finish(Plan &w, int head_dim)
+{
+    AttnParams &p = w.p;
+    p.slots = 0;
+    w.items = 0;
+    for (int i = 0; i < p.n_problems; ++i) {
+        AttnProblem &q = p.pr[i];
+        q.slot0 = p.slots;
+        p.slots += q.splits;
+        const int64_t n = static_cast<int64_t>(q.batch) * p.Hkv * q.q_tiles * q.splits;
+        if (n >= (int64_t{1} << 30)) return KVEVICT_ERR_INVALID_ARG;
+        q.n_items = static_cast<int>(n);
+        w.items += n;
+    }
+    w.bytes = 0;
+    if (p.slots > 1)
+        w.bytes = up256(static_cast<size_t>(p.slots) * p.rows * head_dim * 4) + up256(static_cast<size_t>(p.slots) * p.rows * 4);
+    return KVEVICT_OK;
+}
+
+int plan_window(const kvevict_attention_args *a, Plan &w)
+{
+    AttnParams &p = w.p;
+    p.Hq = a->n_q_heads;
+    p.Hkv = a->n_kv_heads;
+    p.G = p.Hq / p.Hkv;
+    p.n_problems = 1;
+    AttnProblem &q = p.pr[0];
+    const bool packed = a->q_starts != nullptr;
+    q.batch = a->batch;
+    q.causal = 1;
+    q.n_sink = static_cast<int>(std::min<int64_t>(a->n_sink, a->k_rows));
+    q.window = a->window >= a->k_rows ? 0 : a->window;  // a window as long as the keys hides nothing
+    q.q_rows = static_cast<int>(a->q_rows);
+    q.k_rows = static_cast<int>(a->k_rows);
+    q.max_q = packed ? static_cast<int>(std::min<int64_t>(a->max_q, a->q_rows)) : q.q_rows;
+    const int64_t max_k = packed ? std::min<int64_t>(a->max_k, a->k_rows) : a->k_rows;
+    const int64_t N = a->q_rows;
+    p.rows = (packed ? 1 : static_cast<int64_t>(a->batch)) * p.Hq * N;
+    if (packed) {
+        q.rs[0] = 0; q.rs[1] = 1; q.rs[2] = p.Hq;
+    } else {
+        q.rs[0] = p.Hq * N; q.rs[1] = N; q.rs[2] = 1;
+    }
+    w.few = p.G <= kAttnF32FewRows && few_rows(p.G, q.max_q);
+    cut(q, p.G, p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows, kAttnF32Keys, max_k, 0, true);
+    return finish(w, a->head_dim);
+}
+
+int plan_shared(const kvevict_shared_prefix_args *s, Plan &w)
+{
+    const kvevict_attention_args *a = &s->a;
+    AttnParams &p = w.p;
+    p.Hq = a->n_q_heads;
+    p.Hkv = a->n_kv_heads;
+    p.G = p.Hq / p.Hkv;
+    p.n_problems = 2;
+    p.rows = static_cast<int64_t>(a->batch) * p.Hq;
+    // the prefix: one sequence whose tokens are the batch's sequences
+    AttnProblem &x = p.pr[0];
+    x.batch = 1;
+    x.q_rows = x.max_q = a->batch;
+    x.k_rows = static_cast<int>(s->prefix_rows);
+    x.rs[0] = 0; x.rs[1] = 1; x.rs[2] = p.Hq;
+    // the suffixes: one token each
+    AttnProblem &y = p.pr[1];
+    y.batch = a->batch;
+    y.q_rows = y.max_q = 1;
+    y.k_rows = static_cast<int>(a->k_rows);
+    y.rs[0] = p.Hq; y.rs[1] = 1; y.rs[2] = 0;
+    w.few = p.G <= kAttnF32FewRows && few_rows(p.G, a->batch);
+    const int rows = w.few ? kAttnF32FewRows : kAttnF32Rows;
+    cut(x, p.G, p.Hkv, rows, kAttnF32Keys, x.k_rows, 0, true);
+    cut(y, p.G, p.Hkv, rows, kAttnF32Keys, y.k_rows, 0, true);
+    return finish(w, a->head_dim);
+}
+
+int check_tensors(const kvevict_attention_args *a, bool needs_k)
+{
+    const int elem = a->dtype == KVEVICT_F32 ? 4 : 2;
+    const int64_t seqs = a->q_starts ? 1 : a->batch;
+    const int64_t qn[3] = {seqs, a->n_q_heads, a->q_rows}, kn[3] = {seqs, a->n_kv_heads, a->k_rows};
+    if (!a->q || !a->out || !aligned(a->q, 16) || !aligned(a->out, 16) || !strides_ok(a->q_stride, qn, 3, elem) ||
+        !strides_ok(a->out_stride, qn, 3, elem))
+        return KVEVICT_ERR_INVALID_ARG;
+    if (needs_k && (!a->k || !a->v || !aligned(a->k, 16) || !aligned(a->v, 16) || !strides_ok(a->k_stride, kn, 3, elem) ||
+                    !strides_ok(a->v_stride, kn, 3, elem)))
+        return KVEVICT_ERR_INVALID_ARG;
+    if (!aligned(a->lse, 4) || !aligned(a->q_lens, 4) || !aligned(a->kv_lens, 4) || !aligned(a->error_word, 4))
+        return KVEVICT_ERR_INVALID_ARG;
+    return KVEVICT_OK;
+}
+
+int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
+{
+    AttnParams &p = w.p;
+    if (w.bytes) {
+        if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < w.bytes) return KVEVICT_ERR_INVALID_ARG;
+        p.part_o = static_cast<float *>(a->workspace);
+        p.part_l = reinterpret_cast<float *>(static_cast<uint8_t *>(a->workspace) +
+                                             up256(static_cast<size_t>(p.slots) * p.rows * a->head_dim * 4));
+    }
+    const double scale = a->scale > 0.f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->head_dim));
+    p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    p.out = a->out;
+    p.lse = a->lse;
+    p.err = a->error_word;
+    const bool bf16 = a->dtype == KVEVICT_BF16;
+    cudaError_t e = launch_attn_f32(p, a->head_dim, bf16, w.few, st);
+    if (e == cudaSuccess && p.slots > 1) e = launch_attn_join(p, a->head_dim, bf16, st);
+    return e == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
+}
+
+void copy3(long long (&d)[3], const int64_t *s)
+{
+    for (int i = 0; i < 3; ++i) d[i] = s[i];
+}
+
+int check_shared(const kvevict_shared_prefix_args *s)
+{
+    if (!s) return KVEVICT_ERR_INVALID_ARG;
+    const int rc = check_shape(&s->a);
+    if (rc) return rc;
+    const kvevict_attention_args *a = &s->a;
+    if (a->q_starts || a->k_starts || a->q_lens || a->n_sink || a->window || a->q_rows != 1 || s->prefix_rows < 0 ||
+        s->prefix_rows >= kMaxRows)
+        return KVEVICT_ERR_INVALID_ARG;
+    return KVEVICT_OK;
+}
+
+}  // namespace
+
+extern "C" int kvevict_window_attention_workspace_bytes(const kvevict_attention_args *a, size_t *bytes)
+{
+    int rc = check_shape(a);
+    if (rc) return rc;
+    if (!bytes) return KVEVICT_ERR_INVALID_ARG;
+    Plan w;
+    rc = plan_window(a, w);
+    if (rc == KVEVICT_OK) *bytes = w.bytes;
+    return rc;
+}
+
+extern "C" int kvevict_window_attention(const kvevict_attention_args *a, void *cuda_stream)
+{
+    int rc = check_shape(a);
+    if (rc) return rc;
+    Plan w;
+    rc = plan_window(a, w);
+    if (rc) return rc;
+    if (w.items == 0) return KVEVICT_OK;  // no query rows
+    rc = check_tensors(a, a->k_rows > 0);
+    if (rc) return rc;
+    AttnProblem &q = w.p.pr[0];
+    q.q = a->q; q.k = a->k; q.v = a->v;
+    copy3(q.qs, a->q_stride);
+    copy3(q.ks, a->k_stride);
+    copy3(q.vs, a->v_stride);
+    copy3(q.os, a->out_stride);
+    if (a->q_starts) q.os[0] = 0;
+    q.q_starts = a->q_starts; q.k_starts = a->k_starts; q.q_lens = a->q_lens; q.k_lens = a->kv_lens;
+    return run(a, w, static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" int kvevict_shared_prefix_attention_workspace_bytes(const kvevict_shared_prefix_args *s, size_t *bytes)
+{
+    int rc = check_shared(s);
+    if (rc) return rc;
+    if (!bytes) return KVEVICT_ERR_INVALID_ARG;
+    Plan w;
+    rc = plan_shared(s, w);
+    if (rc == KVEVICT_OK) *bytes = w.bytes;
+    return rc;
+}
+
+extern "C" int kvevict_shared_prefix_attention(const kvevict_shared_prefix_args *s, void *cuda_stream)
+{
+    int rc = check_shared(s);
+    if (rc) return rc;
+    const kvevict_attention_args *a = &s->a;
+    Plan w;
+    rc = plan_shared(s, w);
+    if (rc) return rc;
+    if (a->batch == 0) return KVEVICT_OK;
+    rc = check_tensors(a, a->k_rows > 0);
+    if (rc) return rc;
+    const int elem = a->dtype == KVEVICT_F32 ? 4 : 2;
+    const int64_t pn[2] = {a->n_kv_heads, s->prefix_rows};
+    if (s->prefix_rows > 0 && (!s->k_prefix || !s->v_prefix || !aligned(s->k_prefix, 16) || !aligned(s->v_prefix, 16) ||
+                               !strides_ok(s->k_prefix_stride, pn, 2, elem) || !strides_ok(s->v_prefix_stride, pn, 2, elem)))
+        return KVEVICT_ERR_INVALID_ARG;
+    AttnProblem &x = w.p.pr[0], &y = w.p.pr[1];
+    x.q = y.q = a->q;
+    x.qs[0] = 0; x.qs[1] = a->q_stride[1]; x.qs[2] = a->q_stride[0];
+    y.qs[0] = a->q_stride[0]; y.qs[1] = a->q_stride[1]; y.qs[2] = 0;
+    x.os[0] = 0; x.os[1] = a->out_stride[1]; x.os[2] = a->out_stride[0];
+    y.os[0] = a->out_stride[0]; y.os[1] = a->out_stride[1]; y.os[2] = 0;
+    x.k = s->k_prefix; x.v = s->v_prefix;
+    x.ks[0] = x.vs[0] = 0;
+    x.ks[1] = s->k_prefix_stride[0]; x.ks[2] = s->k_prefix_stride[1];
+    x.vs[1] = s->v_prefix_stride[0]; x.vs[2] = s->v_prefix_stride[1];
+    y.k = a->k; y.v = a->v;
+    copy3(y.ks, a->k_stride);
+    copy3(y.vs, a->v_stride);
+    y.k_lens = a->kv_lens;
+    return run(a, w, static_cast<cudaStream_t>(cuda_stream));
+}

@@ -1,0 +1,301 @@
+"""Operators around the decode step (include/kvevict_ops.h): argument checks
+and marshalling only, every step runs in the library's kernels.
+
+Work is queued on the current stream of the tensors' device. Nothing here
+waits for the GPU, and every call can be captured in a CUDA graph.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import struct
+
+import torch
+
+from ._lib import BF16, F32, check, lib
+
+_DT = {torch.float32: F32, torch.bfloat16: BF16}
+
+# The argument structs of include/kvevict_ops.h, as their fields in order.
+_ATTN = struct.Struct("@9if2q5P12q4PPNP")
+_SHARED = struct.Struct("@9if2q5P12q4PPNP2P5q")
+_ROT = struct.Struct("@8i2q4P12qP3qPf4x")
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name}: need float32 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: need a CUDA tensor, got one on {t.device}")
+    return dt
+
+
+def _like(t: torch.Tensor, q: torch.Tensor, dims: int, name: str, shape=None) -> torch.Tensor:
+    if t.dtype != q.dtype or t.device != q.device or t.dim() != dims or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: need a {q.dtype} tensor of {dims if shape is None else tuple(shape)} "
+                         f"{'axes' if shape is None else ''} on {q.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t
+
+
+def _ints(t, n: int, q: torch.Tensor, name: str) -> int:
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.device != q.device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous int32 tensor of {n} on {q.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _scale(scale) -> float:
+    if scale is None:
+        return 0.0
+    if not (scale > 0 and math.isfinite(scale)):
+        raise ValueError("scale: need a positive finite number")
+    return float(scale)
+
+
+def _outputs(q, out, lse, return_lse, lse_shape):
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _like(out, q, q.dim(), "out", q.shape)
+    if lse is None:
+        if return_lse:
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.device != q.device or lse.shape != lse_shape or not lse.is_contiguous():
+        raise ValueError(f"lse: need a contiguous float32 tensor of {tuple(lse_shape)} on {q.device}")
+    return out, lse
+
+
+def _workspace(workspace, need: int, q: torch.Tensor):
+    if need == 0:
+        return None, 0, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    size = workspace.numel() * workspace.element_size()
+    if workspace.device != q.device or not workspace.is_contiguous() or size < need:
+        raise ValueError(f"workspace: need {need} contiguous bytes on {q.device}")
+    return workspace, workspace.data_ptr(), size
+
+
+def _error_word(t, q: torch.Tensor) -> int:
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.device != q.device or t.numel() < 1:
+        raise ValueError(f"error_word: need an int32 tensor on {q.device}")
+    return t.data_ptr()
+
+
+def _on(q: torch.Tensor, call):
+    """call(stream) with q's device current."""
+    dev = q.device.index
+    if dev == torch.cuda.current_device():
+        return call(torch.cuda.current_stream(dev).cuda_stream)
+    with torch.cuda.device(dev):
+        return call(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _need(name: str, args: bytes) -> int:
+    n = ctypes.c_size_t(0)
+    check(getattr(lib(), name)(args, n), name)
+    return n.value
+
+
+def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sink: int = 0, window: int | None = None,
+                     scale: float | None = None, q_starts: torch.Tensor | None = None,
+                     k_starts: torch.Tensor | None = None, max_q: int | None = None, max_k: int | None = None,
+                     q_lens: torch.Tensor | None = None, kv_lens: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None, return_lse: bool = False,
+                     workspace: torch.Tensor | None = None, error_word: torch.Tensor | None = None):
+    """Attention in which a query at position p sees the keys up to p that are
+    among the first n_sink or the newest `window` (None: all of them). The
+    queries are the last rows of their sequence: whole prompts, chunks of one,
+    or single tokens.
+
+    Padded: q [B][Hq][N][d], k and v [B][Hkv][M][d]; q_lens and kv_lens (int32
+    [B] on the device) say how many rows are real. Packed (q_starts and
+    k_starts, int32 [B + 1] on the device, with max_q and max_k the longest
+    sequences): q [T][Hq][d], k and v [S][Hkv][d]. Any strides, d contiguous.
+    Returns out (as q), or (out, lse) with return_lse or an lse tensor: fp32
+    [B][Hq][N], or [T][Hq] packed. A row that sees nothing gives 0 and -inf.
+    """
+    dt = _dtype(q, "q")
+    packed = q_starts is not None
+    dims = 3 if packed else 4
+    _like(q, q, dims, "q")
+    _like(k, q, dims, "k")
+    _like(v, q, dims, "v", k.shape)
+    if window is None:
+        window = 0
+    elif window < 1:
+        raise ValueError("window: need at least 1, or None for no window")
+    if n_sink < 0:
+        raise ValueError("n_sink: need 0 or more")
+    d = q.shape[-1]
+    if k.shape[-1] != d:
+        raise ValueError(f"k: head_dim {k.shape[-1]}, q has {d}")
+    if packed:
+        if k_starts is None or max_q is None or max_k is None or q_lens is not None or kv_lens is not None:
+            raise ValueError("packed: give q_starts, k_starts, max_q and max_k, and no lengths")
+        B = q_starts.shape[0] - 1
+        N, Hq, M, Hkv = q.shape[0], q.shape[1], k.shape[0], k.shape[1]
+        qs, ks = (0, q.stride(1), q.stride(0)), (0, k.stride(1), k.stride(0))
+        vs = (0, v.stride(1), v.stride(0))
+        lse_shape = q.shape[:2]
+    else:
+        if k_starts is not None:
+            raise ValueError("k_starts: goes with q_starts")
+        B, Hq, N = q.shape[:3]
+        if k.shape[0] != B:
+            raise ValueError(f"k: {k.shape[0]} sequences, q has {B}")
+        Hkv, M = k.shape[1], k.shape[2]
+        qs, ks, vs = q.stride()[:3], k.stride()[:3], v.stride()[:3]
+        max_q = max_k = 0
+        lse_shape = q.shape[:3]
+    out, lse = _outputs(q, out, lse, return_lse, lse_shape)
+    os = (0, out.stride(1), out.stride(0)) if packed else out.stride()[:3]
+    head = (dt, d, Hq, Hkv, B, n_sink, min(window, 2**31 - 1), max_q, max_k, _scale(scale), N, M, q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), *qs, *ks, *vs, *os,
+            _ints(q_starts, B + 1, q, "q_starts"), _ints(k_starts, B + 1, q, "k_starts"),
+            _ints(q_lens, B, q, "q_lens"), _ints(kv_lens, B, q, "kv_lens"))
+    err = _error_word(error_word, q)
+    need = _need("kvevict_window_attention_workspace_bytes", _ATTN.pack(*head, 0, 0, err))
+    workspace, wp, wn = _workspace(workspace, need, q)
+    args = _ATTN.pack(*head, wp, wn, err)
+    check(_on(q, lambda st: lib().kvevict_window_attention(args, st)), "kvevict_window_attention")
+    return out if lse is None else (out, lse)
+
+
+def shared_prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, k: torch.Tensor,
+                            v: torch.Tensor, kv_lens: torch.Tensor | None = None, *, scale: float | None = None,
+                            out: torch.Tensor | None = None, lse: torch.Tensor | None = None, return_lse: bool = False,
+                            workspace: torch.Tensor | None = None, error_word: torch.Tensor | None = None):
+    """One token of every sequence, q [B][Hq][d], over a prefix that all share,
+    k_prefix and v_prefix [Hkv][P][d], and a suffix of its own, k and v
+    [B][Hkv][M][d], of kv_lens rows (int32 [B] on the device; None: M). The
+    prefix is read once for the batch. P and M may be 0. Returns out (as q), or
+    (out, lse [B][Hq])."""
+    dt = _dtype(q, "q")
+    _like(q, q, 3, "q")
+    _like(k_prefix, q, 3, "k_prefix")
+    _like(v_prefix, q, 3, "v_prefix", k_prefix.shape)
+    _like(k, q, 4, "k")
+    _like(v, q, 4, "v", k.shape)
+    B, Hq, d = q.shape
+    Hkv, M = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != d or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != d:
+        raise ValueError(f"k, k_prefix: need [{B}][Hkv][M][{d}] and [Hkv][P][{d}], got {tuple(k.shape)} and {tuple(k_prefix.shape)}")
+    out, lse = _outputs(q, out, lse, return_lse, q.shape[:2])
+    head = (dt, d, Hq, Hkv, B, 0, 0, 0, 0, _scale(scale), 1, M, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+            0 if lse is None else lse.data_ptr(), q.stride(0), q.stride(1), 0, *k.stride()[:3], *v.stride()[:3],
+            out.stride(0), out.stride(1), 0, 0, 0, 0, _ints(kv_lens, B, q, "kv_lens"))
+    tail = (_error_word(error_word, q), k_prefix.data_ptr(), v_prefix.data_ptr(), *k_prefix.stride()[:2],
+            *v_prefix.stride()[:2], k_prefix.shape[1])
+    need = _need("kvevict_shared_prefix_attention_workspace_bytes", _SHARED.pack(*head, 0, 0, *tail))
+    workspace, wp, wn = _workspace(workspace, need, q)
+    args = _SHARED.pack(*head, wp, wn, *tail)
+    check(_on(q, lambda st: lib().kvevict_shared_prefix_attention(args, st)), "kvevict_shared_prefix_attention")
+    return out if lse is None else (out, lse)
+
+
+def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       original_context: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                       device=None) -> tuple[torch.Tensor, float]:
+    """The angles per position of a head's pairs, fp64 [rotary_dim / 2], and the
+    factor on cosines and sines, for rotary(). inv_freq_i = base^(-2 i /
+    rotary_dim), changed for longer contexts by `scaling`:
+    "linear": every frequency / factor (positions interpolated);
+    "ntk": base * factor^(rotary_dim / (rotary_dim - 2)), which slows the
+    slowest pair by `factor` and leaves the fastest;
+    "yarn": pairs that turn more than beta_fast times over original_context
+    positions stay, those that turn less than beta_slow times are slowed by
+    `factor`, a linear ramp over the pair index between; the factor on the
+    result is 0.1 ln(factor) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim: need an even number of at least 2")
+    if not (base > 1 and factor >= 1):
+        raise ValueError("base: above 1; factor: at least 1")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "ntk":
+        if rotary_dim == 2:
+            raise ValueError("ntk: needs a rotary_dim above 2")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = base ** (-2.0 * i / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        def pair_of(turns):
+            return rotary_dim * math.log(original_context / (turns * 2 * math.pi)) / (2 * math.log(base))
+        low, high = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), rotary_dim - 1)
+        slow = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+        f = f / factor * slow + f * (1 - slow)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"scaling: None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    return f.to(device if device is not None else "cuda"), scale
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.Tensor, *, interleaved: bool = False,
+           scale: float = 1.0, inverse: bool = False, q_out: torch.Tensor | None = None,
+           k_out: torch.Tensor | None = None):
+    """Rotary positions of queries and keys in one launch: the first
+    2 * len(inv_freq) elements of every head turn by positions * inv_freq,
+    pairs (i, i + half) or, interleaved, (2 i, 2 i + 1); the rest is copied.
+
+    q [T][Hq][d] with positions [T], or q [B][Hq][N][d] with positions [B][N]
+    (or [N], the same for every sequence); k alike with its own heads, or None.
+    positions: an int32 or int64 tensor on the device, or an int, the first
+    token's position. inv_freq: fp64 on the device (rotary_frequencies).
+    q_out / k_out may be q / k: in place. inverse: by the negative angle, the
+    gradient of the forward call. Returns (q_out, k_out), or q_out without k."""
+    dt = _dtype(q, "q")
+    dims = q.dim()
+    if dims not in (3, 4):
+        raise ValueError(f"q: need [T][H][d] or [B][H][N][d], got {tuple(q.shape)}")
+    _like(q, q, dims, "q")
+    d = q.shape[-1]
+    if dims == 3:
+        B, N, Hq = 1, q.shape[0], q.shape[1]
+    else:
+        B, Hq, N = q.shape[:3]
+
+    def st(t):
+        return (0, t.stride(1), t.stride(0)) if dims == 3 else t.stride()[:3]
+
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _like(q_out, q, dims, "q_out", q.shape)
+    if k is not None:
+        _like(k, q, dims, "k")
+        Hk = k.shape[1]
+        if k.shape[-1] != d or k.shape[0] != q.shape[0] or (dims == 4 and k.shape[2] != N):
+            raise ValueError(f"k: {tuple(k.shape)} does not go with q {tuple(q.shape)}")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        else:
+            _like(k_out, q, dims, "k_out", k.shape)
+        kp, kop, kst, kost = k.data_ptr(), k_out.data_ptr(), st(k), st(k_out)
+    else:
+        Hk, kp, kop, kst, kost = 0, 0, 0, (0, 0, 0), (0, 0, 0)
+    if inv_freq.dtype != torch.float64 or inv_freq.device != q.device or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq: need a contiguous float64 vector on {q.device}")
+    if isinstance(positions, int):
+        pp, p64, ps, start = 0, 0, (0, 0), positions
+    else:
+        if positions.device != q.device or positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"positions: need int32 or int64 on {q.device}, got {positions.dtype} on {positions.device}")
+        if positions.shape == (N,):
+            ps = (0, positions.stride(0))
+        elif dims == 4 and positions.shape == (B, N):
+            ps = positions.stride()
+        else:
+            raise ValueError(f"positions: {tuple(positions.shape)} does not go with q {tuple(q.shape)}")
+        pp, p64, start = positions.data_ptr(), int(positions.dtype == torch.int64), 0
+    args = _ROT.pack(dt, d, 2 * inv_freq.shape[0], int(interleaved), int(inverse), p64, Hq, Hk, B, N, q.data_ptr(), kp,
+                     q_out.data_ptr(), kop, *st(q), *st(q_out), *kst, *kost, pp, *ps, start, inv_freq.data_ptr(), scale)
+    check(_on(q, lambda stream: lib().kvevict_rotary(args, stream)), "kvevict_rotary")
+    return q_out if k is None else (q_out, k_out)
