@@ -1,7 +1,11 @@
 // api_ops.cu -- host side of the attention operators (include/kvevict_ops.h):
 // argument checks, how the work is cut into items, and the launches.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "kvevict_ops.h"
 #include "window_attn.h"
@@ -65,6 +69,7 @@ void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int64_t max_k, int6
     p.q_tiles = (p.max_q + per - 1) / per;
     const int64_t items = static_cast<int64_t>(p.batch) * Hkv * p.q_tiles;
     p.splits = 1;
+    p.pair = 0;
     if (may_split && items + other_items < 2 * kSMs) {
         const int64_t tiles = key_tiles(max_k, p.n_sink, p.causal ? p.window : 0, std::min(per, p.max_q), keys);
         const int64_t want = (4 * kSMs + items - 1) / std::max<int64_t>(1, items);
@@ -73,14 +78,31 @@ void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int64_t max_k, int6
 }
 
 struct Plan {
-    AttnParams p{};
-    bool few = false;
+    AttnTcParams tc{};
+    AttnParams &p = tc.a;
+    bool tensor = false;  // bf16: the tensor-core kernel
+    bool few = false;     // fp32: tiles of 16 rows
     int64_t items = 0;
     size_t bytes = 0;  // workspace
 };
 
-// rows a tile holds: 16 where a unit has no more, else 64
-bool few_rows(int G, int64_t max_q) { return G * max_q <= kAttnF32FewRows; }
+// fp32: tiles of 16 rows where every unit has that few, else of 64.
+bool few_rows(int G, int64_t max_q) { return G <= kAttnF32FewRows && G * max_q <= kAttnF32FewRows; }
+
+// Cuts a problem for the kernel of the plan's type. The tensor cores take two
+// tiles of 128 rows an item, or one (with alternate key tiles) where the rows
+// fit one: then only parts of two key tiles or more make sense.
+void cut_for(Plan &w, AttnProblem &q, int64_t max_k)
+{
+    const int G = w.p.G;
+    if (w.tensor) {
+        const bool pair = q.max_q <= kAttnTcRows / G;
+        cut(q, G, w.p.Hkv, (pair ? 1 : 2) * (kAttnTcRows / G) * G, kAttnTcKeys, max_k, 0, true);
+        q.pair = pair;
+    } else {
+        cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows, kAttnF32Keys, max_k, 0, true);
+    }
+}
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -129,8 +151,9 @@ int plan_window(const kvevict_attention_args *a, Plan &w)
     } else {
         q.rs[0] = p.Hq * N; q.rs[1] = N; q.rs[2] = 1;
     }
-    w.few = p.G <= kAttnF32FewRows && few_rows(p.G, q.max_q);
-    cut(q, p.G, p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows, kAttnF32Keys, max_k, 0, true);
+    w.tensor = a->dtype == KVEVICT_BF16;
+    w.few = few_rows(p.G, q.max_q);
+    cut_for(w, q, max_k);
     return finish(w, a->head_dim);
 }
 
@@ -155,10 +178,10 @@ int plan_shared(const kvevict_shared_prefix_args *s, Plan &w)
     y.q_rows = y.max_q = 1;
     y.k_rows = static_cast<int>(a->k_rows);
     y.rs[0] = p.Hq; y.rs[1] = 1; y.rs[2] = 0;
-    w.few = p.G <= kAttnF32FewRows && few_rows(p.G, a->batch);
-    const int rows = w.few ? kAttnF32FewRows : kAttnF32Rows;
-    cut(x, p.G, p.Hkv, rows, kAttnF32Keys, x.k_rows, 0, true);
-    cut(y, p.G, p.Hkv, rows, kAttnF32Keys, y.k_rows, 0, true);
+    w.tensor = a->dtype == KVEVICT_BF16;
+    w.few = few_rows(p.G, a->batch);
+    cut_for(w, x, x.k_rows);
+    cut_for(w, y, y.k_rows);
     return finish(w, a->head_dim);
 }
 
@@ -178,6 +201,54 @@ int check_tensors(const kvevict_attention_args *a, bool needs_k)
     return KVEVICT_OK;
 }
 
+// Encodes a bf16 tensor map of `rank` axes, the first (head_dim) contiguous.
+// strides: in elements, of axes 1.. ; an axis of one entry takes any valid stride.
+int encode_map(AttnTmap *out, const void *base, int rank, const uint64_t *dims, const long long *strides, const uint32_t *box)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn) : nullptr;
+    }();
+    if (!encode) return KVEVICT_ERR_CUDA;
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i) s[i - 1] = static_cast<cuuint64_t>(dims[i] > 1 ? strides[i - 1] : static_cast<long long>(dims[0])) * 2;
+    }
+    static_assert(sizeof(CUtensorMap) == sizeof(AttnTmap), "tensor map size");
+    CUtensorMap m;
+    if (encode(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, b, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return KVEVICT_ERR_INVALID_ARG;
+    std::memcpy(out, &m, sizeof m);
+    return KVEVICT_OK;
+}
+
+int make_maps(AttnTcMaps &t, const AttnProblem &p, int G, int Hkv, int head_dim)
+{
+    const uint64_t D = static_cast<uint64_t>(head_dim);
+    const uint64_t qseq = p.q_starts ? 1 : p.batch, kseq = p.k_starts ? 1 : p.batch;
+    const uint64_t qd[5] = {D, static_cast<uint64_t>(G), static_cast<uint64_t>(p.q_rows), static_cast<uint64_t>(Hkv), qseq};
+    const long long qs[4] = {p.qs[1], p.qs[2], G * p.qs[1], p.qs[0]};
+    const uint32_t qb[5] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(kAttnTcRows / G), 1, 1};
+    int rc = encode_map(&t.q, p.q, 5, qd, qs, qb);
+    // without keys nothing is loaded: any address does
+    const uint64_t kd[4] = {D, static_cast<uint64_t>(std::max(p.k_rows, 1)), static_cast<uint64_t>(Hkv), kseq};
+    const long long ks[3] = {p.ks[2], p.ks[1], p.ks[0]}, vs[3] = {p.vs[2], p.vs[1], p.vs[0]};
+    const long long any[3] = {head_dim, head_dim, head_dim};
+    const uint32_t kb[4] = {64, kAttnTcKeys, 1, 1};
+    const bool none = p.k_rows == 0;
+    if (!rc) rc = encode_map(&t.k, none ? p.q : p.k, 4, kd, none ? any : ks, kb);
+    if (!rc) rc = encode_map(&t.v, none ? p.q : p.v, 4, kd, none ? any : vs, kb);
+    return rc;
+}
+
 int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
 {
     AttnParams &p = w.p;
@@ -193,7 +264,16 @@ int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
     p.lse = a->lse;
     p.err = a->error_word;
     const bool bf16 = a->dtype == KVEVICT_BF16;
-    cudaError_t e = launch_attn_f32(p, a->head_dim, bf16, w.few, st);
+    cudaError_t e;
+    if (w.tensor) {
+        for (int i = 0; i < p.n_problems; ++i) {
+            const int rc = make_maps(w.tc.maps[i], p.pr[i], p.G, p.Hkv, a->head_dim);
+            if (rc) return rc;
+        }
+        e = launch_attn_tc(w.tc, a->head_dim, kSMs, st);
+    } else {
+        e = launch_attn_f32(p, a->head_dim, w.few, st);
+    }
     if (e == cudaSuccess && p.slots > 1) e = launch_attn_join(p, a->head_dim, bf16, st);
     return e == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
 }

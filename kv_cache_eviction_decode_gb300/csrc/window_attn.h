@@ -25,6 +25,7 @@ struct AttnProblem {
     int batch, causal, n_sink, window;  // window 0: none
     int q_tiles, splits, slot0;         // slot0: the first part's slot
     int n_items;
+    int pair;                           // tensor cores: the rows fit one tile, two tiles share the keys
 };
 
 struct AttnParams {
@@ -43,8 +44,26 @@ struct AttnParams {
 
 constexpr int kAttnF32Rows = 64, kAttnF32FewRows = 16, kAttnF32Keys = 64;
 
+// Tensor maps of one problem: q as (d, group head, token, KV head, sequence),
+// boxes of 64 x G x (128 / G) tokens; k and v as (d, key, KV head, sequence),
+// boxes of 64 x 128 keys; 128-byte swizzle.
+struct alignas(64) AttnTmap {
+    uint64_t word[16];
+};
+struct AttnTcMaps {
+    AttnTmap q, k, v;
+};
+struct AttnTcParams {
+    AttnTcMaps maps[2];
+    AttnParams a;
+};
+
+constexpr int kAttnTcRows = 128, kAttnTcKeys = 128;
+
+// bf16 attention on the tensor cores, at most one CTA on each of `sms` SMs.
+cudaError_t launch_attn_tc(const AttnTcParams &p, int head_dim, int sms, cudaStream_t st);
 // fp32 attention on the CUDA cores; `few`: tiles of 16 rows, else 64.
-cudaError_t launch_attn_f32(const AttnParams &p, int head_dim, bool bf16, bool few, cudaStream_t st);
+cudaError_t launch_attn_f32(const AttnParams &p, int head_dim, bool few, cudaStream_t st);
 // Joins the slots: out = sum_s 2^(l_s - l) o_s, l = log2 sum_s 2^(l_s).
 cudaError_t launch_attn_join(const AttnParams &p, int head_dim, bool bf16, cudaStream_t st);
 

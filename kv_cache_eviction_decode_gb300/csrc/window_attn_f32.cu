@@ -31,18 +31,8 @@ template <int D, int R> struct F32Layout {
     static constexpr int kBytes = kFloats * 4;
 };
 
-template <typename T> __device__ __forceinline__ float4 load4(const T *p)
-{
-    float v[4];
-    load_f32<T, 4>(p, v);
-    return make_float4(v[0], v[1], v[2], v[3]);
-}
-
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
-{
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
 
 __device__ __forceinline__ float half_max(float v)
 {
@@ -58,7 +48,7 @@ __device__ __forceinline__ float half_sum(float v)
     return v;
 }
 
-template <typename T, int D, int R>
+template <int D, int R>
 __global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_constant__ AttnParams ap)
 {
     using L = F32Layout<D, R>;
@@ -88,17 +78,17 @@ __global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_c
     const int i_hi = static_cast<int>(static_cast<long long>(keys.count) * (part + 1) / p.splits);
 
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const T *qb = static_cast<const T *>(p.q) + (p.q_starts ? 0 : b * p.qs[0]) +
+    const float *qb = static_cast<const float *>(p.q) + (p.q_starts ? 0 : b * p.qs[0]) +
                   static_cast<long long>(kvh) * G * p.qs[1] + static_cast<long long>(sq.q0 + t0) * p.qs[2];
-    const T *kb = static_cast<const T *>(p.k) + (p.k_starts ? 0 : b * p.ks[0]) + kvh * p.ks[1] + sq.k0 * p.ks[2];
-    const T *vb = static_cast<const T *>(p.v) + (p.k_starts ? 0 : b * p.vs[0]) + kvh * p.vs[1] + sq.k0 * p.vs[2];
+    const float *kb = static_cast<const float *>(p.k) + (p.k_starts ? 0 : b * p.ks[0]) + kvh * p.ks[1] + sq.k0 * p.ks[2];
+    const float *vb = static_cast<const float *>(p.v) + (p.k_starts ? 0 : b * p.vs[0]) + kvh * p.vs[1] + sq.k0 * p.vs[2];
 
     for (int e = tid; e < R * (D / 4); e += kThreadsF32) {
         const int r = e / (D / 4), c = (e - r * (D / 4)) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < nrows) {
             const int t = r / G, g = r - t * G;
-            v = load4<T>(qb + g * p.qs[1] + t * p.qs[2] + c);
+            v = load4(qb + g * p.qs[1] + t * p.qs[2] + c);
             v.x *= ap.scale_log2; v.y *= ap.scale_log2; v.z *= ap.scale_log2; v.w *= ap.scale_log2;
         }
         *reinterpret_cast<float4 *>(sQ + r * L::kQ + c) = v;
@@ -122,13 +112,13 @@ __global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_c
         for (int c = 0; c < CV; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 
-    auto load_tile = [&](const T *base, long long stride, int j0) {
+    auto load_tile = [&](const float *base, long long stride, int j0) {
         for (int e = tid; e < kBK * (D / 4); e += kThreadsF32) {
             const int r = e / (D / 4), c = (e - r * (D / 4)) * 4;
             const int j = j0 + r;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             // only keys that a row of this tile sees are read
-            if (j < keys.sink || (j >= keys.lo && j < keys.hi)) v = load4<T>(base + j * stride + c);
+            if (j < keys.sink || (j >= keys.lo && j < keys.hi)) v = load4(base + j * stride + c);
             *reinterpret_cast<float4 *>(sK + r * L::kQ + c) = v;
         }
     };
@@ -228,7 +218,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_c
                 store4(po + tx * 4 + c * 64, make_float4(o[a][c].x * inv, o[a][c].y * inv, o[a][c].z * inv, o[a][c].w * inv));
             if (tx == 0) ap.part_l[at] = lse2;
         } else {
-            T *po = static_cast<T *>(ap.out) + b * p.os[0] + h * p.os[1] + t * p.os[2];
+            float *po = static_cast<float *>(ap.out) + b * p.os[0] + h * p.os[1] + t * p.os[2];
 #pragma unroll
             for (int c = 0; c < CV; ++c)
                 store4(po + tx * 4 + c * 64, make_float4(o[a][c].x * inv, o[a][c].y * inv, o[a][c].z * inv, o[a][c].w * inv));
@@ -281,9 +271,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     }
 }
 
-template <typename T, int D, int R> cudaError_t launch_f32(const AttnParams &p, cudaStream_t st)
+template <int D, int R> cudaError_t launch_f32(const AttnParams &p, cudaStream_t st)
 {
-    auto kern = attn_f32_kernel<T, D, R>;
+    auto kern = attn_f32_kernel<D, R>;
     constexpr int bytes = F32Layout<D, R>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
@@ -302,14 +292,10 @@ template <typename T, int D> cudaError_t launch_join(const AttnParams &p, cudaSt
 
 }  // namespace
 
-cudaError_t launch_attn_f32(const AttnParams &p, int head_dim, bool bf16, bool few, cudaStream_t st)
+cudaError_t launch_attn_f32(const AttnParams &p, int head_dim, bool few, cudaStream_t st)
 {
-    if (bf16) {
-        if (head_dim == 64) return few ? launch_f32<__nv_bfloat16, 64, 16>(p, st) : launch_f32<__nv_bfloat16, 64, 64>(p, st);
-        return few ? launch_f32<__nv_bfloat16, 128, 16>(p, st) : launch_f32<__nv_bfloat16, 128, 64>(p, st);
-    }
-    if (head_dim == 64) return few ? launch_f32<float, 64, 16>(p, st) : launch_f32<float, 64, 64>(p, st);
-    return few ? launch_f32<float, 128, 16>(p, st) : launch_f32<float, 128, 64>(p, st);
+    if (head_dim == 64) return few ? launch_f32<64, 16>(p, st) : launch_f32<64, 64>(p, st);
+    return few ? launch_f32<128, 16>(p, st) : launch_f32<128, 64>(p, st);
 }
 
 cudaError_t launch_attn_join(const AttnParams &p, int head_dim, bool bf16, cudaStream_t st)
