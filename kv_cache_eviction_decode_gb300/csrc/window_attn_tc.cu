@@ -35,9 +35,9 @@ constexpr int kSubThreads = 128;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kSchedWarp = 10;
 constexpr int kTcThreads = 384;       // warp 11 only completes the third warpgroup, for the register split
 // Registers a thread: the launch's 168 (65,536 over 384 threads), of which the
-// third warpgroup gives up 112 to the softmax warpgroups, whose threads hold a
-// whole row of 128 logits: 2 x 224 + 56 = 3 x 168.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 224, kIssueRegs = 56;
+// third warpgroup gives up 80 to the softmax warpgroups, whose threads hold a
+// whole row of 128 logits: 2 x 208 + 88 = 3 x 168.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kIssueRegs = 88;
 static_assert(2 * kSoftmaxRegs + kIssueRegs <= 3 * kLaunchRegs, "register split");
 constexpr uint32_t kTcTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * sub
@@ -110,6 +110,13 @@ __device__ __forceinline__ void tc_mma_ts_bf16(uint32_t d_tmem, uint32_t a_tmem,
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
+}
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Shared-memory descriptor of a V tile as the B operand with N (head_dim)
@@ -218,11 +225,11 @@ __device__ __forceinline__ bool tc_active(const TcItem &it, int n, int s)
     return t < it.sub[s].tiles_sink || (t >= it.sub[s].main0 && t < it.sub[s].end);
 }
 
-// Keys of tile n to work on, a multiple of 16: the others are seen by no row.
-__device__ __forceinline__ int tc_keys_of(const TcItem &it, int n)
+// Keys of a tile to work on, a multiple of 16: the others are seen by no row.
+__device__ __forceinline__ int tc_keys_in(const AttnKeys &keys, bool sink_tile, int tile)
 {
-    const int j0 = attn_tile_at(it.keys, n) * kBN;
-    const int last = n < it.keys.sink_tiles && j0 + kBN <= it.keys.lo ? min(it.keys.sink, it.keys.hi) : it.keys.hi;
+    const int j0 = tile * kBN;
+    const int last = sink_tile && j0 + kBN <= keys.lo ? min(keys.sink, keys.hi) : keys.hi;
     return min(kBN, (last - j0 + 15) & ~15);
 }
 
@@ -307,11 +314,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     uint64_t *fin = i_empty + kItemSlots;       // the MMA warp's last operation completed
     uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 1);
     TcItem *items = reinterpret_cast<TcItem *>(sm + L::kOffItem);
-    int *left = reinterpret_cast<int *>(sm + L::kOffItem + 240);  // [2] MMA issuer: tiles of the item left per sub
     float *xl = reinterpret_cast<float *>(sm + L::kOffX);
     static_assert((10 + 2 * L::kStages + 2 * kItemSlots + 1) * 8 + 4 <= 256, "barrier area");
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp-uniform to the compiler
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1);
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tslot);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(tslot), 0);
     static_assert(kItemSlots * sizeof(TcItem) <= 240, "item area");
     const int n_items = ap.pr[0].n_items + (ap.n_problems > 1 ? ap.pr[1].n_items : 0);
 
@@ -428,100 +435,130 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
         } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t idesc_pv = idesc_bf16_f32(kBM, D) | (1u << 16);  // B with N contiguous
-                bool ok = true;
-                int ld = 0;              // ring loads of the items before this one
-                uint32_t nq = 0, np = 0; // bit s: parity of the rows' tiles and of the probabilities taken
-                // per sub: the pending P V's ring load (-1: none), its keys, and whether it starts the sum
-                int pv0 = -1, pv1 = -1, pk0 = 0, pk1 = 0;
-                uint32_t fresh = 0;      // bit s: no tile of this item yet; pf: the pending one starts the sum
-                uint32_t pf = 0;
-                // Tile n of the item: first the subs that see it (the pending P V of each, then its Q K^T:
-                // S is overwritten behind the P V that read P from it, in issue order), then the pending
-                // P V of those that do not. n = -1: only what is pending, at the end.
-                auto step = [&](const TcItem *it, int n) {
-                    int kl = 0, st = 0, keys = 0;
-                    if (n >= 0) {
-                        kl = ld + 2 * (n - it->lo);
-                        st = kl % L::kStages;
-                        keys = tc_keys_of(*it, n);
-                        if (!mbar_wait(&kv_full[st], (kl / L::kStages) & 1)) return false;
+            // The whole warp walks the items with warp-uniform values (the instruction takes its
+            // descriptors from uniform registers; issued from one lane of divergent code, each MMA
+            // cost about 90 cycles of moves); one elected lane issues.
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(kBM, D) | (1u << 16);  // B with N contiguous
+            const bool leader = elect_one();
+            bool ok = true;
+            const uint32_t q_addr = smem_u32(sm + L::kOffQ), kv_addr = smem_u32(sm + L::kOffKV);
+            uint32_t st = 0, ph = 0;     // ring stage of the next K tile, and its phase's parity
+            uint32_t nq = 0, np = 0;     // bit s: parity of the rows' tiles and of the probabilities taken
+            // per sub: the pending P V's ring stage (-1: none) with its phase, and its 16-key steps
+            int pv[2] = {-1, -1};
+            uint32_t vph[2] = {0, 0};
+            int psteps[2] = {0, 0};
+            bool pfirst[2] = {false, false};
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+            auto issue_pv = [&](int s) {
+                const int v = pv[s];
+                if (!wait(&p_full[s], (np >> s) & 1) || !wait(&kv_full[v], vph[s])) return false;
+                np ^= 1u << s;
+                tc_fence_after();
+                const uint64_t vd = smem_desc_v(kv_addr + v * L::kTile);
+                const uint32_t d = tmem + kColO + 128u * s, a = tmem + kColS + 128u * s;
+                const bool last_use = pv[1 - s] != v;  // the other sub has no use of this V (any more)
+                if (leader) {
+                    if (psteps[s] == kBN / 16) {
+#pragma unroll
+                        for (int kk = 0; kk < kBN / 16; ++kk)
+                            tc_mma_ts_bf16(d, a + 8u * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || !pfirst[s]);
+                    } else {
+                        for (int kk = 0; kk < psteps[s]; ++kk)
+                            tc_mma_ts_bf16(d, a + 8u * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || !pfirst[s]);
                     }
+                    tc_commit(&o_done[s]);
+                    if (last_use) tc_commit(&kv_empty[v]);
+                }
+                __syncwarp();
+                pv[s] = -1;
+                return true;
+            };
+            for (int i = 0;; ++i) {
+                const TcItem *ip = take(i, ok);
+                if (!__all_sync(0xffffffffu, ip != nullptr)) break;
+                // the fields a step needs, in registers
+                auto get = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+                const int lo = get(ip->lo), hi = get(ip->hi), pair = get(ip->pair);
+                const AttnKeys keys = {get(ip->keys.sink), get(ip->keys.lo), get(ip->keys.hi), get(ip->keys.sink_tiles), get(ip->keys.main0), 0};
+                int left[2], sink[2], main0[2], end[2];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    left[s] = get(ip->sub[s].count);
+                    sink[s] = get(ip->sub[s].tiles_sink);
+                    main0[s] = get(ip->sub[s].main0);
+                    end[s] = get(ip->sub[s].end);
+                }
+                __syncwarp();
+                if (leader) mbar_arrive(&i_empty[i % kItemSlots]);
+                bool first[2] = {true, true};
 #pragma unroll 1
-                    for (int q = n >= 0 ? 0 : 2; q < 4; ++q) {
-                        const int s = q & 1;
-                        const bool act = n >= 0 && tc_active(*it, n, s);
-                        if (q == 2 && n >= 0) tc_commit(&kv_empty[st]);  // K of this tile has been used
-                        if (act != (q < 2)) continue;
-                        const int v = s ? pv1 : pv0;
-                        if (v >= 0) {
-                            const int vst = v % L::kStages;
-                            if (!mbar_wait(&p_full[s], (np >> s) & 1) || !mbar_wait(&kv_full[vst], (v / L::kStages) & 1)) return false;
-                            np ^= 1u << s;
-                            tc_fence_after();
-                            uint64_t vd = smem_desc_v(smem_u32(sm + L::kOffKV + vst * L::kTile));
-                            const uint32_t d = tmem + kColO + 128u * s, a = tmem + kColS + 128u * s;
-                            const int steps = (s ? pk1 : pk0) / 16;
-                            bool add = !((pf >> s) & 1);
-#pragma unroll 1
-                            for (int kk = 0; kk < steps; ++kk, vd += 2048 >> 4) {
-                                tc_mma_ts_bf16(d, a + 8u * kk, vd, idesc_pv, add);
-                                add = true;
-                            }
-                            tc_commit(&o_done[s]);
-                            if ((s ? pv0 : pv1) != v) tc_commit(&kv_empty[vst]);  // the other sub has no use of it (any more)
-                            if (s) pv1 = -1;
-                            else pv0 = -1;
-                        }
-                        if (!act) continue;
-                        if ((fresh >> s) & 1) {
-                            if (!mbar_wait(&q_full[s], (nq >> s) & 1)) return false;
+                for (int n = lo; n < hi && ok; ++n) {
+                    const int t = n < keys.sink_tiles ? n : keys.main0 + n - keys.sink_tiles;
+                    const int nk = tc_keys_in(keys, n < keys.sink_tiles, t);
+                    bool act[2];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        act[s] = pair ? ((n - lo) & 1) == s : t < sink[s] || (t >= main0[s] && t < end[s]);
+                    const uint32_t vs = st + 1 == L::kStages ? 0 : st + 1;  // V follows K in the ring
+                    const uint32_t vp = st + 1 == L::kStages ? ph ^ 1 : ph;
+                    ok = wait(&kv_full[st], ph);
+                    // first the subs that see the tile: the pending P V of each, then its Q K^T (S is
+                    // overwritten behind the P V that reads P from it, in issue order)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (!ok || !act[s]) continue;
+                        if (pv[s] >= 0) ok = issue_pv(s);
+                        if (ok && first[s]) {
+                            ok = wait(&q_full[s], (nq >> s) & 1);
                             nq ^= 1u << s;
                         }
+                        if (!ok) continue;
                         tc_fence_after();
-                        const uint32_t idesc = idesc_bf16_f32(kBM, keys);
-                        const uint64_t qd = smem_desc_sw128(smem_u32(sm + L::kOffQ + s * L::kTile));
-                        const uint64_t kd = smem_desc_sw128(smem_u32(sm + L::kOffKV + st * L::kTile));
+                        const uint32_t idesc = idesc_bf16_f32(kBM, nk);
+                        const uint64_t qd = smem_desc_sw128(q_addr + s * L::kTile), kd = smem_desc_sw128(kv_addr + st * L::kTile);
+                        --left[s];
+                        if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t koff = static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                            tc_mma_bf16(tmem + kColS + 128u * s, qd + koff, kd + koff, idesc, kk > 0);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t koff = static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                                tc_mma_bf16(tmem + kColS + 128u * s, qd + koff, kd + koff, idesc, kk > 0);
+                            }
+                            tc_commit(&s_full[s]);
+                            if (left[s] == 0) tc_commit(&q_empty[s]);
                         }
-                        tc_commit(&s_full[s]);
-                        if (s) {
-                            pv1 = kl + 1;
-                            pk1 = keys;
-                        } else {
-                            pv0 = kl + 1;
-                            pk0 = keys;
-                        }
-                        pf = (pf & ~(1u << s)) | (fresh & (1u << s));
-                        fresh &= ~(1u << s);
-                        if (--left[s] == 0) tc_commit(&q_empty[s]);
+                        __syncwarp();
+                        pv[s] = static_cast<int>(vs);
+                        vph[s] = vp;
+                        psteps[s] = nk / 16;
+                        pfirst[s] = first[s];
+                        first[s] = false;
                     }
-                    return true;
-                };
-                for (int i = 0;; ++i) {
-                    const TcItem *it = take(i, ok);
-                    if (!it) break;
-                    fresh = 3u;
-                    left[0] = it->sub[0].count;
-                    left[1] = it->sub[1].count;
-#pragma unroll 1
-                    for (int n = it->lo; n < it->hi && ok; ++n) ok = step(it, n);
-                    // an item without tiles pushes nothing out: what is pending goes now, or the softmax
-                    // warps, and behind them the scheduler, would wait for it
-                    if (ok && it->lo == it->hi) ok = step(nullptr, -1);
-                    if (!ok) break;
-                    ld += 2 * (it->hi - it->lo);
-                    mbar_arrive(&i_empty[i % kItemSlots]);
+                    if (ok && leader) tc_commit(&kv_empty[st]);  // K of this tile has been used
+                    __syncwarp();
+                    // then the pending P V of those that do not see it
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        if (ok && !act[s] && pv[s] >= 0) ok = issue_pv(s);
+                    st = vs + 1 == L::kStages ? 0 : vs + 1;
+                    ph = vs + 1 == L::kStages ? vp ^ 1 : vp;
                 }
-                if (ok) ok = step(nullptr, -1);
+                // an item without tiles pushes nothing out: what is pending goes now, or the softmax
+                // warps, and behind them the scheduler, would wait for it
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (ok && lo == hi && pv[s] >= 0) ok = issue_pv(s);
+                if (!ok) break;
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (ok && pv[s] >= 0) ok = issue_pv(s);
+            if (leader) {
                 if (!ok) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
                 tc_commit(fin);
                 mbar_wait(fin, 0);
             }
+            __syncwarp();
         }
     } else {
         // ------------------------------------------------ softmax and output
@@ -567,7 +604,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 }
                 tc_fence_after();
                 const int j0 = attn_tile_at(it.keys, n) * kBN;
-                const int keys = tc_keys_of(it, n);
+                const int keys = tc_keys_in(it.keys, n < it.keys.sink_tiles, j0 / kBN);
                 if (ok && live) {
                     const bool masked = j0 + kBN - 1 > top_min || (j0 < low_max && j0 + kBN > p.n_sink);
                     uint32_t r[4][32];
