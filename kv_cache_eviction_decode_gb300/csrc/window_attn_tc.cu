@@ -11,15 +11,16 @@
 //
 // A persistent CTA per SM walks items (window_attn.h). It holds two row tiles
 // of 128 rows ("subs"), each with its own S/P and O in TMEM (S0 S1 O0 O1: 512
-// columns; P overwrites the first half of S) and its own softmax warpgroup, a
-// row a thread: while one sub's rows go through the softmax the tensor cores
+// columns; P overwrites the first half of S) and its own softmax warps, two
+// threads a row: while one sub's rows go through the softmax the tensor cores
 // work for the other. A K or V tile of 128 keys is loaded once for both subs
 // (TMA ring). Where a unit's rows fit one sub ("pair": decoding, short
 // chunks), both hold the same rows and take alternate key tiles; their sums
 // are joined through TMEM at the end of the item. Rows are (token, group
 // head) pairs, so all query heads of a KV head share its tiles.
 //
-// Warps 0-3, 4-7: softmax and output of sub 0, 1; 8: TMA; 9: MMA issue; 10: the items.
+// Warps 0-3, 4-7: softmax and output of sub 0, 1, the first 64 keys of each
+// tile; 8-11, 12-15: the other 64; 16: TMA; 17: MMA issue; 18: the items.
 #include <cmath>
 
 #include "tc5_common.cuh"
@@ -31,14 +32,14 @@ namespace kvevict {
 namespace {
 
 constexpr int kBM = kAttnTcRows, kBN = kAttnTcKeys;
-constexpr int kSubThreads = 128;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kSchedWarp = 10;
-constexpr int kTcThreads = 384;       // warp 11 only completes the third warpgroup, for the register split
-// Registers a thread: the launch's 168 (65,536 over 384 threads), of which the
-// third warpgroup gives up 80 to the softmax warpgroups, whose threads hold a
-// whole row of 128 logits: 2 x 208 + 88 = 3 x 168.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kIssueRegs = 88;
-static_assert(2 * kSoftmaxRegs + kIssueRegs <= 3 * kLaunchRegs, "register split");
+constexpr int kSoftmaxWarps = 8;  // then four output warps
+constexpr int kTmaWarp = 12, kSchedWarp = 13, kMmaWarp = 14;  // and 15
+constexpr int kTcThreads = 512;
+// Registers a thread: the launch's 128 (65,536 over 512 threads), moved to the
+// two softmax warpgroups, whose threads hold a whole row of 128 logits:
+// 2 x 168 + 104 + 72 = 4 x 128.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kOutRegs = 104, kIssueRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOutRegs + kIssueRegs <= 4 * kLaunchRegs, "register split");
 constexpr uint32_t kTcTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * sub
 constexpr float kRescale = 8.f;             // log2 units
@@ -50,9 +51,10 @@ template <int D> struct TcLayout {
     static constexpr int kOffQ = 0;
     static constexpr int kOffKV = 2 * kTile;
     static constexpr int kOffBar = kOffKV + kStages * kTile;
-    static constexpr int kOffX = kOffBar + 256;               // [2][128] log2 normalisers of the subs' rows
-    static constexpr int kOffItem = kOffX + 2 * kBM * 4;      // posted items
-    static constexpr int kBytes = kOffItem + 256 + 1024;  // + slack to align the base to 1 KB
+    static constexpr int kOffX = kOffBar + 384;            // [2 subs][2][128 rows]: log2 normalisers, 1 / l
+    static constexpr int kOffItem = kOffX + 4 * kBM * 4;   // posted items
+    static constexpr int kOffStep = kOffItem + 288;        // the two subs' steps; a cancelled block's index
+    static constexpr int kBytes = kOffStep + 32;
 };
 static_assert(TcLayout<128>::kBytes <= 232448 && TcLayout<64>::kBytes <= 232448, "shared memory");
 
@@ -90,15 +92,28 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
     return d;
 }
 
-// Named barrier over nthreads threads that counts those with a true `pred`.
-__device__ __forceinline__ int named_bar_count(int id, int nthreads, bool pred)
+// Cluster launch control: asks the hardware for one of the grid's blocks that
+// has not started; 16 bytes arrive at `slot`, completing on `bar`.
+__device__ __forceinline__ void steal_request(void *slot, uint64_t *bar)
 {
-    int n;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, %1, %2, p;\n\t}"
-                 : "=r"(n)
-                 : "r"(id), "r"(nthreads), "r"(pred ? 1u : 0u)
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(slot)),
+                 "r"(smem_u32(bar))
                  : "memory");
-    return n;
+}
+
+// The block that was taken over, or -1: none was left.
+__device__ __forceinline__ int steal_result(const void *slot)
+{
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, h;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(slot))
+        : "memory");
+    return got ? static_cast<int>(x) : -1;
 }
 
 // D[tmem] (+)= A[tmem] * B for one K step, A bf16 pairs in TMEM columns.
@@ -133,15 +148,21 @@ __device__ __forceinline__ uint64_t smem_desc_v(uint32_t addr)
     return d;
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -197,13 +218,49 @@ __device__ __forceinline__ void tc_exp32(const uint32_t (&r)[32], float2 c2, flo
     }
 }
 
+// Writes 64 bytes of every lane's row. Lane by lane that would be 32 lines an
+// instruction, 16 bytes of each; the four lanes of a quad exchange their 16-byte
+// pieces (a 4 x 4 transpose in two rounds), so that each store covers 64 bytes
+// of eight rows. dst: the quad's four rows, + the lane's piece; null: no row.
+__device__ __forceinline__ void tc_store_rows(const uint4 (&w)[4], uint4 *const (&dst)[4], int at)
+{
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+    auto swap = [](uint4 &a, uint4 &b, bool up, int mask) {  // a of the upper lane for b of the lower
+        const uint4 out = up ? a : b;
+        uint4 in;
+        in.x = __shfl_xor_sync(0xffffffffu, out.x, mask);
+        in.y = __shfl_xor_sync(0xffffffffu, out.y, mask);
+        in.z = __shfl_xor_sync(0xffffffffu, out.z, mask);
+        in.w = __shfl_xor_sync(0xffffffffu, out.w, mask);
+        if (up) a = in;
+        else b = in;
+    };
+    uint4 a = w[0], b = w[1], c = w[2], d = w[3];
+    swap(a, b, odd, 1);
+    swap(c, d, odd, 1);
+    swap(a, c, high, 2);
+    swap(b, d, high, 2);
+    if (dst[0]) dst[0][at] = a;
+    if (dst[1]) dst[1][at] = b;
+    if (dst[2]) dst[2][at] = c;
+    if (dst[3]) dst[3][at] = d;
+}
+
 // One sub of an item: its tokens, the key tiles they see, how many of them
 // are in this part.
 struct TcSub {
     int t0, nt;
     int tiles_sink, main0, end;
     int count;
+    int top_min, low_max;  // of its rows: the least last key seen, the greatest first one of the window
 };
+
+// What a softmax warp has to know about the tile whose logits are ready.
+struct TcStep {
+    int j0;            // first key
+    int what;          // keys to work on | kStepMask | kStepEdge | V's ring stage << 16 | its parity << 24
+};
+constexpr int kStepMask = 256, kStepEdge = 512;
 
 // An item as the scheduler warp posts it in shared memory.
 struct TcItem {
@@ -272,6 +329,9 @@ __device__ __forceinline__ void tc_make_item(const AttnTcParams &tp, int idx, Tc
         TcSub &u = it.sub[s];
         u.t0 = s ? t1 : t0;
         u.nt = s ? n1 : n0;
+        const int pa = p.causal ? sq.p0 + u.t0 : sq.m - 1, pb = p.causal ? pa + u.nt - 1 : sq.m - 1;
+        u.top_min = pa;
+        u.low_max = p.window > 0 ? max(0, pb - p.window + 1) : 0;
         AttnKeys k = {};
         if (u.nt > 0) k = attn_keys(p, sq.m, sq.p0 + u.t0, sq.p0 + u.t0 + u.nt - 1, kBN);
         u.tiles_sink = k.sink_tiles;
@@ -281,17 +341,11 @@ __device__ __forceinline__ void tc_make_item(const AttnTcParams &tp, int idx, Tc
         if (it.pair) {
             u.count = (it.hi - it.lo + 1 - s) / 2;
         } else {
-            for (int n = it.lo; n < it.hi; ++n) u.count += tc_active(it, n, s) ? 1 : 0;
+            if (p.splits == 1) u.count = k.count;
+            else
+                for (int n = it.lo; n < it.hi; ++n) u.count += tc_active(it, n, s) ? 1 : 0;
         }
     }
-}
-
-// The i-th item of this CTA: the direction alternates, so that with items in
-// the order of their work the CTAs' sums stay close.
-__device__ __forceinline__ int tc_item_index(int i)
-{
-    const int c = blockIdx.x, n = gridDim.x;
-    return i * n + ((i & 1) ? n - 1 - c : c);
 }
 
 template <int D>
@@ -299,8 +353,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 {
     using L = TcLayout<D>;
     const AttnParams &ap = tp.a;
-    extern __shared__ uint8_t traw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(traw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kOffBar);
     uint64_t *q_full = bars;                    // [2] a sub's rows landed
     uint64_t *q_empty = q_full + 2;             // [2] its last Q K^T completed
@@ -309,13 +362,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     uint64_t *o_done = p_full + 2;              // [2] P V completed
     uint64_t *kv_full = o_done + 2;             // [kStages]
     uint64_t *kv_empty = kv_full + L::kStages;  // [kStages]
-    uint64_t *i_full = kv_empty + L::kStages;   // [kItemSlots] an item is posted
+    uint64_t *l_ready = kv_empty + L::kStages;  // [2] a sub's sums of the item are in shared memory
+    uint64_t *o_free = l_ready + 2;             // [2] its O has been read
+    uint64_t *i_full = o_free + 2;              // [kItemSlots] an item is posted
     uint64_t *i_empty = i_full + kItemSlots;    // [kItemSlots] every role is done with it
-    uint64_t *fin = i_empty + kItemSlots;       // the MMA warp's last operation completed
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 1);
+    uint64_t *fin = i_empty + kItemSlots;       // [2] an MMA warp's last operation completed
+    uint64_t *stolen = fin + 2;                 // the answer about another block is there
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(stolen + 1);
     TcItem *items = reinterpret_cast<TcItem *>(sm + L::kOffItem);
+    TcStep *steps = reinterpret_cast<TcStep *>(sm + L::kOffStep);  // [2]
+    uint8_t *steal_slot = sm + L::kOffStep + 16;
     float *xl = reinterpret_cast<float *>(sm + L::kOffX);
-    static_assert((10 + 2 * L::kStages + 2 * kItemSlots + 1) * 8 + 4 <= 256, "barrier area");
+    static_assert((15 + 2 * L::kStages + 2 * kItemSlots + 2) * 8 + 4 <= 384, "barrier area");
+    static_assert(kItemSlots * sizeof(TcItem) <= 288 && L::kOffStep % 16 == 0, "item area");
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp-uniform to the compiler
@@ -323,19 +382,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1);
             mbar_init(&q_empty[s], 1);
-            mbar_init(&s_full[s], 1);
+            mbar_init(&s_full[s], 2);  // the step is posted; its logits are complete
             mbar_init(&p_full[s], 4);
             mbar_init(&o_done[s], 1);
+            mbar_init(&l_ready[s], 4);
+            mbar_init(&o_free[s], 4);
+            mbar_init(&fin[s], 1);
         }
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 1);
+            mbar_init(&kv_empty[s], 2);
         }
         for (int s = 0; s < kItemSlots; ++s) {
             mbar_init(&i_full[s], 1);
-            mbar_init(&i_empty[s], 2 + 8);  // TMA, MMA, the softmax warps
+            mbar_init(&i_empty[s], 3 + kSoftmaxWarps + 4);  // TMA, MMA, softmax, output warps
         }
-        mbar_init(fin, 1);
+        mbar_init(stolen, 1);
         mbar_fence_init();
     }
     if (warp == kTmaWarp) tmem_alloc(tslot, kTcTmemCols);
@@ -343,9 +405,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(tslot), 0);
-    static_assert(kItemSlots * sizeof(TcItem) <= 240, "item area");
-    const int n_items = ap.pr[0].n_items + (ap.n_problems > 1 ? ap.pr[1].n_items : 0);
-
     // The i-th posted item; null where there is none or the wait ran out.
     auto take = [&](int i, bool &ok) -> const TcItem * {
         if (!mbar_wait(&i_full[i % kItemSlots], (i / kItemSlots) & 1)) {
@@ -360,21 +419,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == kSchedWarp) {
             // -------------------------------------------------------- scheduler
+            // The grid has a block for every item, in the order of tc_make_item; a block that runs
+            // takes over one after another of those that have not started.
             if (lane == 0) {
-                for (int i = 0, k = 0;; ++k) {
-                    const bool end = k * static_cast<int>(gridDim.x) >= n_items;
-                    const int idx = tc_item_index(k);
-                    if (!end && idx >= n_items) continue;
+                int idx = blockIdx.x;
+                for (int i = 0;; ++i) {
                     const int slot = i % kItemSlots;
                     if (i >= kItemSlots && !mbar_wait(&i_empty[slot], ((i / kItemSlots) - 1) & 1)) {
                         attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
                         break;
                     }
-                    if (end) items[slot].prob = -1;
+                    if (idx < 0) items[slot].prob = -1;
                     else tc_make_item(tp, idx, items[slot]);
                     mbar_arrive(&i_full[slot]);
-                    if (end) break;
-                    ++i;
+                    if (idx < 0) break;
+                    mbar_arrive_expect_tx(stolen, 16);
+                    steal_request(steal_slot, stolen);
+                    if (!mbar_wait(stolen, i & 1)) {
+                        attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
+                        break;
+                    }
+                    idx = steal_result(steal_slot);
+                    fence_proxy_async_smem();  // read before the next answer is written
                 }
             }
         } else if (warp == kTmaWarp) {
@@ -433,45 +499,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 if (nq0 > 0) mbar_wait(&q_full[0], (nq0 - 1) & 1);
                 if (nq1 > 0) mbar_wait(&q_full[1], (nq1 - 1) & 1);
             }
-        } else if (warp == kMmaWarp) {
-            // -------------------------------------------------------- MMA issuer
+        } else {
+            // ------------------------------------------- MMA issue, a warp a sub
+            // A sub's products follow one another through its P and S; two warps, because a warp's
+            // waits and the issue itself take as long as its MMAs run: meanwhile the other sub's run.
             // The whole warp walks the items with warp-uniform values (the instruction takes its
             // descriptors from uniform registers; issued from one lane of divergent code, each MMA
             // cost about 90 cycles of moves); one elected lane issues.
             constexpr uint32_t idesc_pv = idesc_bf16_f32(kBM, D) | (1u << 16);  // B with N contiguous
+            const int s = warp == kMmaWarp ? 0 : 1;
             const bool leader = elect_one();
             bool ok = true;
-            const uint32_t q_addr = smem_u32(sm + L::kOffQ), kv_addr = smem_u32(sm + L::kOffKV);
+            const uint32_t q_addr = smem_u32(sm + L::kOffQ + s * L::kTile), kv_addr = smem_u32(sm + L::kOffKV);
+            const uint32_t tS = tmem + kColS + 128u * s, tO = tmem + kColO + 128u * s;
             uint32_t st = 0, ph = 0;     // ring stage of the next K tile, and its phase's parity
-            uint32_t nq = 0, np = 0;     // bit s: parity of the rows' tiles and of the probabilities taken
-            // per sub: the pending P V's ring stage (-1: none) with its phase, and its 16-key steps
-            int pv[2] = {-1, -1};
-            uint32_t vph[2] = {0, 0};
-            int psteps[2] = {0, 0};
-            bool pfirst[2] = {false, false};
+            uint32_t nq = 0, np = 0;     // parities of the rows' tiles and of the probabilities taken
+            int pv = -1;                 // ring stage of the pending P V's tile (-1: none), with
+            uint32_t vph = 0;            // its phase's parity,
+            int psteps = 0;              // its steps of 16 keys,
+            bool pfirst = false;         // and whether it starts the sum
+            int pitem = 0;               // the item it belongs to
             auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
-            auto issue_pv = [&](int s) {
-                const int v = pv[s];
-                if (!wait(&p_full[s], (np >> s) & 1) || !wait(&kv_full[v], vph[s])) return false;
-                np ^= 1u << s;
+            auto issue_pv = [&]() {
+                if (!wait(&kv_full[pv], vph) || !wait(&p_full[s], np)) return false;
+                // the sum starts over O once the last item's has been read (o_free: a phase an item)
+                if (pfirst && pitem > 0 && !wait(&o_free[s], (pitem - 1) & 1)) return false;
+                np ^= 1;
                 tc_fence_after();
-                const uint64_t vd = smem_desc_v(kv_addr + v * L::kTile);
-                const uint32_t d = tmem + kColO + 128u * s, a = tmem + kColS + 128u * s;
-                const bool last_use = pv[1 - s] != v;  // the other sub has no use of this V (any more)
+                const uint64_t vd = smem_desc_v(kv_addr + pv * L::kTile);
                 if (leader) {
-                    if (psteps[s] == kBN / 16) {
+                    if (psteps == kBN / 16) {
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
-                            tc_mma_ts_bf16(d, a + 8u * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || !pfirst[s]);
+                            tc_mma_ts_bf16(tO, tS + 8u * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || !pfirst);
                     } else {
-                        for (int kk = 0; kk < psteps[s]; ++kk)
-                            tc_mma_ts_bf16(d, a + 8u * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || !pfirst[s]);
+                        for (int kk = 0; kk < psteps; ++kk)
+                            tc_mma_ts_bf16(tO, tS + 8u * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || !pfirst);
                     }
                     tc_commit(&o_done[s]);
-                    if (last_use) tc_commit(&kv_empty[v]);
+                    tc_commit(&kv_empty[pv]);
                 }
                 __syncwarp();
-                pv[s] = -1;
+                pv = -1;
                 return true;
             };
             for (int i = 0;; ++i) {
@@ -481,153 +550,140 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 auto get = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
                 const int lo = get(ip->lo), hi = get(ip->hi), pair = get(ip->pair);
                 const AttnKeys keys = {get(ip->keys.sink), get(ip->keys.lo), get(ip->keys.hi), get(ip->keys.sink_tiles), get(ip->keys.main0), 0};
-                int left[2], sink[2], main0[2], end[2];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    left[s] = get(ip->sub[s].count);
-                    sink[s] = get(ip->sub[s].tiles_sink);
-                    main0[s] = get(ip->sub[s].main0);
-                    end[s] = get(ip->sub[s].end);
-                }
+                const int n_sink = ap.pr[get(ip->prob)].n_sink;
+                const TcSub &sub = ip->sub[s];
+                int left = get(sub.count);
+                const int sink = get(sub.tiles_sink), main0 = get(sub.main0), end = get(sub.end);
+                const int top_min = get(sub.top_min), low_max = get(sub.low_max);
                 __syncwarp();
                 if (leader) mbar_arrive(&i_empty[i % kItemSlots]);
-                bool first[2] = {true, true};
+                bool first = true;
 #pragma unroll 1
                 for (int n = lo; n < hi && ok; ++n) {
                     const int t = n < keys.sink_tiles ? n : keys.main0 + n - keys.sink_tiles;
-                    const int nk = tc_keys_in(keys, n < keys.sink_tiles, t);
-                    bool act[2];
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        act[s] = pair ? ((n - lo) & 1) == s : t < sink[s] || (t >= main0[s] && t < end[s]);
-                    const uint32_t vs = st + 1 == L::kStages ? 0 : st + 1;  // V follows K in the ring
-                    const uint32_t vp = st + 1 == L::kStages ? ph ^ 1 : ph;
-                    ok = wait(&kv_full[st], ph);
-                    // first the subs that see the tile: the pending P V of each, then its Q K^T (S is
-                    // overwritten behind the P V that reads P from it, in issue order)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (!ok || !act[s]) continue;
-                        if (pv[s] >= 0) ok = issue_pv(s);
-                        if (ok && first[s]) {
-                            ok = wait(&q_full[s], (nq >> s) & 1);
-                            nq ^= 1u << s;
-                        }
-                        if (!ok) continue;
-                        tc_fence_after();
-                        const uint32_t idesc = idesc_bf16_f32(kBM, nk);
-                        const uint64_t qd = smem_desc_sw128(q_addr + s * L::kTile), kd = smem_desc_sw128(kv_addr + st * L::kTile);
-                        --left[s];
-                        if (leader) {
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t koff = static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                                tc_mma_bf16(tmem + kColS + 128u * s, qd + koff, kd + koff, idesc, kk > 0);
-                            }
-                            tc_commit(&s_full[s]);
-                            if (left[s] == 0) tc_commit(&q_empty[s]);
-                        }
-                        __syncwarp();
-                        pv[s] = static_cast<int>(vs);
-                        vph[s] = vp;
-                        psteps[s] = nk / 16;
-                        pfirst[s] = first[s];
-                        first[s] = false;
-                    }
-                    if (ok && leader) tc_commit(&kv_empty[st]);  // K of this tile has been used
-                    __syncwarp();
-                    // then the pending P V of those that do not see it
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        if (ok && !act[s] && pv[s] >= 0) ok = issue_pv(s);
+                    const uint32_t ks = st, kp = ph;
+                    const uint32_t vs = ks + 1 == L::kStages ? 0 : ks + 1;  // V follows K in the ring
+                    const uint32_t vp = ks + 1 == L::kStages ? kp ^ 1 : kp;
                     st = vs + 1 == L::kStages ? 0 : vs + 1;
                     ph = vs + 1 == L::kStages ? vp ^ 1 : vp;
+                    if (pair ? ((n - lo) & 1) != s : !(t < sink || (t >= main0 && t < end))) {
+                        // not this sub's: what is pending goes, and the tile is given up (once it is
+                        // there: a phase of kv_empty takes one arrival of each sub)
+                        if (pv >= 0) ok = issue_pv();
+                        ok = ok && wait(&kv_full[ks], kp);
+                        if (ok && leader) mbar_arrive(&kv_empty[ks]);
+                        ok = ok && wait(&kv_full[vs], vp);
+                        if (ok && leader) mbar_arrive(&kv_empty[vs]);
+                        __syncwarp();
+                        continue;
+                    }
+                    const int j0 = t * kBN, nk = tc_keys_in(keys, n < keys.sink_tiles, t);
+                    const bool edge = j0 + nk > keys.hi || (j0 < keys.lo && j0 + nk > keys.sink);
+                    const bool mask = j0 + kBN - 1 > top_min || (j0 < low_max && j0 + kBN > n_sink);
+                    const TcStep step = {j0, nk | (mask ? kStepMask : 0) | (edge ? kStepEdge : 0) | static_cast<int>(vs << 16 | vp << 24)};
+                    const uint32_t idesc = idesc_bf16_f32(kBM, nk);
+                    const uint64_t qd = smem_desc_sw128(q_addr), kd = smem_desc_sw128(kv_addr + ks * L::kTile);
+                    ok = wait(&kv_full[ks], kp);
+                    if (ok && first) {
+                        ok = wait(&q_full[s], nq);
+                        nq ^= 1;
+                    }
+                    // the pending P V, then Q K^T: S is overwritten behind the P V that reads P from it, in issue order
+                    if (ok && pv >= 0) ok = issue_pv();
+                    if (!ok) break;
+                    tc_fence_after();
+                    --left;
+                    if (leader) {
+                        steps[s] = step;  // the softmax warps are done with the last one: they have written its P
+                        mbar_arrive(&s_full[s]);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t koff = static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                            tc_mma_bf16(tS, qd + koff, kd + koff, idesc, kk > 0);
+                        }
+                        tc_commit(&s_full[s]);
+                        tc_commit(&kv_empty[ks]);
+                        if (left == 0) tc_commit(&q_empty[s]);
+                    }
+                    __syncwarp();
+                    pv = static_cast<int>(vs);
+                    vph = vp;
+                    psteps = nk / 16;
+                    pfirst = first;
+                    pitem = i;
+                    first = false;
                 }
                 // an item without tiles pushes nothing out: what is pending goes now, or the softmax
                 // warps, and behind them the scheduler, would wait for it
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    if (ok && lo == hi && pv[s] >= 0) ok = issue_pv(s);
+                if (ok && lo == hi && pv >= 0) ok = issue_pv();
                 if (!ok) break;
             }
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (ok && pv[s] >= 0) ok = issue_pv(s);
+            if (ok && pv >= 0) ok = issue_pv();
             if (leader) {
                 if (!ok) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
-                tc_commit(fin);
-                mbar_wait(fin, 0);
+                tc_commit(&fin[s]);
+                mbar_wait(&fin[s], 0);
             }
             __syncwarp();
         }
-    } else {
-        // ------------------------------------------------ softmax and output
+    } else if (warp < kSoftmaxWarps) {
+        // ----------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int s = warp >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tS = tmem + kColS + 128u * s + lanes, tO = tmem + kColO + 128u * s + lanes;
         const float c = ap.scale_log2;
-        const int G = ap.G;
         bool ok = true;
-        int ld = 0, nt = 0;  // ring loads before this item; tiles of this sub so far
-        for (int i = 0;; ++i) {
+        uint32_t nt = 0;          // parity of this sub's next tile
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity))) {
+                ok = false;
+                if (lane == 0) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
+            }
+        };
+        for (int i = 0; ok; ++i) {
             bool got = true;
             const TcItem *ip = take(i, got);
-            // all 256 threads leave together: they meet at barriers inside
-            const int votes = named_bar_count(2, 2 * kSubThreads, ip != nullptr);
-            if (votes < 2 * kSubThreads) {
-                if ((votes > 0 || !got) && lane == 0) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
+            if (!__all_sync(0xffffffffu, ip != nullptr)) {
+                if (!got && lane == 0) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
                 break;
             }
             const TcItem &it = *ip;
             const AttnProblem &p = ap.pr[it.prob];
-            const TcSub u = it.sub[s];
             if (it.bad && tid == 0) attn_flag(ap.err, KVEVICT_DEV_BAD_LENGTH);
-            const int nrows = u.nt * G;
+            const int n_sink = p.n_sink;
+            // the keys this row sees: j <= top, and j < n_sink or j >= low
+            int top = it.m - 1, low = 0;
+            const int nrows = it.sub[s].nt * ap.G;
+            if (p.causal) {
+                top = it.sub[s].top_min + min(row, nrows - 1) / ap.G;
+                if (p.window > 0) low = max(0, top - p.window + 1);
+            }
             const bool live = quad * 32 < nrows;  // this warp has rows
-            // the positions this row sees: j <= top, and j < n_sink or j >= low
-            const int pos = p.causal ? it.p0 + u.t0 + min(row, nrows - 1) / G : it.m - 1;
-            const int top = pos;
-            const int low = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-            // of all the sub's rows: the least top, the greatest low
-            const int top_min = p.causal ? it.p0 + u.t0 : it.m - 1;
-            const int pos_max = p.causal ? it.p0 + u.t0 + u.nt - 1 : it.m - 1;
-            const int low_max = p.window > 0 && pos_max >= p.window ? pos_max - p.window + 1 : 0;
             float m = -INFINITY, l = 0.f;
-            int done = 0;  // tiles of this item
-            for (int n = it.lo; n < it.hi; ++n) {
-                if (!tc_active(it, n, s)) continue;
-                if (ok && !__all_sync(0xffffffffu, mbar_wait(&s_full[s], nt & 1))) {
-                    ok = false;
-                    if (lane == 0) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
-                }
+            const int count = it.sub[s].count;
+#pragma unroll 1
+            for (int k = 0; k < count; ++k) {
+                wait(&s_full[s], nt);
                 tc_fence_after();
-                const int j0 = attn_tile_at(it.keys, n) * kBN;
-                const int keys = tc_keys_in(it.keys, n < it.keys.sink_tiles, j0 / kBN);
+                const TcStep step = steps[s];
                 if (ok && live) {
-                    const bool masked = j0 + kBN - 1 > top_min || (j0 < low_max && j0 + kBN > p.n_sink);
+                    const bool small = (step.what & 255) <= 32;
                     uint32_t r[4][32];
-                    const bool small = keys <= 32;
                     tmem_ld32(tS, r[0]);
                     if (!small) {
-                        tmem_ld32(tS + 32, r[1]);
-                        tmem_ld32(tS + 64, r[2]);
-                        tmem_ld32(tS + 96, r[3]);
+#pragma unroll
+                        for (int g = 1; g < 4; ++g) tmem_ld32(tS + 32u * g, r[g]);
                     }
                     tc_wait_ld();
-                    float mx;
-                    if (small) {
-                        if (masked) tc_mask32(r[0], top - j0, low - j0, p.n_sink - j0);
-                        mx = tc_max32(r[0]);
-                    } else {
-                        if (masked) {
+                    if (step.what & kStepMask) {
 #pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                tc_mask32(r[g], top - j0 - 32 * g, low - j0 - 32 * g, p.n_sink - j0 - 32 * g);
-                        }
-                        mx = fmaxf(fmaxf(tc_max32(r[0]), tc_max32(r[1])), fmaxf(tc_max32(r[2]), tc_max32(r[3])));
+                        for (int g = 0; g < 4; ++g)
+                            tc_mask32(r[g], top - step.j0 - 32 * g, low - step.j0 - 32 * g, n_sink - step.j0 - 32 * g);
                     }
+                    float mx = tc_max32(r[0]);
+                    if (!small) mx = fmaxf(fmaxf(mx, tc_max32(r[1])), fmaxf(tc_max32(r[2]), tc_max32(r[3])));
                     mx *= c;
                     // rescale where the maximum outgrew the one in use (a first finite one included)
                     const bool grow = mx > m + kRescale || (m == -INFINITY && mx != -INFINITY);
@@ -636,21 +692,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         const float f = m == -INFINITY ? 0.f : ex2(m - mn);
                         m = mn;
                         l *= f;
-                        if (done > 0) {
+                        if (k > 0) {
                             // O holds tiles before this one: wait for the last of them, then scale it
-                            if (!__all_sync(0xffffffffu, mbar_wait(&o_done[s], (nt - 1) & 1))) {
-                                ok = false;
-                                if (lane == 0) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
-                            } else {
+                            wait(&o_done[s], nt ^ 1);
+                            if (ok) {
                                 tc_fence_after();
-#pragma unroll
-                                for (int q = 0; q < D; q += 32) {
-                                    uint32_t o[32];
-                                    tmem_ld32(tO + q, o);
+#pragma unroll 1
+                                for (int q = 0; q < D; q += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tO + q, o);
                                     tc_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st32(tO + q, o);
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st16(tO + q, o);
                                 }
                             }
                         }
@@ -660,123 +714,166 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     float2 sum[4];
 #pragma unroll
                     for (int g = 0; g < 4; ++g) sum[g] = make_float2(0.f, 0.f);
-                    uint32_t pk[32];  // 64 probabilities
-                    tc_exp32(r[0], c2, nm2, sum, pk);
-                    if (!small) {
-                        tc_exp32(r[1], c2, nm2, sum, pk + 16);
-                        tmem_st32(tS, pk);
-                        tc_exp32(r[2], c2, nm2, sum, pk);
-                        tc_exp32(r[3], c2, nm2, sum, pk + 16);
-                        tmem_st32(tS + 32, pk);
+                    if (small) {
+                        uint32_t pk[16];
+                        tc_exp32(r[0], c2, nm2, sum, pk);
+                        tmem_st16(tS, pk);
                     } else {
 #pragma unroll
-                        for (int e = 16; e < 32; ++e) pk[e] = 0u;
-                        tmem_st32(tS, pk);
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t pk[16];  // 32 probabilities
+                            tc_exp32(r[g], c2, nm2, sum, pk);
+                            tmem_st16(tS + 16u * g, pk);
+                        }
                     }
-                    const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
-                    l += t.x + t.y;
+                    const float2 t2 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                    l += t2.x + t2.y;
                     tc_wait_st();
                 }
-                // V rows that no row of the item sees may hold anything: 0 times that must be 0
-                const bool edge = j0 + keys > it.keys.hi || (j0 < it.keys.lo && j0 + keys > it.keys.sink);
-                if (edge) {
-                    const int v = ld + 2 * (n - it.lo) + 1, st = v % L::kStages;
-                    if (ok && !__all_sync(0xffffffffu, mbar_wait(&kv_full[st], (v / L::kStages) & 1))) {
-                        ok = false;
-                        if (lane == 0) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
-                    }
-                    const int j = j0 + row;
-                    if (ok && row < keys && !(j < it.keys.sink || (j >= it.keys.lo && j < it.keys.hi))) {
-                        uint4 *z = reinterpret_cast<uint4 *>(sm + L::kOffKV + st * L::kTile + row * 128);
+                if (step.what & kStepEdge) {
+                    // V rows that no row of the item sees may hold anything: 0 times that must be 0
+                    const int vs = (step.what >> 16) & 255;
+                    wait(&kv_full[vs], step.what >> 24);
+                    const int j = step.j0 + row;
+                    if (ok && row < (step.what & 255) && !(j < it.keys.sink || (j >= it.keys.lo && j < it.keys.hi))) {
 #pragma unroll
-                        for (int e = 0; e < D / 64; ++e)
+                        for (int x = 0; x < D / 64; ++x) {
+                            uint4 *z = reinterpret_cast<uint4 *>(sm + L::kOffKV + vs * L::kTile + x * 16384 + row * 128);
 #pragma unroll
-                            for (int w = 0; w < 8; ++w) z[e * 1024 + w] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int w = 0; w < 8; ++w) z[w] = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[s]);
-                ++nt;
-                ++done;
+                nt ^= 1;
             }
-            ld += 2 * (it.hi - it.lo);
-
-            // -------------------------------------------------------- output
-            if (done > 0 && ok && !__all_sync(0xffffffffu, mbar_wait(&o_done[s], (nt - 1) & 1))) {
+            // the row's sum, for the output warps: they have read the last item's
+            if (i > 0) wait(&o_free[s], (i - 1) & 1);
+            xl[(s * 2) * kBM + row] = l == 0.f ? -INFINITY : m + log2f(l);
+            xl[(s * 2 + 1) * kBM + row] = l > 0.f ? 1.f / l : l;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&l_ready[s]);
+                mbar_arrive(&i_empty[i % kItemSlots]);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ output
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const uint32_t tO = tmem + kColO + (static_cast<uint32_t>(quad * 32) << 16);
+        bool ok = true;
+        uint32_t tiles = 0;  // bit s: parity of the sub's tiles so far
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity))) {
                 ok = false;
                 if (lane == 0) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
             }
-            tc_fence_after();
-            const int t = it.q0 + u.t0 + row / G, h = it.kvh * G + row % G;
-            const long long at = it.b * p.rs[0] + h * p.rs[1] + t * p.rs[2];
-            float f0 = l > 0.f ? 1.f / l : l, f1 = 0.f;  // factors on this sub's O and the other's
-            float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-            int col0 = 0, cols = D;
-            uint32_t tO1 = tO;
-            if (it.pair) {
-                // both subs hold the same rows: each scales its own O to a normalised one, by
-                // weights from the normalisers (shared memory), and writes half of the columns of
-                // the sum; the other's O is read through TMEM (the two warpgroups' warps address
-                // the same lanes), its factor 1 / l with the weight (shared memory again)
-                xl[s * kBM + row] = lse2;
-                named_bar_sync(1, 2 * kSubThreads);
-                const float other = xl[(1 - s) * kBM + row];
-                const float mt = fmaxf(lse2, other), mm = mt == -INFINITY ? 0.f : mt;
-                const float w = ex2(lse2 - mm), total = w + ex2(other - mm);
-                lse2 = total == 0.f ? -INFINITY : mt + log2f(total);
-                f0 = l == 0.f ? 0.f : f0 * (w / total);
-                named_bar_sync(1, 2 * kSubThreads);
-                xl[s * kBM + row] = f0;
-                tc_fence_before();
-                named_bar_sync(1, 2 * kSubThreads);
-                tc_fence_after();
-                f1 = xl[(1 - s) * kBM + row];
-                cols = D / 2;
-                col0 = s * cols;
-                tO1 = tmem + kColO + 128u * (1 - s) + lanes;
+        };
+        for (int i = 0; ok; ++i) {
+            bool got = true;
+            const TcItem *ip = take(i, got);
+            if (!__all_sync(0xffffffffu, ip != nullptr)) {
+                if (!got && lane == 0) attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
+                break;
             }
-            if (ok && live) {
-                const bool split = ap.slots > 1;
-                const long long slot = (p.slot0 + it.part) * ap.rows + at;
-                float *po = split ? ap.part_o + slot * D : nullptr;
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(ap.out) + it.b * p.os[0] + h * p.os[1] + t * p.os[2];
-                const bool any0 = f0 != 0.f, any1 = f1 != 0.f;
-                for (int q = col0; q < col0 + cols; q += 32) {
-                    uint32_t o[32];
-                    float v[32];
-                    tmem_ld32(tO + q, o);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = any0 ? __uint_as_float(o[e]) * f0 : 0.f;
-                    if (it.pair) {
-                        tmem_ld32(tO1 + q, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] += any1 ? __uint_as_float(o[e]) * f1 : 0.f;
-                    }
-                    if (row < nrows) {
-                        if (split) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4 *>(po + q + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                *reinterpret_cast<uint4 *>(out + q + e) =
-                                    make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
-                                               pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
-                        }
-                    }
+            const TcItem &it = *ip;
+            const AttnProblem &p = ap.pr[it.prob];
+            const bool pair = it.pair != 0, split = ap.slots > 1;
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) {
+                // the sub's sums are there, and its last P V (the one before it was complete when the
+                // softmax warps read their last logits, so the parity is not a phase behind)
+                wait(&l_ready[s], i & 1);
+                tiles ^= (it.sub[s].count & 1) << s;
+                if (it.sub[s].count > 0) wait(&o_done[s], ((tiles >> s) & 1) ^ 1);
+                if (pair && s == 0) continue;
+                tc_fence_after();
+                const int nrows = it.sub[s].nt * ap.G;
+                // factors on this sub's O, or, where both hold the same rows, on both subs'
+                float lse2 = xl[s * 2 * kBM + row], f0 = xl[(s * 2 + 1) * kBM + row], f1 = 0.f;
+                if (pair) {
+                    const float lse_o = xl[row], inv_o = xl[kBM + row];
+                    const float mt = fmaxf(lse2, lse_o), mm = mt == -INFINITY ? 0.f : mt;
+                    const float w0 = ex2(lse2 - mm), w1 = ex2(lse_o - mm), total = w0 + w1;
+                    f0 = lse2 == -INFINITY ? 0.f : f0 * (w0 / total);
+                    f1 = lse_o == -INFINITY ? 0.f : inv_o * (w1 / total);
+                    lse2 = total == 0.f ? -INFINITY : mt + log2f(total);
                 }
-                if (row < nrows && col0 == 0) {
+                const bool any0 = f0 != 0.f, any1 = f1 != 0.f;
+                // where this lane's row goes, in units of 16 bytes, and the four rows of its quad
+                const int tok = it.q0 + it.sub[s].t0 + row / ap.G, h = it.kvh * ap.G + row % ap.G;
+                const long long at = it.b * p.rs[0] + h * p.rs[1] + tok * p.rs[2];
+                const long long slot = (p.slot0 + it.part) * ap.rows + at;
+                const long long base = split ? slot * (D / 4) : (it.b * p.os[0] + h * p.os[1] + tok * p.os[2]) / 8;
+                const bool live = ok && quad * 32 < nrows;
+                if (live && row < nrows) {
                     if (split) ap.part_l[slot] = lse2;
                     else if (ap.lse) ap.lse[at] = lse2 * kLn2;
                 }
+                uint4 *dst[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const long long off = __shfl_sync(0xffffffffu, base, (lane & ~3) + e);
+                    dst[e] = (split ? reinterpret_cast<uint4 *>(ap.part_o) : static_cast<uint4 *>(ap.out)) + off + (lane & 3);
+                    if (quad * 32 + (lane & ~3) + e >= nrows) dst[e] = nullptr;
+                }
+                // 16 columns of the rows' output
+                auto take16 = [&](int q, float (&v)[16]) {
+                    uint32_t o[16];
+                    tmem_ld16(tO + 128u * s + q, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = any0 ? __uint_as_float(o[e]) * f0 : 0.f;
+                    if (pair) {
+                        tmem_ld16(tO + q, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] += any1 ? __uint_as_float(o[e]) * f1 : 0.f;
+                    }
+                };
+                // O is free for the next item once its last columns are in registers, before their stores
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&o_free[s]);
+                        if (pair) mbar_arrive(&o_free[0]);
+                    }
+                };
+                if (!live) {
+                    release();
+                } else if (split) {
+#pragma unroll 1
+                    for (int q = 0; q < D; q += 16) {
+                        float v[16];
+                        take16(q, v);
+                        if (q + 16 == D) release();
+                        tc_store_rows(*reinterpret_cast<uint4(*)[4]>(v), dst, q / 4);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < D; q += 64) {
+                        uint4 w[8];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float v[16];
+                            take16(q + 16 * x, v);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                w[2 * x + e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                                          pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+                        }
+                        if (q + 64 == D) release();
+                        tc_store_rows(*reinterpret_cast<uint4(*)[4]>(w), dst, q / 8);
+                        tc_store_rows(*reinterpret_cast<uint4(*)[4]>(w + 4), dst, q / 8 + 4);
+                    }
+                }
             }
-            tc_fence_before();
-            if (it.pair) named_bar_sync(1, 2 * kSubThreads);  // the other's O and factors have been read
             __syncwarp();
             if (lane == 0) mbar_arrive(&i_empty[i % kItemSlots]);
         }
@@ -800,7 +897,7 @@ template <int D> cudaError_t launch_tc(const AttnTcParams &p, int sms, cudaStrea
     }();
     if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;  // the split would wait for registers that are not there
     const int n = p.a.pr[0].n_items + (p.a.n_problems > 1 ? p.a.pr[1].n_items : 0);
-    attn_tc_kernel<D><<<n < sms ? n : sms, kTcThreads, bytes, st>>>(p);
+    attn_tc_kernel<D><<<n, kTcThreads, bytes, st>>>(p);
     return cudaGetLastError();
 }
 
