@@ -37,8 +37,8 @@ constexpr int kTmaWarp = 12, kSchedWarp = 13, kMmaWarp = 14;  // and 15
 constexpr int kTcThreads = 512;
 // Registers a thread: the launch's 128 (65,536 over 512 threads), moved to the
 // two softmax warpgroups, whose threads hold a whole row of 128 logits:
-// 2 x 168 + 104 + 72 = 4 x 128.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kOutRegs = 104, kIssueRegs = 72;
+// 2 x 160 + 120 + 72 = 4 x 128.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kOutRegs = 120, kIssueRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOutRegs + kIssueRegs <= 4 * kLaunchRegs, "register split");
 constexpr uint32_t kTcTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * sub
@@ -53,7 +53,7 @@ template <int D> struct TcLayout {
     static constexpr int kOffBar = kOffKV + kStages * kTile;
     static constexpr int kOffX = kOffBar + 384;            // [2 subs][2][128 rows]: log2 normalisers, 1 / l
     static constexpr int kOffItem = kOffX + 4 * kBM * 4;   // posted items
-    static constexpr int kOffStep = kOffItem + 288;        // the two subs' steps; a cancelled block's index
+    static constexpr int kOffStep = kOffItem + 544;        // the two subs' steps; a cancelled block's index
     static constexpr int kBytes = kOffStep + 32;
 };
 static_assert(TcLayout<128>::kBytes <= 232448 && TcLayout<64>::kBytes <= 232448, "shared memory");
@@ -222,7 +222,15 @@ __device__ __forceinline__ void tc_exp32(const uint32_t (&r)[32], float2 c2, flo
 // instruction, 16 bytes of each; the four lanes of a quad exchange their 16-byte
 // pieces (a 4 x 4 transpose in two rounds), so that each store covers 64 bytes
 // of eight rows. dst: the quad's four rows, + the lane's piece; null: no row.
-__device__ __forceinline__ void tc_store_rows(const uint4 (&w)[4], uint4 *const (&dst)[4], int at)
+struct TcWords {
+    uint4 a, b, c, d;
+};
+__device__ __forceinline__ TcWords tc_words(const uint32_t *w)
+{
+    return TcWords{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]), make_uint4(w[8], w[9], w[10], w[11]),
+                   make_uint4(w[12], w[13], w[14], w[15])};
+}
+__device__ __forceinline__ void tc_store_rows(const TcWords &w, uint4 *const (&dst)[4], int at)
 {
     const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
     auto swap = [](uint4 &a, uint4 &b, bool up, int mask) {  // a of the upper lane for b of the lower
@@ -235,7 +243,7 @@ __device__ __forceinline__ void tc_store_rows(const uint4 (&w)[4], uint4 *const 
         if (up) a = in;
         else b = in;
     };
-    uint4 a = w[0], b = w[1], c = w[2], d = w[3];
+    uint4 a = w.a, b = w.b, c = w.c, d = w.d;
     swap(a, b, odd, 1);
     swap(c, d, odd, 1);
     swap(a, c, high, 2);
@@ -273,7 +281,7 @@ struct TcItem {
     int pair;
     TcSub sub[2];
 };
-constexpr int kItemSlots = 2;
+constexpr int kItemSlots = 4;
 
 __device__ __forceinline__ bool tc_active(const TcItem &it, int n, int s)
 {
@@ -363,7 +371,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     uint64_t *kv_full = o_done + 2;             // [kStages]
     uint64_t *kv_empty = kv_full + L::kStages;  // [kStages]
     uint64_t *l_ready = kv_empty + L::kStages;  // [2] a sub's sums of the item are in shared memory
-    uint64_t *o_free = l_ready + 2;             // [2] its O has been read
+    uint64_t *l_free = l_ready + 2;             // [2] and have been read there
+    uint64_t *o_free = l_free + 2;              // [2] its O has been read (a phase an item with tiles of the sub)
     uint64_t *i_full = o_free + 2;              // [kItemSlots] an item is posted
     uint64_t *i_empty = i_full + kItemSlots;    // [kItemSlots] every role is done with it
     uint64_t *fin = i_empty + kItemSlots;       // [2] an MMA warp's last operation completed
@@ -373,8 +382,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     TcStep *steps = reinterpret_cast<TcStep *>(sm + L::kOffStep);  // [2]
     uint8_t *steal_slot = sm + L::kOffStep + 16;
     float *xl = reinterpret_cast<float *>(sm + L::kOffX);
-    static_assert((15 + 2 * L::kStages + 2 * kItemSlots + 2) * 8 + 4 <= 384, "barrier area");
-    static_assert(kItemSlots * sizeof(TcItem) <= 288 && L::kOffStep % 16 == 0, "item area");
+    static_assert((17 + 2 * L::kStages + 2 * kItemSlots + 2) * 8 + 4 <= 384, "barrier area");
+    static_assert(kItemSlots * sizeof(TcItem) <= 544 && L::kOffStep % 16 == 0, "item area");
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp-uniform to the compiler
@@ -386,6 +395,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(&p_full[s], 4);
             mbar_init(&o_done[s], 1);
             mbar_init(&l_ready[s], 4);
+            mbar_init(&l_free[s], 4);
             mbar_init(&o_free[s], 4);
             mbar_init(&fin[s], 1);
         }
@@ -423,24 +433,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             // takes over one after another of those that have not started.
             if (lane == 0) {
                 int idx = blockIdx.x;
+                uint32_t asked = 0;
+                auto next = [&]() {
+                    mbar_arrive_expect_tx(stolen, 16);
+                    steal_request(steal_slot, stolen);
+                    if (!mbar_wait(stolen, asked++ & 1)) {
+                        attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
+                        return -1;
+                    }
+                    const int x = steal_result(steal_slot);
+                    fence_proxy_async_smem();  // read before the next answer is written
+                    return x;
+                };
                 for (int i = 0;; ++i) {
                     const int slot = i % kItemSlots;
                     if (i >= kItemSlots && !mbar_wait(&i_empty[slot], ((i / kItemSlots) - 1) & 1)) {
+                        // a role gave up: the blocks that have not started are taken and dropped, so that
+                        // the launch ends with the ones that run
                         attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
+                        while (idx >= 0) idx = next();
                         break;
                     }
                     if (idx < 0) items[slot].prob = -1;
                     else tc_make_item(tp, idx, items[slot]);
                     mbar_arrive(&i_full[slot]);
                     if (idx < 0) break;
-                    mbar_arrive_expect_tx(stolen, 16);
-                    steal_request(steal_slot, stolen);
-                    if (!mbar_wait(stolen, i & 1)) {
-                        attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
-                        break;
-                    }
-                    idx = steal_result(steal_slot);
-                    fence_proxy_async_smem();  // read before the next answer is written
+                    idx = next();
                 }
             }
         } else if (warp == kTmaWarp) {
@@ -518,12 +536,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             uint32_t vph = 0;            // its phase's parity,
             int psteps = 0;              // its steps of 16 keys,
             bool pfirst = false;         // and whether it starts the sum
-            int pitem = 0;               // the item it belongs to
+            uint32_t sums = 0;           // items with tiles of this sub before the pending one's
             auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
             auto issue_pv = [&]() {
                 if (!wait(&kv_full[pv], vph) || !wait(&p_full[s], np)) return false;
-                // the sum starts over O once the last item's has been read (o_free: a phase an item)
-                if (pfirst && pitem > 0 && !wait(&o_free[s], (pitem - 1) & 1)) return false;
+                // a sum starts over O once the one before has been read
+                if (pfirst && sums++ > 0 && !wait(&o_free[s], sums & 1)) return false;
                 np ^= 1;
                 tc_fence_after();
                 const uint64_t vd = smem_desc_v(kv_addr + pv * L::kTile);
@@ -610,7 +628,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     vph = vp;
                     psteps = nk / 16;
                     pfirst = first;
-                    pitem = i;
                     first = false;
                 }
                 // an item without tiles pushes nothing out: what is pending goes now, or the softmax
@@ -751,7 +768,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 nt ^= 1;
             }
             // the row's sum, for the output warps: they have read the last item's
-            if (i > 0) wait(&o_free[s], (i - 1) & 1);
+            if (i > 0) wait(&l_free[s], (i - 1) & 1);
             xl[(s * 2) * kBM + row] = l == 0.f ? -INFINITY : m + log2f(l);
             xl[(s * 2 + 1) * kBM + row] = l > 0.f ? 1.f / l : l;
             __syncwarp();
@@ -804,6 +821,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     f1 = lse_o == -INFINITY ? 0.f : inv_o * (w1 / total);
                     lse2 = total == 0.f ? -INFINITY : mt + log2f(total);
                 }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&l_free[s]);
+                    if (pair) mbar_arrive(&l_free[0]);
+                }
                 const bool any0 = f0 != 0.f, any1 = f1 != 0.f;
                 // where this lane's row goes, in units of 16 bytes, and the four rows of its quad
                 const int tok = it.q0 + it.sub[s].t0 + row / ap.G, h = it.kvh * ap.G + row % ap.G;
@@ -822,56 +844,60 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     dst[e] = (split ? reinterpret_cast<uint4 *>(ap.part_o) : static_cast<uint4 *>(ap.out)) + off + (lane & 3);
                     if (quad * 32 + (lane & ~3) + e >= nrows) dst[e] = nullptr;
                 }
-                // 16 columns of the rows' output
-                auto take16 = [&](int q, float (&v)[16]) {
-                    uint32_t o[16];
-                    tmem_ld16(tO + 128u * s + q, o);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = any0 ? __uint_as_float(o[e]) * f0 : 0.f;
-                    if (pair) {
-                        tmem_ld16(tO + q, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] += any1 ? __uint_as_float(o[e]) * f1 : 0.f;
-                    }
-                };
                 // O is free for the next item once its last columns are in registers, before their stores
                 auto release = [&]() {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&o_free[s]);
-                        if (pair) mbar_arrive(&o_free[0]);
+                        if (it.sub[s].count > 0) mbar_arrive(&o_free[s]);
+                        if (pair && it.sub[0].count > 0) mbar_arrive(&o_free[0]);
                     }
                 };
                 if (!live) {
                     release();
-                } else if (split) {
+                } else if (pair || split) {
 #pragma unroll 1
-                    for (int q = 0; q < D; q += 16) {
-                        float v[16];
-                        take16(q, v);
-                        if (q + 16 == D) release();
-                        tc_store_rows(*reinterpret_cast<uint4(*)[4]>(v), dst, q / 4);
+                    for (int q = 0; q < D; q += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 128u * s + q, o);
+                        if (pair) {
+                            uint32_t x[32];
+                            tmem_ld32(tO + q, x);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint((any0 ? __uint_as_float(o[e]) * f0 : 0.f) + (any1 ? __uint_as_float(x[e]) * f1 : 0.f));
+                        } else {
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(any0 ? __uint_as_float(o[e]) * f0 : 0.f);
+                        }
+                        if (q + 32 == D) release();
+                        if (split) {
+                            tc_store_rows(tc_words(o), dst, q / 4);
+                            tc_store_rows(tc_words(o + 16), dst, q / 4 + 4);
+                        } else {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                            tc_store_rows(tc_words(w), dst, q / 8);
+                        }
                     }
                 } else {
-#pragma unroll 1
-                    for (int q = 0; q < D; q += 64) {
-                        uint4 w[8];
+                    // all columns first, as bf16
+                    uint32_t w[D / 2];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            float v[16];
-                            take16(q + 16 * x, v);
+                    for (int q = 0; q < D; q += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 128u * s + q, o);
+                        tc_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                w[2 * x + e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                                          pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
-                        }
-                        if (q + 64 == D) release();
-                        tc_store_rows(*reinterpret_cast<uint4(*)[4]>(w), dst, q / 8);
-                        tc_store_rows(*reinterpret_cast<uint4(*)[4]>(w + 4), dst, q / 8 + 4);
+                        for (int e = 0; e < 16; ++e)
+                            w[q / 2 + e] = any0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * f0, __uint_as_float(o[2 * e + 1]) * f0) : 0u;
                     }
+                    release();
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) tc_store_rows(tc_words(w + 16 * q), dst, 4 * q);
                 }
             }
             __syncwarp();
