@@ -98,7 +98,8 @@ void cut_for(Plan &w, AttnProblem &q, int64_t max_k)
     if (w.tensor) {
         const bool pair = q.max_q <= kAttnTcRows / G;
         cut(q, G, w.p.Hkv, (pair ? 1 : 2) * (kAttnTcRows / G) * G, kAttnTcKeys, max_k, 0, true);
-        q.pair = pair;
+        // (one key tile at most: nothing to share, the second tile stays without rows)
+        q.pair = pair && key_tiles(max_k, q.n_sink, q.causal ? q.window : 0, q.max_q, kAttnTcKeys) > 1;
     } else {
         cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows, kAttnF32Keys, max_k, 0, true);
     }
@@ -115,7 +116,7 @@ int finish(Plan &w, int head_dim)
     for (int i = 0; i < p.n_problems; ++i) {
         AttnProblem &q = p.pr[i];
         q.slot0 = p.slots;
-        p.slots += q.splits;
+        p.slots += q.splits * (q.pair ? 2 : 1);  // both row tiles of a pair write a part
         const int64_t n = static_cast<int64_t>(q.batch) * p.Hkv * q.q_tiles * q.splits;
         if (n >= (int64_t{1} << 30)) return KVEVICT_ERR_INVALID_ARG;
         q.n_items = static_cast<int>(n);

@@ -15,8 +15,8 @@
 // threads a row: while one sub's rows go through the softmax the tensor cores
 // work for the other. A K or V tile of 128 keys is loaded once for both subs
 // (TMA ring). Where a unit's rows fit one sub ("pair": decoding, short
-// chunks), both hold the same rows and take alternate key tiles; their sums
-// are joined through TMEM at the end of the item. Rows are (token, group
+// chunks), both hold the same rows and take alternate key tiles, each a part of
+// its own to the join. Rows are (token, group
 // head) pairs, so all query heads of a KV head share its tiles.
 //
 // Warps 0-3, 4-7: softmax and output of sub 0, 1, the first 64 keys of each
@@ -806,98 +806,68 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 // the sub's sums are there, and its last P V (the one before it was complete when the
                 // softmax warps read their last logits, so the parity is not a phase behind)
                 wait(&l_ready[s], i & 1);
-                tiles ^= (it.sub[s].count & 1) << s;
-                if (it.sub[s].count > 0) wait(&o_done[s], ((tiles >> s) & 1) ^ 1);
-                if (pair && s == 0) continue;
-                tc_fence_after();
-                const int nrows = it.sub[s].nt * ap.G;
-                // factors on this sub's O, or, where both hold the same rows, on both subs'
-                float lse2 = xl[s * 2 * kBM + row], f0 = xl[(s * 2 + 1) * kBM + row], f1 = 0.f;
-                if (pair) {
-                    const float lse_o = xl[row], inv_o = xl[kBM + row];
-                    const float mt = fmaxf(lse2, lse_o), mm = mt == -INFINITY ? 0.f : mt;
-                    const float w0 = ex2(lse2 - mm), w1 = ex2(lse_o - mm), total = w0 + w1;
-                    f0 = lse2 == -INFINITY ? 0.f : f0 * (w0 / total);
-                    f1 = lse_o == -INFINITY ? 0.f : inv_o * (w1 / total);
-                    lse2 = total == 0.f ? -INFINITY : mt + log2f(total);
-                }
+                const int count = it.sub[s].count, nrows = it.sub[s].nt * ap.G;
+                const float lse2 = xl[s * 2 * kBM + row], f = xl[(s * 2 + 1) * kBM + row];
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&l_free[s]);
-                    if (pair) mbar_arrive(&l_free[0]);
-                }
-                const bool any0 = f0 != 0.f, any1 = f1 != 0.f;
-                // where this lane's row goes, in units of 16 bytes, and the four rows of its quad
+                if (lane == 0) mbar_arrive(&l_free[s]);
+                // where this lane's row goes, in units of 16 bytes
                 const int tok = it.q0 + it.sub[s].t0 + row / ap.G, h = it.kvh * ap.G + row % ap.G;
                 const long long at = it.b * p.rs[0] + h * p.rs[1] + tok * p.rs[2];
-                const long long slot = (p.slot0 + it.part) * ap.rows + at;
-                const long long base = split ? slot * (D / 4) : (it.b * p.os[0] + h * p.os[1] + tok * p.os[2]) / 8;
-                const bool live = ok && quad * 32 < nrows;
-                if (live && row < nrows) {
+                const long long slot = (p.slot0 + (pair ? 2 * it.part + s : it.part)) * ap.rows + at;
+                const bool mine = ok && row < nrows, live = ok && quad * 32 < nrows;
+                if (mine) {
                     if (split) ap.part_l[slot] = lse2;
                     else if (ap.lse) ap.lse[at] = lse2 * kLn2;
                 }
-                uint4 *dst[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const long long off = __shfl_sync(0xffffffffu, base, (lane & ~3) + e);
-                    dst[e] = (split ? reinterpret_cast<uint4 *>(ap.part_o) : static_cast<uint4 *>(ap.out)) + off + (lane & 3);
-                    if (quad * 32 + (lane & ~3) + e >= nrows) dst[e] = nullptr;
-                }
+                tiles ^= (count & 1) << s;
+                if (count > 0) wait(&o_done[s], ((tiles >> s) & 1) ^ 1);
+                tc_fence_after();
                 // O is free for the next item once its last columns are in registers, before their stores
                 auto release = [&]() {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (it.sub[s].count > 0) mbar_arrive(&o_free[s]);
-                        if (pair && it.sub[0].count > 0) mbar_arrive(&o_free[0]);
-                    }
+                    if (lane == 0 && count > 0) mbar_arrive(&o_free[s]);
                 };
+                const bool any = f != 0.f;
                 if (!live) {
                     release();
-                } else if (pair || split) {
+                } else if (split) {
+                    // a part of its own: normalised fp32 rows, which the join reads once (nothing to
+                    // write where nothing was seen: its weight is 0)
+                    float4 *dst = reinterpret_cast<float4 *>(ap.part_o + slot * D);
 #pragma unroll 1
                     for (int q = 0; q < D; q += 32) {
                         uint32_t o[32];
                         tmem_ld32(tO + 128u * s + q, o);
-                        if (pair) {
-                            uint32_t x[32];
-                            tmem_ld32(tO + q, x);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint((any0 ? __uint_as_float(o[e]) * f0 : 0.f) + (any1 ? __uint_as_float(x[e]) * f1 : 0.f));
-                        } else {
-                            tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(any0 ? __uint_as_float(o[e]) * f0 : 0.f);
-                        }
+                        tc_wait_ld();
                         if (q + 32 == D) release();
-                        if (split) {
-                            tc_store_rows(tc_words(o), dst, q / 4);
-                            tc_store_rows(tc_words(o + 16), dst, q / 4 + 4);
-                        } else {
-                            uint32_t w[16];
+                        if (mine && any) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-                            tc_store_rows(tc_words(w), dst, q / 8);
+                            for (int e = 0; e < 32; e += 4)
+                                dst[(q + e) / 4] = make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                                                               __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
                         }
                     }
                 } else {
-                    // all columns first, as bf16
-                    uint32_t w[D / 2];
+                    uint4 *dst[4];
+                    const long long base = (it.b * p.os[0] + h * p.os[1] + tok * p.os[2]) / 8;
 #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const long long off = __shfl_sync(0xffffffffu, base, (lane & ~3) + e);
+                        dst[e] = static_cast<uint4 *>(ap.out) + off + (lane & 3);
+                        if (quad * 32 + (lane & ~3) + e >= nrows) dst[e] = nullptr;
+                    }
+#pragma unroll 1
                     for (int q = 0; q < D; q += 32) {
-                        uint32_t o[32];
+                        uint32_t o[32], w[16];
                         tmem_ld32(tO + 128u * s + q, o);
                         tc_wait_ld();
+                        if (q + 32 == D) release();
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            w[q / 2 + e] = any0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * f0, __uint_as_float(o[2 * e + 1]) * f0) : 0u;
+                            w[e] = any ? pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
+                        tc_store_rows(tc_words(w), dst, q / 8);
                     }
-                    release();
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) tc_store_rows(tc_words(w + 16 * q), dst, 4 * q);
                 }
             }
             __syncwarp();
