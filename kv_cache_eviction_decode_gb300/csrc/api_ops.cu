@@ -271,7 +271,7 @@ int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
             const int rc = make_maps(w.tc.maps[i], p.pr[i], p.G, p.Hkv, a->head_dim);
             if (rc) return rc;
         }
-        e = launch_attn_tc(w.tc, a->head_dim, kSMs, st);
+        e = launch_attn_tc(w.tc, a->head_dim, st);
     } else {
         e = launch_attn_f32(p, a->head_dim, w.few, st);
     }

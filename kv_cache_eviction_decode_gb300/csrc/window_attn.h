@@ -60,8 +60,8 @@ struct AttnTcParams {
 
 constexpr int kAttnTcRows = 128, kAttnTcKeys = 128;
 
-// bf16 attention on the tensor cores, at most one CTA on each of `sms` SMs.
-cudaError_t launch_attn_tc(const AttnTcParams &p, int head_dim, int sms, cudaStream_t st);
+// bf16 attention on the tensor cores.
+cudaError_t launch_attn_tc(const AttnTcParams &p, int head_dim, cudaStream_t st);
 // fp32 attention on the CUDA cores; `few`: tiles of 16 rows, else 64.
 cudaError_t launch_attn_f32(const AttnParams &p, int head_dim, bool few, cudaStream_t st);
 // Joins the slots: out = sum_s 2^(l_s - l) o_s, l = log2 sum_s 2^(l_s).

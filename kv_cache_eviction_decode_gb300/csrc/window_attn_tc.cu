@@ -21,6 +21,7 @@
 //
 // Warps 0-3, 4-7: softmax and output of sub 0, 1, the first 64 keys of each
 // tile; 8-11, 12-15: the other 64; 16: TMA; 17: MMA issue; 18: the items.
+#include <atomic>
 #include <cmath>
 
 #include "tc5_common.cuh"
@@ -882,16 +883,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     }
 }
 
-template <int D> cudaError_t launch_tc(const AttnTcParams &p, int sms, cudaStream_t st)
+template <int D> cudaError_t launch_tc(const AttnTcParams &p, cudaStream_t st)
 {
     constexpr int bytes = TcLayout<D>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // once a device: the shared-memory limit; and that the kernel has the registers that its split counts on
+    static std::atomic<uint64_t> ready[4] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static const int regs = [] {
+    if (dev > 255 || !(ready[dev >> 6].load() >> (dev & 63) & 1)) {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, attn_tc_kernel<D>) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;  // the split would wait for registers that are not there
+        e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, attn_tc_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+        if (dev <= 255) ready[dev >> 6].fetch_or(uint64_t{1} << (dev & 63));
+    }
     const int n = p.a.pr[0].n_items + (p.a.n_problems > 1 ? p.a.pr[1].n_items : 0);
     attn_tc_kernel<D><<<n, kTcThreads, bytes, st>>>(p);
     return cudaGetLastError();
@@ -899,9 +906,9 @@ template <int D> cudaError_t launch_tc(const AttnTcParams &p, int sms, cudaStrea
 
 }  // namespace
 
-cudaError_t launch_attn_tc(const AttnTcParams &p, int head_dim, int sms, cudaStream_t st)
+cudaError_t launch_attn_tc(const AttnTcParams &p, int head_dim, cudaStream_t st)
 {
-    return head_dim == 64 ? launch_tc<64>(p, sms, st) : launch_tc<128>(p, sms, st);
+    return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
 }
 
 }  // namespace kvevict

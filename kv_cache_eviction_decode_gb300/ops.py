@@ -7,12 +7,13 @@ waits for the GPU, and every call can be captured in a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import struct
 
 import torch
 
-from ._lib import BF16, F32, check, lib
+from ._lib import BF16, F32, OK, check, lib
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -20,6 +21,10 @@ _DT = {torch.float32: F32, torch.bfloat16: BF16}
 _ATTN = struct.Struct("@9if2q5P12q4PPNP")
 _SHARED = struct.Struct("@9if2q5P12q4PPNP2P5q")
 _ROT = struct.Struct("@8i2q4P12qP3qPf4x")
+
+# The handle of a device's current stream as a number (torch.cuda.current_stream
+# builds a Stream object first, ten times the cost), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -31,19 +36,21 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return dt
 
 
-def _like(t: torch.Tensor, q: torch.Tensor, dims: int, name: str, shape=None) -> torch.Tensor:
+def _like(t: torch.Tensor, q: torch.Tensor, dims: int, name: str, shape=None) -> None:
+    """t goes with q: its type, device, `dims` axes (or the whole shape), the last one contiguous."""
+    if t.dtype is q.dtype and t.get_device() == q.get_device() and (t.dim() == dims if shape is None else t.shape == shape) \
+            and (t.stride(-1) == 1 or t.shape[-1] <= 1):
+        return
     if t.dtype != q.dtype or t.device != q.device or t.dim() != dims or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: need a {q.dtype} tensor of {dims if shape is None else tuple(shape)} "
                          f"{'axes' if shape is None else ''} on {q.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    return t
+    raise ValueError(f"{name}: the last axis must be contiguous")
 
 
 def _ints(t, n: int, q: torch.Tensor, name: str) -> int:
     if t is None:
         return 0
-    if t.dtype != torch.int32 or t.device != q.device or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.get_device() != q.get_device() or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous int32 tensor of {n} on {q.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -88,18 +95,25 @@ def _error_word(t, q: torch.Tensor) -> int:
     return t.data_ptr()
 
 
-def _on(q: torch.Tensor, call):
-    """call(stream) with q's device current."""
-    dev = q.device.index
+def _call(name: str, q: torch.Tensor, args: bytes) -> None:
+    """The entry point on the current stream of q's device, with that device current."""
+    dev = q.get_device()
     if dev == torch.cuda.current_device():
-        return call(torch.cuda.current_stream(dev).cuda_stream)
-    with torch.cuda.device(dev):
-        return call(torch.cuda.current_stream(dev).cuda_stream)
+        rc = getattr(lib(), name)(args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib(), name)(args, _raw_stream(dev))
+    if rc != OK:
+        check(rc, name)
 
 
-def _need(name: str, args: bytes) -> int:
+@functools.lru_cache(maxsize=4096)
+def _need(name: str, fmt: struct.Struct, shape: tuple, packed: bool, *tail) -> int:
+    """Workspace bytes: a function of the shape alone."""
     n = ctypes.c_size_t(0)
-    check(getattr(lib(), name)(args, n), name)
+    starts = (16, 16) if packed else (0, 0)  # any addresses: only whether there are starts counts
+    name += "_workspace_bytes"
+    check(getattr(lib(), name)(fmt.pack(*shape, *(0,) * 17, *starts, 0, 0, 0, 0, 0, *tail), n), name)
     return n.value
 
 
@@ -156,15 +170,12 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sin
         lse_shape = q.shape[:3]
     out, lse = _outputs(q, out, lse, return_lse, lse_shape)
     os = (0, out.stride(1), out.stride(0)) if packed else out.stride()[:3]
-    head = (dt, d, Hq, Hkv, B, n_sink, min(window, 2**31 - 1), max_q, max_k, _scale(scale), N, M, q.data_ptr(), k.data_ptr(),
-            v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), *qs, *ks, *vs, *os,
-            _ints(q_starts, B + 1, q, "q_starts"), _ints(k_starts, B + 1, q, "k_starts"),
-            _ints(q_lens, B, q, "q_lens"), _ints(kv_lens, B, q, "kv_lens"))
-    err = _error_word(error_word, q)
-    need = _need("kvevict_window_attention_workspace_bytes", _ATTN.pack(*head, 0, 0, err))
-    workspace, wp, wn = _workspace(workspace, need, q)
-    args = _ATTN.pack(*head, wp, wn, err)
-    check(_on(q, lambda st: lib().kvevict_window_attention(args, st)), "kvevict_window_attention")
+    shape = (dt, d, Hq, Hkv, B, n_sink, min(window, 2**31 - 1), max_q, max_k, _scale(scale), N, M)
+    workspace, wp, wn = _workspace(workspace, _need("kvevict_window_attention", _ATTN, shape, packed), q)
+    _call("kvevict_window_attention", q, _ATTN.pack(
+        *shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        *qs, *ks, *vs, *os, _ints(q_starts, B + 1, q, "q_starts"), _ints(k_starts, B + 1, q, "k_starts"),
+        _ints(q_lens, B, q, "q_lens"), _ints(kv_lens, B, q, "kv_lens"), wp, wn, _error_word(error_word, q)))
     return out if lse is None else (out, lse)
 
 
@@ -188,15 +199,15 @@ def shared_prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: t
     if k.shape[0] != B or k.shape[3] != d or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != d:
         raise ValueError(f"k, k_prefix: need [{B}][Hkv][M][{d}] and [Hkv][P][{d}], got {tuple(k.shape)} and {tuple(k_prefix.shape)}")
     out, lse = _outputs(q, out, lse, return_lse, q.shape[:2])
-    head = (dt, d, Hq, Hkv, B, 0, 0, 0, 0, _scale(scale), 1, M, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-            0 if lse is None else lse.data_ptr(), q.stride(0), q.stride(1), 0, *k.stride()[:3], *v.stride()[:3],
-            out.stride(0), out.stride(1), 0, 0, 0, 0, _ints(kv_lens, B, q, "kv_lens"))
-    tail = (_error_word(error_word, q), k_prefix.data_ptr(), v_prefix.data_ptr(), *k_prefix.stride()[:2],
-            *v_prefix.stride()[:2], k_prefix.shape[1])
-    need = _need("kvevict_shared_prefix_attention_workspace_bytes", _SHARED.pack(*head, 0, 0, *tail))
+    P = k_prefix.shape[1]
+    shape = (dt, d, Hq, Hkv, B, 0, 0, 0, 0, _scale(scale), 1, M)
+    need = _need("kvevict_shared_prefix_attention", _SHARED, shape, False, 0, 0, 0, 0, 0, 0, P)
     workspace, wp, wn = _workspace(workspace, need, q)
-    args = _SHARED.pack(*head, wp, wn, *tail)
-    check(_on(q, lambda st: lib().kvevict_shared_prefix_attention(args, st)), "kvevict_shared_prefix_attention")
+    _call("kvevict_shared_prefix_attention", q, _SHARED.pack(
+        *shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        q.stride(0), q.stride(1), 0, *k.stride()[:3], *v.stride()[:3], out.stride(0), out.stride(1), 0, 0, 0, 0,
+        _ints(kv_lens, B, q, "kv_lens"), wp, wn, _error_word(error_word, q), k_prefix.data_ptr(), v_prefix.data_ptr(),
+        *k_prefix.stride()[:2], *v_prefix.stride()[:2], P))
     return out if lse is None else (out, lse)
 
 
@@ -281,12 +292,12 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
         kp, kop, kst, kost = k.data_ptr(), k_out.data_ptr(), st(k), st(k_out)
     else:
         Hk, kp, kop, kst, kost = 0, 0, 0, (0, 0, 0), (0, 0, 0)
-    if inv_freq.dtype != torch.float64 or inv_freq.device != q.device or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq: need a contiguous float64 vector on {q.device}")
     if isinstance(positions, int):
         pp, p64, ps, start = 0, 0, (0, 0), positions
     else:
-        if positions.device != q.device or positions.dtype not in (torch.int32, torch.int64):
+        if positions.get_device() != q.get_device() or positions.dtype not in (torch.int32, torch.int64):
             raise ValueError(f"positions: need int32 or int64 on {q.device}, got {positions.dtype} on {positions.device}")
         if positions.shape == (N,):
             ps = (0, positions.stride(0))
@@ -295,7 +306,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
         else:
             raise ValueError(f"positions: {tuple(positions.shape)} does not go with q {tuple(q.shape)}")
         pp, p64, start = positions.data_ptr(), int(positions.dtype == torch.int64), 0
-    args = _ROT.pack(dt, d, 2 * inv_freq.shape[0], int(interleaved), int(inverse), p64, Hq, Hk, B, N, q.data_ptr(), kp,
-                     q_out.data_ptr(), kop, *st(q), *st(q_out), *kst, *kost, pp, *ps, start, inv_freq.data_ptr(), scale)
-    check(_on(q, lambda stream: lib().kvevict_rotary(args, stream)), "kvevict_rotary")
+    _call("kvevict_rotary", q, _ROT.pack(
+        dt, d, 2 * inv_freq.shape[0], int(interleaved), int(inverse), p64, Hq, Hk, B, N, q.data_ptr(), kp, q_out.data_ptr(), kop,
+        *st(q), *st(q_out), *kst, *kost, pp, *ps, start, inv_freq.data_ptr(), scale))
     return q_out if k is None else (q_out, k_out)
