@@ -60,20 +60,34 @@ int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens, int key
 }
 
 // Cuts a problem into items: tiles of `rows` rows, and parts of the key range
-// where the tiles alone would leave SMs idle. Four items an SM keep the end of
-// the launch short (a quarter of an item's time idle on average), two key tiles
-// a part at least pay for the part's own output.
-void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int64_t max_k, int64_t other_items, bool may_split)
+// where the tiles alone would leave SMs idle. An SM works on one item after
+// another (two on the CUDA cores side by side); with `tiles` key tiles an item,
+// p parts and items * p over the SMs in w waves, the launch takes about
+// w * (tiles / p + kItemCost): an item's start and end, and its part's output
+// and join, cost as much as kItemCost key tiles (on the tensor cores 4.9 us for
+// an item of 5.7 tiles that would stream in 2.4: 32 sequences, 8 KV heads, window
+// 2044). `other`: key tiles of a problem in the same launch.
+constexpr double kItemCost = 1.8;
+
+void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int64_t max_k, double other)
 {
     const int per = rows / G;
     p.q_tiles = (p.max_q + per - 1) / per;
     const int64_t items = static_cast<int64_t>(p.batch) * Hkv * p.q_tiles;
     p.splits = 1;
     p.pair = 0;
-    if (may_split && items + other_items < 2 * kSMs) {
-        const int64_t tiles = key_tiles(max_k, p.n_sink, p.causal ? p.window : 0, std::min(per, p.max_q), keys);
-        const int64_t want = (4 * kSMs + items - 1) / std::max<int64_t>(1, items);
-        p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, (tiles + 1) / 2, kMaxParts})));
+    if (items == 0 || items >= 4 * kSMs) return;
+    const int64_t tiles = key_tiles(max_k, p.n_sink, p.causal ? p.window : 0, std::min(per, p.max_q), keys);
+    double best = 0;
+    for (int64_t s = 1; s <= std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (tiles + 1) / 2)); ++s) {
+        const double part = static_cast<double>((tiles + s - 1) / s) + kItemCost;
+        // alone, in whole waves; beside another problem's items the SMs are shared evenly
+        const double load = other > 0 ? std::max(part, (static_cast<double>(items * s) * part + other) / kSMs)
+                                      : static_cast<double>((items * s + kSMs - 1) / kSMs) * part;
+        if (s == 1 || load < best * 0.97) {
+            best = load;
+            p.splits = static_cast<int>(s);
+        }
     }
 }
 
@@ -86,22 +100,27 @@ struct Plan {
     size_t bytes = 0;  // workspace
 };
 
-// fp32: tiles of 16 rows where every unit has that few, else of 64.
-bool few_rows(int G, int64_t max_q) { return G <= kAttnF32FewRows && G * max_q <= kAttnF32FewRows; }
+// fp32: tiles of 16 rows where every unit has that few, or where tiles of 64
+// would leave SMs idle (8 heads x 256 rows: 23 us with 32 tiles of 64); else of 64.
+bool few_rows(int G, int64_t units, int64_t max_q)
+{
+    const int64_t per = kAttnF32Rows / G;
+    return G <= kAttnF32FewRows && (G * max_q <= kAttnF32FewRows || units * ((max_q + per - 1) / per) < kSMs);
+}
 
 // Cuts a problem for the kernel of the plan's type. The tensor cores take two
 // tiles of 128 rows an item, or one (with alternate key tiles) where the rows
 // fit one: then only parts of two key tiles or more make sense.
-void cut_for(Plan &w, AttnProblem &q, int64_t max_k)
+void cut_for(Plan &w, AttnProblem &q, int64_t max_k, double other = 0)
 {
     const int G = w.p.G;
     if (w.tensor) {
         const bool pair = q.max_q <= kAttnTcRows / G;
-        cut(q, G, w.p.Hkv, (pair ? 1 : 2) * (kAttnTcRows / G) * G, kAttnTcKeys, max_k, 0, true);
+        cut(q, G, w.p.Hkv, (pair ? 1 : 2) * (kAttnTcRows / G) * G, kAttnTcKeys, max_k, other);
         // (one key tile at most: nothing to share, the second tile stays without rows)
         q.pair = pair && key_tiles(max_k, q.n_sink, q.causal ? q.window : 0, q.max_q, kAttnTcKeys) > 1;
     } else {
-        cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows, kAttnF32Keys, max_k, 0, true);
+        cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows, kAttnF32Keys, max_k, other);
     }
 }
 
@@ -153,7 +172,7 @@ int plan_window(const kvevict_attention_args *a, Plan &w)
         q.rs[0] = p.Hq * N; q.rs[1] = N; q.rs[2] = 1;
     }
     w.tensor = a->dtype == KVEVICT_BF16;
-    w.few = few_rows(p.G, q.max_q);
+    w.few = few_rows(p.G, static_cast<int64_t>(q.batch) * p.Hkv, q.max_q);
     cut_for(w, q, max_k);
     return finish(w, a->head_dim);
 }
@@ -180,9 +199,12 @@ int plan_shared(const kvevict_shared_prefix_args *s, Plan &w)
     y.k_rows = static_cast<int>(a->k_rows);
     y.rs[0] = p.Hq; y.rs[1] = 1; y.rs[2] = 0;
     w.tensor = a->dtype == KVEVICT_BF16;
-    w.few = few_rows(p.G, a->batch);
-    cut_for(w, x, x.k_rows);
-    cut_for(w, y, y.k_rows);
+    w.few = few_rows(p.G, p.Hkv, a->batch);
+    const double keys = w.tensor ? kAttnTcKeys : kAttnF32Keys;
+    const double yt = static_cast<double>(a->batch) * p.Hkv * std::ceil(y.k_rows / keys);
+    const double xt = p.Hkv * std::ceil(x.k_rows / keys);
+    cut_for(w, x, x.k_rows, yt);
+    cut_for(w, y, y.k_rows, xt);
     return finish(w, a->head_dim);
 }
 

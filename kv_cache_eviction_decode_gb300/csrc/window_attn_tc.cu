@@ -377,13 +377,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     uint64_t *i_full = o_free + 2;              // [kItemSlots] an item is posted
     uint64_t *i_empty = i_full + kItemSlots;    // [kItemSlots] every role is done with it
     uint64_t *fin = i_empty + kItemSlots;       // [2] an MMA warp's last operation completed
-    uint64_t *stolen = fin + 2;                 // the answer about another block is there
+    uint64_t *taken = fin + 2;                  // the TMA warp has taken up an item
+    uint64_t *stolen = taken + 1;               // the answer about another block is there
     uint32_t *tslot = reinterpret_cast<uint32_t *>(stolen + 1);
     TcItem *items = reinterpret_cast<TcItem *>(sm + L::kOffItem);
     TcStep *steps = reinterpret_cast<TcStep *>(sm + L::kOffStep);  // [2]
     uint8_t *steal_slot = sm + L::kOffStep + 16;
     float *xl = reinterpret_cast<float *>(sm + L::kOffX);
-    static_assert((17 + 2 * L::kStages + 2 * kItemSlots + 2) * 8 + 4 <= 384, "barrier area");
+    static_assert((18 + 2 * L::kStages + 2 * kItemSlots + 2) * 8 + 4 <= 384, "barrier area");
     static_assert(kItemSlots * sizeof(TcItem) <= 544 && L::kOffStep % 16 == 0, "item area");
 
     const int tid = threadIdx.x, lane = tid & 31;
@@ -408,6 +409,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(&i_full[s], 1);
             mbar_init(&i_empty[s], 3 + kSoftmaxWarps + 4);  // TMA, MMA, softmax, output warps
         }
+        mbar_init(taken, 1);
         mbar_init(stolen, 1);
         mbar_fence_init();
     }
@@ -448,18 +450,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 };
                 for (int i = 0;; ++i) {
                     const int slot = i % kItemSlots;
-                    if (i >= kItemSlots && !mbar_wait(&i_empty[slot], ((i / kItemSlots) - 1) & 1)) {
+                    // a block is taken over when the loads of the item before it begin: what waits here
+                    // could be running elsewhere
+                    if ((i >= kItemSlots && !mbar_wait(&i_empty[slot], ((i / kItemSlots) - 1) & 1)) ||
+                        (i > 0 && !mbar_wait(taken, (i - 1) & 1))) {
                         // a role gave up: the blocks that have not started are taken and dropped, so that
                         // the launch ends with the ones that run
                         attn_flag(ap.err, KVEVICT_DEV_WAIT_TIMEOUT);
                         while (idx >= 0) idx = next();
                         break;
                     }
+                    if (i > 0) idx = next();
+                    // (an item whose rows lie behind its sequence's last has nothing to do)
+                    while (idx >= 0) {
+                        tc_make_item(tp, idx, items[slot]);
+                        if (items[slot].bad) attn_flag(ap.err, KVEVICT_DEV_BAD_LENGTH);
+                        if (items[slot].sub[0].nt > 0) break;
+                        idx = next();
+                    }
                     if (idx < 0) items[slot].prob = -1;
-                    else tc_make_item(tp, idx, items[slot]);
                     mbar_arrive(&i_full[slot]);
                     if (idx < 0) break;
-                    idx = next();
                 }
             }
         } else if (warp == kTmaWarp) {
@@ -472,6 +483,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 for (int i = 0; ok; ++i) {
                     const TcItem *ip = take(i, ok);
                     if (!ip) break;
+                    mbar_arrive(taken);
                     const TcItem &it = *ip;
                     const AttnTcMaps &mp = tp.maps[it.prob];
                     const int qb = ap.pr[it.prob].q_starts ? 0 : it.b;
@@ -669,7 +681,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             const TcItem &it = *ip;
             const AttnProblem &p = ap.pr[it.prob];
-            if (it.bad && tid == 0) attn_flag(ap.err, KVEVICT_DEV_BAD_LENGTH);
             const int n_sink = p.n_sink;
             // the keys this row sees: j <= top, and j < n_sink or j >= low
             int top = it.m - 1, low = 0;
