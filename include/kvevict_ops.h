@@ -167,6 +167,45 @@ typedef struct {
 
 int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream);
 
+/*
+ * With a handle: the prompt of an empty layer, attended and appended in one
+ * call. out (and lse, where not NULL) get the prompt's attention under the
+ * tokens that the policy keeps in view -- KVEVICT_SINK_WINDOW: the first n_sink
+ * and the newest n_recent + 1, which is what kvevict_decode_step would have
+ * attended to token by token; the other policies: every earlier token -- by
+ * kvevict_window_attention; then the prompt enters the cache as
+ * kvevict_prefill(h, layer, K, V, n_tokens) puts it there.
+ *   Q, out: device, [batch][n_q_heads][n_tokens][head_dim]; K, V: device,
+ *           [batch][n_kv_heads][n_tokens][head_dim]; lse: fp32
+ *           [batch][n_q_heads][n_tokens] or NULL;
+ *   workspace: as kvevict_prefill_attend_workspace_bytes() says (NULL where 0).
+ * On the handle's stream; error bits in the handle's error word. INVALID_ARG
+ * for n_tokens outside 1 .. 2^30 - 1, null or misaligned pointers or a short
+ * workspace; STATE if the layer is out of range, already holds tokens or has
+ * decoded; CAPACITY for a KVEVICT_RANDOM prompt beyond max_prompt. */
+int kvevict_prefill_attend_workspace_bytes(kvevict_t h, int n_tokens, size_t *bytes);
+int kvevict_prefill_attend(kvevict_t h, int layer, const void *Q, const void *K, const void *V, int n_tokens, void *out,
+                           float *lse, void *workspace, size_t workspace_bytes);
+
+/*
+ * kvevict_decode_step over the layer's cache and, in front of it, a prefix that
+ * all sequences share: one softmax over prefix, retained tokens and the new
+ * token. The cache does what the step always does (it appends, evicts and
+ * counts positions as if there were no prefix); only the attention is joined
+ * with the prefix's, three launches in all. For the policies that keep no
+ * scores (KVEVICT_SINK_WINDOW, KVEVICT_RANDOM): scores would be attention
+ * probabilities, which the prefix takes a share of.
+ *   q, k_new, v_new, out: as kvevict_decode_step; k_prefix, v_prefix: device,
+ *   [n_kv_heads][prefix_rows][head_dim], NULL where prefix_rows is 0;
+ *   workspace: kvevict_decode_step_shared_workspace_bytes(), 256-byte aligned;
+ *   calls that may overlap on the GPU need one each.
+ * INVALID_ARG for other policies, a negative prefix_rows, null or misaligned
+ * pointers or a short workspace; STATE as kvevict_decode_step. */
+int kvevict_decode_step_shared_workspace_bytes(kvevict_t h, int prefix_rows, size_t *bytes);
+int kvevict_decode_step_shared(kvevict_t h, int layer, const void *q, const void *k_new, const void *v_new,
+                               const void *k_prefix, const void *v_prefix, int prefix_rows, void *out, void *workspace,
+                               size_t workspace_bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -98,6 +98,13 @@ def lib() -> ctypes.CDLL:
             for n in ("kvevict_window_attention_workspace_bytes", "kvevict_shared_prefix_attention_workspace_bytes"):
                 getattr(L, n).argtypes = [ctypes.c_char_p, ctypes.POINTER(SZ)]
                 getattr(L, n).restype = I
+            L.kvevict_prefill_attend_workspace_bytes.argtypes = [P, I, ctypes.POINTER(SZ)]
+            L.kvevict_prefill_attend.argtypes = [P, I, P, P, P, I, P, P, P, SZ]
+            L.kvevict_decode_step_shared_workspace_bytes.argtypes = [P, I, ctypes.POINTER(SZ)]
+            L.kvevict_decode_step_shared.argtypes = [P, I, P, P, P, P, P, I, P, P, SZ]
+            for n in ("kvevict_prefill_attend_workspace_bytes", "kvevict_prefill_attend",
+                      "kvevict_decode_step_shared_workspace_bytes", "kvevict_decode_step_shared"):
+                getattr(L, n).restype = I
             L.kvevict_destroy.argtypes = [P]
             L.kvevict_destroy.restype = None
             for n in ("kvevict_state_bytes", "kvevict_create", "kvevict_prefill", "kvevict_prefill_scored_workspace_bytes",

@@ -9,7 +9,7 @@ import ctypes
 
 import torch
 
-from . import _lib
+from . import _lib, ops
 from ._lib import BF16, F32, H2O, RANDOM, SINK_WINDOW, Config, Stats, check, lib
 
 _DT = {F32: torch.float32, BF16: torch.bfloat16}
@@ -142,6 +142,82 @@ class KVEvictCache:
         off = (self.B * self.Hq * ps * 4 + 255) // 256 * 256
         raw = workspace.view(torch.uint8).reshape(-1)[off:off + self.B * self.Hq * n * 4]
         return raw.view(torch.float32).view(self.B, self.Hq, n)
+
+    def _workspace(self, workspace: torch.Tensor | None, need: int):
+        """Scratch for a call on the handle's stream: (keep alive, address, bytes)."""
+        if need == 0:
+            return None, None, 0
+        if workspace is None:
+            with torch.cuda.stream(self.stream):  # so that the allocator hands it on in this stream's order
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        size = workspace.numel() * workspace.element_size()
+        if workspace.device != self.device or not workspace.is_contiguous() or size < need:
+            raise ValueError(f"workspace: need {need} contiguous bytes on {self.device}")
+        return workspace, _ptr(workspace), size
+
+    def prefill_attend(self, layer: int, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None, return_lse: bool = False,
+                       workspace: torch.Tensor | None = None):
+        """The prompt of an empty layer, Q [B][Hq][P][d], K/V [B][Hkv][P][d]: its
+        attention under the tokens the policy keeps in view (SINK_WINDOW: sinks
+        and the newest n_recent + 1; else every earlier one), then prefill().
+        Returns out (as Q), or (out, lse [B][Hq][P] fp32)."""
+        n = K.shape[2]
+        self._dev(Q, (self.B, self.Hq, n, self.D), "Q")
+        self._dev(K, (self.B, self.Hkv, n, self.D), "K")
+        self._dev(V, (self.B, self.Hkv, n, self.D), "V")
+        if out is None:
+            out = torch.empty_like(Q)
+        self._dev(out, Q.shape, "out")
+        if lse is None and return_lse:
+            lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=self.device)
+        if lse is not None:
+            self._dev(lse, Q.shape[:3], "lse", torch.float32)
+        need = ctypes.c_size_t()
+        check(self._L.kvevict_prefill_attend_workspace_bytes(self.h, n, ctypes.byref(need)),
+              "kvevict_prefill_attend_workspace_bytes")
+        keep, wp, wn = self._workspace(workspace, need.value)
+        check(self._L.kvevict_prefill_attend(self.h, layer, _ptr(Q), _ptr(K), _ptr(V), n, _ptr(out),
+                                             None if lse is None else _ptr(lse), wp, wn), "kvevict_prefill_attend")
+        return out if lse is None else (out, lse)
+
+    def rotate(self, layer: int, q: torch.Tensor, k: torch.Tensor, inv_freq: torch.Tensor, *, offset: int = 0,
+               interleaved: bool = False, scale: float = 1.0):
+        """Rotary positions in place, at the layer's next positions (+ offset, for
+        instance a shared prefix's length): q [B][Hq][d] and k [B][Hkv][d] of the
+        next decode step, or [B][Hq][P][d] and [B][Hkv][P][d] of a prompt (chunk)
+        before it is appended. inv_freq, scale: rotary_frequencies(). Returns (q, k)."""
+        prompt, steps, _ = self.layer_state(layer)
+        q4, k4 = (t.unsqueeze(2) if t.dim() == 3 else t for t in (q, k))
+        n = q4.shape[2] if q4.dim() == 4 else 0
+        self._dev(q, (self.B, self.Hq, n, self.D) if q.dim() == 4 else (self.B, self.Hq, self.D), "q")
+        self._dev(k, (self.B, self.Hkv, n, self.D) if k.dim() == 4 else (self.B, self.Hkv, self.D), "k")
+        with torch.cuda.stream(self.stream):
+            ops.rotary(q4, k4, offset + prompt + steps, inv_freq, interleaved=interleaved, scale=scale, q_out=q4, k_out=k4)
+        return q, k
+
+    def decode_step_shared(self, layer: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                           k_prefix: torch.Tensor, v_prefix: torch.Tensor, out: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None) -> torch.Tensor:
+        """decode_step with a prefix that all sequences share in front of the cache,
+        k_prefix and v_prefix [Hkv][P][d]: one softmax over prefix, retained tokens
+        and the new one (SINK_WINDOW and RANDOM)."""
+        P = k_prefix.shape[1]
+        self._dev(q, (self.B, self.Hq, self.D), "q")
+        self._dev(k_new, (self.B, self.Hkv, self.D), "k_new")
+        self._dev(v_new, (self.B, self.Hkv, self.D), "v_new")
+        self._dev(k_prefix, (self.Hkv, P, self.D), "k_prefix")
+        self._dev(v_prefix, (self.Hkv, P, self.D), "v_prefix")
+        if out is None:
+            out = torch.empty((self.B, self.Hq, self.D), dtype=self.dtype, device=self.device)
+        self._dev(out, (self.B, self.Hq, self.D), "out")
+        need = ctypes.c_size_t()
+        check(self._L.kvevict_decode_step_shared_workspace_bytes(self.h, P, ctypes.byref(need)),
+              "kvevict_decode_step_shared_workspace_bytes")
+        keep, wp, wn = self._workspace(workspace, need.value)
+        check(self._L.kvevict_decode_step_shared(self.h, layer, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_prefix),
+                                                 _ptr(v_prefix), P, _ptr(out), wp, wn), "kvevict_decode_step_shared")
+        return out
 
     def decode_step(self, layer: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                     out: torch.Tensor | None = None) -> torch.Tensor:

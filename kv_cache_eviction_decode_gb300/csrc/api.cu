@@ -12,6 +12,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -475,7 +476,9 @@ int pick_clusters(const kvevict_handle *h, int S, const DecodeKernelInfo &ki, si
     return KVEVICT_OK;
 }
 
-int launch_decode(kvevict_handle *h, int layer, const void *q, const void *kn, const void *vn, void *out)
+// part_o, part_l: the step's output goes there as a part for a join (fp32, with its log2 normalisers) instead of to out.
+int launch_decode(kvevict_handle *h, int layer, const void *q, const void *kn, const void *vn, void *out,
+                  float *part_o = nullptr, float *part_l = nullptr)
 {
     const kvevict_config &c = h->cfg;
     const Layout &L = h->L;
@@ -483,6 +486,7 @@ int launch_decode(kvevict_handle *h, int layer, const void *q, const void *kn, c
 
     DecodeParams P{};
     P.q = q; P.k_new = kn; P.v_new = vn; P.out = out;
+    P.part_o = part_o; P.part_l = part_l;
     P.kc = h->state + L.off_k + layer * L.kv_layer_bytes;
     P.vc = h->state + L.off_v + layer * L.kv_layer_bytes;
     P.pos = at<int32_t>(h, L.off_pos) + layer * L.layer_pslots;
@@ -1208,6 +1212,130 @@ int kvevict_decode_step(kvevict_t h, int layer, const void *q, const void *k_new
     if (h->layers[layer].prompt_len + static_cast<long long>(h->layers[layer].t) >= (1LL << 31) - 1)
         return KVEVICT_ERR_STATE;
     return launch_decode(h, layer, q, k_new, v_new, out);
+}
+
+namespace {
+
+// The prompt's attention as kvevict_window_attention takes it: the tokens a
+// SINK_WINDOW cache keeps, every earlier one for the other policies.
+kvevict_attention_args prompt_args(const kvevict_handle *h, const void *Q, const void *K, const void *V, int n, void *out,
+                                   float *lse, void *workspace, size_t bytes)
+{
+    const kvevict_config &c = h->cfg;
+    kvevict_attention_args a{};
+    a.dtype = c.dtype;
+    a.head_dim = c.head_dim;
+    a.n_q_heads = c.n_q_heads;
+    a.n_kv_heads = c.n_kv_heads;
+    a.batch = c.batch;
+    if (c.policy == KVEVICT_SINK_WINDOW) {
+        a.n_sink = c.n_sink;
+        a.window = c.n_recent < INT_MAX ? c.n_recent + 1 : 0;
+    }
+    a.q_rows = a.k_rows = n;
+    a.q = Q; a.k = K; a.v = V;
+    a.out = out;
+    a.lse = lse;
+    const int64_t d = c.head_dim, per = static_cast<int64_t>(n) * d;
+    const int64_t qs[3] = {c.n_q_heads * per, per, d}, ks[3] = {c.n_kv_heads * per, per, d};
+    for (int i = 0; i < 3; ++i) {
+        a.q_stride[i] = a.out_stride[i] = qs[i];
+        a.k_stride[i] = a.v_stride[i] = ks[i];
+    }
+    a.workspace = workspace;
+    a.workspace_bytes = bytes;
+    a.error_word = reinterpret_cast<uint32_t *>(h->state + h->L.off_err);
+    return a;
+}
+
+// Every check of kvevict_prefill_attend but those on its tensors.
+int prompt_check(const kvevict_handle *h, int layer, int n)
+{
+    if (!h) return KVEVICT_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= h->cfg.n_layers) return KVEVICT_ERR_STATE;
+    if (n < 1 || n >= (1 << 30)) return KVEVICT_ERR_INVALID_ARG;
+    const LayerState &ls = h->layers[layer];
+    if (ls.prompt_len != 0 || ls.t != 0) return KVEVICT_ERR_STATE;
+    if (h->cfg.policy == KVEVICT_RANDOM && n > h->cfg.max_prompt) return KVEVICT_ERR_CAPACITY;
+    return KVEVICT_OK;
+}
+
+kvevict_shared_prefix_args prefix_args(const kvevict_handle *h, const void *q, const void *kp, const void *vp, int rows,
+                                       void *out, void *workspace, size_t bytes)
+{
+    const kvevict_config &c = h->cfg;
+    kvevict_shared_prefix_args s{};
+    kvevict_attention_args &a = s.a;
+    a.dtype = c.dtype;
+    a.head_dim = c.head_dim;
+    a.n_q_heads = c.n_q_heads;
+    a.n_kv_heads = c.n_kv_heads;
+    a.batch = c.batch;
+    a.q_rows = 1;
+    a.q = q;
+    a.out = out;
+    const int64_t d = c.head_dim;
+    a.q_stride[0] = a.out_stride[0] = c.n_q_heads * d;
+    a.q_stride[1] = a.out_stride[1] = d;
+    a.workspace = workspace;
+    a.workspace_bytes = bytes;
+    a.error_word = reinterpret_cast<uint32_t *>(h->state + h->L.off_err);
+    s.k_prefix = kp;
+    s.v_prefix = vp;
+    s.prefix_rows = rows;
+    s.k_prefix_stride[0] = s.v_prefix_stride[0] = rows * d;
+    s.k_prefix_stride[1] = s.v_prefix_stride[1] = d;
+    return s;
+}
+
+// The policies whose step does not depend on the attention's normaliser.
+bool prefix_policy(const kvevict_handle *h) { return !scored(h->cfg.policy); }
+
+}  // namespace
+
+int kvevict_prefill_attend_workspace_bytes(kvevict_t h, int n_tokens, size_t *bytes)
+{
+    if (!h || !bytes || n_tokens < 1 || n_tokens >= (1 << 30)) return KVEVICT_ERR_INVALID_ARG;
+    const kvevict_attention_args a = prompt_args(h, nullptr, nullptr, nullptr, n_tokens, nullptr, nullptr, nullptr, 0);
+    return kvevict_window_attention_workspace_bytes(&a, bytes);
+}
+
+int kvevict_prefill_attend(kvevict_t h, int layer, const void *Q, const void *K, const void *V, int n_tokens, void *out,
+                           float *lse, void *workspace, size_t workspace_bytes)
+{
+    NvtxRange nvtx("kvevict_prefill_attend");
+    int rc = prompt_check(h, layer, n_tokens);
+    if (rc) return rc;
+    const kvevict_attention_args a = prompt_args(h, Q, K, V, n_tokens, out, lse, workspace, workspace_bytes);
+    rc = kvevict_window_attention(&a, h->stream);
+    return rc ? rc : kvevict_prefill(h, layer, K, V, n_tokens);
+}
+
+int kvevict_decode_step_shared_workspace_bytes(kvevict_t h, int prefix_rows, size_t *bytes)
+{
+    if (!h || !bytes || prefix_rows < 0 || !prefix_policy(h)) return KVEVICT_ERR_INVALID_ARG;
+    const kvevict_shared_prefix_args s = prefix_args(h, nullptr, nullptr, nullptr, prefix_rows, nullptr, nullptr, 0);
+    return kvevict_prefix_bytes(&s, bytes);
+}
+
+int kvevict_decode_step_shared(kvevict_t h, int layer, const void *q, const void *k_new, const void *v_new,
+                               const void *k_prefix, const void *v_prefix, int prefix_rows, void *out, void *workspace,
+                               size_t workspace_bytes)
+{
+    NvtxRange nvtx("kvevict_decode_step_shared");
+    if (!h) return KVEVICT_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= h->cfg.n_layers) return KVEVICT_ERR_STATE;
+    if (!prefix_policy(h) || prefix_rows < 0) return KVEVICT_ERR_INVALID_ARG;
+    if (!q || !k_new || !v_new || !out) return KVEVICT_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out)) return KVEVICT_ERR_INVALID_ARG;
+    if (h->layers[layer].prompt_len + static_cast<long long>(h->layers[layer].t) >= (1LL << 31) - 1)
+        return KVEVICT_ERR_STATE;
+    const kvevict_shared_prefix_args s = prefix_args(h, q, k_prefix, v_prefix, prefix_rows, out, workspace, workspace_bytes);
+    float *part_o = nullptr, *part_l = nullptr;
+    int rc = kvevict_prefix_part(&s, &part_o, &part_l);
+    if (rc) return rc;
+    rc = launch_decode(h, layer, q, k_new, v_new, out, part_o, part_l);
+    return rc ? rc : kvevict_prefix_run(&s, h->stream);
 }
 
 int kvevict_sync(kvevict_t h)

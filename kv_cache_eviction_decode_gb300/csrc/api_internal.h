@@ -2,7 +2,7 @@
 // library (not part of the C ABI: hidden from the shared library's exports).
 #pragma once
 
-#include "kvevict.h"
+#include "kvevict_ops.h"
 
 #define KVEVICT_INTERNAL __attribute__((visibility("hidden")))
 
@@ -23,5 +23,15 @@ KVEVICT_INTERNAL int kvevict_prefill_scored_check(kvevict_t h, int layer, const 
 // `device`, looked up once per device and cached; the lookup makes `device`
 // current for its duration and restores the caller's device.
 KVEVICT_INTERNAL int kvevict_static_scratch_address(int device, void **out);
+
+// Shared-prefix attention whose suffix part the caller computes: `s` as for
+// kvevict_shared_prefix_attention with k_rows = 0. _bytes: the workspace;
+// _part: where in it the caller's part goes, fp32 outputs [batch][n_q_heads][d]
+// and log2 normalisers [batch][n_q_heads] (every check of the call is made
+// here); _run: the prefix's part and the join, after the caller's part on the
+// same stream.
+KVEVICT_INTERNAL int kvevict_prefix_bytes(const kvevict_shared_prefix_args *s, size_t *bytes);
+KVEVICT_INTERNAL int kvevict_prefix_part(const kvevict_shared_prefix_args *s, float **part_o, float **part_l);
+KVEVICT_INTERNAL int kvevict_prefix_run(const kvevict_shared_prefix_args *s, void *cuda_stream);
 
 }  // extern "C"

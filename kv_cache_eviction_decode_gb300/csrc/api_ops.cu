@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "api_internal.h"
 #include "kvevict_ops.h"
 #include "window_attn.h"
 
@@ -177,7 +178,8 @@ int plan_window(const kvevict_attention_args *a, Plan &w)
     return finish(w, a->head_dim);
 }
 
-int plan_shared(const kvevict_shared_prefix_args *s, Plan &w)
+// `outside`: the suffixes' part is one that the caller writes.
+int plan_shared(const kvevict_shared_prefix_args *s, Plan &w, bool outside)
 {
     const kvevict_attention_args *a = &s->a;
     AttnParams &p = w.p;
@@ -201,10 +203,11 @@ int plan_shared(const kvevict_shared_prefix_args *s, Plan &w)
     w.tensor = a->dtype == KVEVICT_BF16;
     w.few = few_rows(p.G, p.Hkv, a->batch);
     const double keys = w.tensor ? kAttnTcKeys : kAttnF32Keys;
-    const double yt = static_cast<double>(a->batch) * p.Hkv * std::ceil(y.k_rows / keys);
+    const double yt = outside ? 0 : static_cast<double>(a->batch) * p.Hkv * std::ceil(y.k_rows / keys);
     const double xt = p.Hkv * std::ceil(x.k_rows / keys);
     cut_for(w, x, x.k_rows, yt);
-    cut_for(w, y, y.k_rows, xt);
+    if (outside) y.splits = 1;  // no items
+    else cut_for(w, y, y.k_rows, xt);
     return finish(w, a->head_dim);
 }
 
@@ -272,7 +275,7 @@ int make_maps(AttnTcMaps &t, const AttnProblem &p, int G, int Hkv, int head_dim)
     return rc;
 }
 
-int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
+int bind_workspace(const kvevict_attention_args *a, Plan &w)
 {
     AttnParams &p = w.p;
     if (w.bytes) {
@@ -281,6 +284,14 @@ int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
         p.part_l = reinterpret_cast<float *>(static_cast<uint8_t *>(a->workspace) +
                                              up256(static_cast<size_t>(p.slots) * p.rows * a->head_dim * 4));
     }
+    return KVEVICT_OK;
+}
+
+int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
+{
+    AttnParams &p = w.p;
+    const int rw = bind_workspace(a, w);
+    if (rw) return rw;
     const double scale = a->scale > 0.f ? a->scale : 1.0 / std::sqrt(static_cast<double>(a->head_dim));
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     p.out = a->out;
@@ -358,21 +369,18 @@ extern "C" int kvevict_shared_prefix_attention_workspace_bytes(const kvevict_sha
     if (rc) return rc;
     if (!bytes) return KVEVICT_ERR_INVALID_ARG;
     Plan w;
-    rc = plan_shared(s, w);
+    rc = plan_shared(s, w, false);
     if (rc == KVEVICT_OK) *bytes = w.bytes;
     return rc;
 }
 
-extern "C" int kvevict_shared_prefix_attention(const kvevict_shared_prefix_args *s, void *cuda_stream)
+namespace {
+
+// Checks the call's tensors, and fills the plan with them.
+int bind_shared(const kvevict_shared_prefix_args *s, Plan &w)
 {
-    int rc = check_shared(s);
-    if (rc) return rc;
     const kvevict_attention_args *a = &s->a;
-    Plan w;
-    rc = plan_shared(s, w);
-    if (rc) return rc;
-    if (a->batch == 0) return KVEVICT_OK;
-    rc = check_tensors(a, a->k_rows > 0);
+    const int rc = check_tensors(a, a->k_rows > 0);
     if (rc) return rc;
     const int elem = a->dtype == KVEVICT_F32 ? 4 : 2;
     const int64_t pn[2] = {a->n_kv_heads, s->prefix_rows};
@@ -393,5 +401,53 @@ extern "C" int kvevict_shared_prefix_attention(const kvevict_shared_prefix_args 
     copy3(y.ks, a->k_stride);
     copy3(y.vs, a->v_stride);
     y.k_lens = a->kv_lens;
-    return run(a, w, static_cast<cudaStream_t>(cuda_stream));
+    return KVEVICT_OK;
+}
+
+int shared_call(const kvevict_shared_prefix_args *s, Plan &w, bool outside)
+{
+    int rc = check_shared(s);
+    if (!rc) rc = plan_shared(s, w, outside);
+    return rc;
+}
+
+}  // namespace
+
+extern "C" int kvevict_shared_prefix_attention(const kvevict_shared_prefix_args *s, void *cuda_stream)
+{
+    Plan w;
+    int rc = shared_call(s, w, false);
+    if (rc) return rc;
+    if (s->a.batch == 0) return KVEVICT_OK;
+    rc = bind_shared(s, w);
+    return rc ? rc : run(&s->a, w, static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" int kvevict_prefix_bytes(const kvevict_shared_prefix_args *s, size_t *bytes)
+{
+    Plan w;
+    const int rc = shared_call(s, w, true);
+    if (rc == KVEVICT_OK) *bytes = w.bytes;
+    return rc;
+}
+
+extern "C" int kvevict_prefix_part(const kvevict_shared_prefix_args *s, float **part_o, float **part_l)
+{
+    Plan w;
+    int rc = shared_call(s, w, true);
+    if (!rc) rc = bind_shared(s, w);
+    if (!rc) rc = bind_workspace(&s->a, w);
+    if (rc) return rc;
+    const AttnParams &p = w.p;
+    *part_o = p.part_o + static_cast<size_t>(p.pr[1].slot0) * p.rows * s->a.head_dim;
+    *part_l = p.part_l + static_cast<size_t>(p.pr[1].slot0) * p.rows;
+    return KVEVICT_OK;
+}
+
+extern "C" int kvevict_prefix_run(const kvevict_shared_prefix_args *s, void *cuda_stream)
+{
+    Plan w;
+    int rc = shared_call(s, w, true);
+    if (!rc) rc = bind_shared(s, w);
+    return rc ? rc : run(&s->a, w, static_cast<cudaStream_t>(cuda_stream));
 }

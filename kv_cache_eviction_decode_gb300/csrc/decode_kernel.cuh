@@ -95,6 +95,8 @@ struct DecodeParams {
     const void *k_new;   // [B][Hkv][D]
     const void *v_new;   // [B][Hkv][D]
     void *out;           // [B][Hkv*G][D]
+    float *part_o;       // null, or [B][Hkv*G][D]: the output in fp32 goes here instead of to out, and
+    float *part_l;       // the log2 of each row's softmax normaliser here (a part for a join with others)
     void *kc, *vc;       // this layer's cache, [B][Hkv][C][D]
     int32_t *pos;        // [B][Hkv][cstride]
     void *score;         // [B][Hkv][cstride] fp32 (fp16 with score_half), or null when the policy keeps no scores
@@ -1186,6 +1188,10 @@ __global__ void __launch_bounds__((warps_for<G, MMA>() * 32), (min_blocks<G, MMA
                     float ox, oy;
                     cta_o(g, ox, oy);
                     const float inv = 1.f / cta_l(g);
+                    if (P.part_o) {
+                        *reinterpret_cast<float2 *>(P.part_o + unit * (G * D) + 2 * jp) = make_float2(ox * inv, oy * inv);
+                        continue;
+                    }
                     TPair<T> o2;
                     o2.x = E::from_f32(ox * inv);
                     o2.y = E::from_f32(oy * inv);
@@ -1196,6 +1202,7 @@ __global__ void __launch_bounds__((warps_for<G, MMA>() * 32), (min_blocks<G, MMA
             if (tid < G) {
                 const float l = cta_l(tid);
                 if (!(l > 0.f && l <= FLT_MAX)) atomicOr(P.err, KVEVICT_DEV_NONFINITE);
+                if (P.part_l) P.part_l[unit * G + tid] = M.m[tid] + log2f(l);
             }
             if (has_score) {
                 // ------------------------------ cumulative scores (H2O)
@@ -1403,6 +1410,7 @@ __global__ void __launch_bounds__((warps_for<G, MMA>() * 32), (min_blocks<G, MMA
                     if (ml.x != -INFINITY) lg += ml.y * exp2f(ml.x - mg);
                 }
                 if (ri == 0 && !(lg > 0.f && lg <= FLT_MAX)) atomicOr(P.err, KVEVICT_DEV_NONFINITE);
+                if (ri == 0 && P.part_l) P.part_l[unit * G + tid] = mg + log2f(lg);
                 const float inv = 1.f / lg;
                 for (int c = 0; c < S; ++c) {
                     const float mc = M.xml[b][c][tid].x;
@@ -1417,7 +1425,8 @@ __global__ void __launch_bounds__((warps_for<G, MMA>() * 32), (min_blocks<G, MMA
                     const int g = (i0 + k) / D;
                     float o = 0.f;
                     for (int c = 0; c < S; ++c) o = fmaf(M.xo[b][c * SL + k], M.fac[c][g], o);
-                    outp[i0 + k] = E::from_f32(o);
+                    if (P.part_o) P.part_o[unit * GD + i0 + k] = o;
+                    else outp[i0 + k] = E::from_f32(o);
                 }
             };
             if (!alias) write_slice();
