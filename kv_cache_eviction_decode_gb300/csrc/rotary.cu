@@ -15,6 +15,7 @@
 
 #include "device_common.cuh"
 #include "kvevict_ops.h"
+#include "launch.h"
 
 namespace kvevict {
 
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const __grid_co
 {
     constexpr int N = Vec<T>::N;
     extern __shared__ float2 cs[];  // [R / 2] cos, sin
+    grid_dependency_wait();
     const long long bt = blockIdx.x;
     const long long b = bt / p.tokens, t = bt - b * p.tokens;
     const long long at = b * p.ps0 + t * p.ps1;
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_con
 {
     constexpr int N = Vec<T>::N, kBatch = INTER ? 4 : 2;
     extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    grid_dependency_wait();
     const uint32_t half = p.R / 2;
     const uint32_t pairs = INTER ? 0 : half / N;                       // units of two chunks a head
     const uint32_t units = INTER ? p.D / N : pairs + (p.D - p.R) / N;  // units a head
@@ -300,6 +303,7 @@ extern "C" int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream)
     p.total = total;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const int n = 16 / elem;  // elements of a chunk
+    cudaError_t e;
     if (a->interleaved ? p.R % n == 0 : p.R / 2 % n == 0) {
         const uint32_t heads = static_cast<uint32_t>(p.heads[0] + p.heads[1]);
         const uint32_t units = static_cast<uint32_t>(a->interleaved ? p.D / n : p.R / 2 / n + (p.D - p.R) / n);
@@ -317,16 +321,16 @@ extern "C" int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream)
         const unsigned g = static_cast<unsigned>(blocks);
         const size_t smem = static_cast<size_t>(p.tokens_per) * (p.R / 2) * sizeof(float2);
         if (a->interleaved) {
-            if (elem == 4) rotary_kernel<float, true><<<g, kRotThreads, smem, st>>>(p);
-            else rotary_kernel<__nv_bfloat16, true><<<g, kRotThreads, smem, st>>>(p);
+            if (elem == 4) e = launch_dependent(rotary_kernel<float, true>, g, kRotThreads, smem, st, p);
+            else e = launch_dependent(rotary_kernel<__nv_bfloat16, true>, g, kRotThreads, smem, st, p);
         } else {
-            if (elem == 4) rotary_kernel<float, false><<<g, kRotThreads, smem, st>>>(p);
-            else rotary_kernel<__nv_bfloat16, false><<<g, kRotThreads, smem, st>>>(p);
+            if (elem == 4) e = launch_dependent(rotary_kernel<float, false>, g, kRotThreads, smem, st, p);
+            else e = launch_dependent(rotary_kernel<__nv_bfloat16, false>, g, kRotThreads, smem, st, p);
         }
     } else {
         const size_t smem = static_cast<size_t>(p.R / 2) * sizeof(float2);
-        if (elem == 4) rotary_any_kernel<float><<<static_cast<unsigned>(total), kRotThreads, smem, st>>>(p);
-        else rotary_any_kernel<__nv_bfloat16><<<static_cast<unsigned>(total), kRotThreads, smem, st>>>(p);
+        if (elem == 4) e = launch_dependent(rotary_any_kernel<float>, static_cast<unsigned>(total), kRotThreads, smem, st, p);
+        else e = launch_dependent(rotary_any_kernel<__nv_bfloat16>, static_cast<unsigned>(total), kRotThreads, smem, st, p);
     }
-    return cudaGetLastError() == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
+    return e == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
 }

@@ -13,6 +13,7 @@
 // loads.
 #include <cmath>
 
+#include "launch.h"
 #include "window_attn.h"
 #include "window_attn_common.cuh"
 
@@ -57,6 +58,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_c
     extern __shared__ float fsm[];
     float *sQ = fsm, *sK = sQ + R * L::kQ, *sP = sK + kBK * L::kQ;
 
+    grid_dependency_wait();
     int item = blockIdx.x;
     const bool second = item >= ap.pr[0].n_items;
     if (second) item -= ap.pr[0].n_items;
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 {
     constexpr int N = D / 32;
     const AttnProblem &p = ap.pr[ap.n_problems - 1];
+    grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const long long rows = static_cast<long long>(p.batch) * ap.Hq * p.max_q;
     for (long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < rows;
@@ -277,8 +280,7 @@ template <int D, int R> cudaError_t launch_f32(const AttnParams &p, cudaStream_t
     constexpr int bytes = F32Layout<D, R>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kern<<<p.pr[0].n_items + (p.n_problems > 1 ? p.pr[1].n_items : 0), kThreadsF32, bytes, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(kern, p.pr[0].n_items + (p.n_problems > 1 ? p.pr[1].n_items : 0), kThreadsF32, bytes, st, p);
 }
 
 template <typename T, int D> cudaError_t launch_join(const AttnParams &p, cudaStream_t st)
@@ -286,8 +288,7 @@ template <typename T, int D> cudaError_t launch_join(const AttnParams &p, cudaSt
     const AttnProblem &q = p.pr[p.n_problems - 1];
     const long long rows = static_cast<long long>(q.batch) * p.Hq * q.max_q;
     const long long blocks = (rows + 7) / 8;
-    attn_join_kernel<T, D><<<static_cast<int>(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(attn_join_kernel<T, D>, static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, st, p);
 }
 
 }  // namespace

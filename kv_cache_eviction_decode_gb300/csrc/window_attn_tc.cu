@@ -24,6 +24,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "launch.h"
 #include "tc5_common.cuh"
 #include "window_attn.h"
 #include "window_attn_common.cuh"
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(tslot), 0);
+    grid_dependency_wait();
     // The i-th posted item; null where there is none or the wait ran out.
     auto take = [&](int i, bool &ok) -> const TcItem * {
         if (!mbar_wait(&i_full[i % kItemSlots], (i / kItemSlots) & 1)) {
@@ -911,8 +913,7 @@ template <int D> cudaError_t launch_tc(const AttnTcParams &p, cudaStream_t st)
         if (dev <= 255) ready[dev >> 6].fetch_or(uint64_t{1} << (dev & 63));
     }
     const int n = p.a.pr[0].n_items + (p.a.n_problems > 1 ? p.a.pr[1].n_items : 0);
-    attn_tc_kernel<D><<<n, kTcThreads, bytes, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(attn_tc_kernel<D>, n, kTcThreads, bytes, st, p);
 }
 
 }  // namespace

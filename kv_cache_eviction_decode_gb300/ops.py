@@ -7,7 +7,6 @@ waits for the GPU, and every call can be captured in a CUDA graph.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import struct
 
@@ -21,9 +20,13 @@ _DT = {torch.float32: F32, torch.bfloat16: BF16}
 _ATTN = struct.Struct("@9if2q5P12q4PPNP")
 _SHARED = struct.Struct("@9if2q5P12q4PPNP2P5q")
 _ROT = struct.Struct("@8i2q4P12qP3qPf4x")
+# ... and in pieces: shapes, addresses, strides, addresses (all multiples of 8 bytes).
+_HEAD, _PTRS, _Q9, _Q3, _TAIL = (struct.Struct("@" + f) for f in ("9if2q", "5P", "9q", "3q", "4PPNP"))
+_ROT_HEAD, _Q12, _ROT_TAIL, _P2, _P4 = (struct.Struct("@" + f) for f in ("8i2q", "12q", "P3qPf4x", "2P", "4P"))
 
 # The handle of a device's current stream as a number (torch.cuda.current_stream
 # builds a Stream object first, ten times the cost), where torch has it.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
@@ -95,26 +98,44 @@ def _error_word(t, q: torch.Tensor) -> int:
     return t.data_ptr()
 
 
-def _call(name: str, q: torch.Tensor, args: bytes) -> None:
-    """The entry point on the current stream of q's device, with that device current."""
-    dev = q.get_device()
-    if dev == torch.cuda.current_device():
-        rc = getattr(lib(), name)(args, _raw_stream(dev))
+_entry = {}  # the library's entry points, looked up once
+
+
+def _call(name: str, dev: int, args: bytes) -> None:
+    """The entry point on the current stream of device `dev`, with that device current."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
+    if dev == _current_device():
+        rc = fn(args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = getattr(lib(), name)(args, _raw_stream(dev))
+            rc = fn(args, _raw_stream(dev))
     if rc != OK:
         check(rc, name)
 
 
-@functools.lru_cache(maxsize=4096)
-def _need(name: str, fmt: struct.Struct, shape: tuple, packed: bool, *tail) -> int:
-    """Workspace bytes: a function of the shape alone."""
+def _workspace_need(name: str, args: bytes) -> int:
     n = ctypes.c_size_t(0)
-    starts = (16, 16) if packed else (0, 0)  # any addresses: only whether there are starts counts
-    name += "_workspace_bytes"
-    check(getattr(lib(), name)(fmt.pack(*shape, *(0,) * 17, *starts, 0, 0, 0, 0, 0, *tail), n), name)
+    check(getattr(lib(), name + "_workspace_bytes")(args, n), name + "_workspace_bytes")
     return n.value
+
+
+class _Layout:
+    """What a call's argument struct holds besides addresses, checked and packed once per shapes, strides, types and
+    options: the checks and the packing cost more than the launch."""
+
+    __slots__ = ("head", "strides", "out_strides", "need", "out_shape", "lse_shape", "batch", "tail")
+
+
+_layouts: dict = {}
+
+
+def _remember(key, layout: _Layout) -> _Layout:
+    if len(_layouts) >= 4096:
+        _layouts.clear()
+    _layouts[key] = layout
+    return layout
 
 
 def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sink: int = 0, window: int | None = None,
@@ -135,6 +156,32 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sin
     Returns out (as q), or (out, lse) with return_lse or an lse tensor: fp32
     [B][Hq][N], or [T][Hq] packed. A row that sees nothing gives 0 and -inf.
     """
+    packed = q_starts is not None
+    key = (q.dtype, k.dtype, v.dtype, q.get_device(), k.get_device(), v.get_device(), q.shape, k.shape, v.shape, q.stride(),
+           k.stride(), v.stride(), n_sink, window, scale, max_q, max_k, q_starts.shape if packed else None)
+    lay = _layouts.get(key) or _remember(key, _window_layout(q, k, v, n_sink, window, scale, q_starts, max_q, max_k))
+    if packed:
+        if k_starts is None or q_lens is not None or kv_lens is not None:
+            raise ValueError("packed: give q_starts, k_starts, max_q and max_k, and no lengths")
+        starts = (_ints(q_starts, lay.batch + 1, q, "q_starts"), _ints(k_starts, lay.batch + 1, q, "k_starts"), 0, 0)
+    else:
+        if k_starts is not None:
+            raise ValueError("k_starts: goes with q_starts")
+        starts = (0, 0, _ints(q_lens, lay.batch, q, "q_lens"), _ints(kv_lens, lay.batch, q, "kv_lens"))
+    given = out is not None
+    out, lse = _outputs(q, out, lse, return_lse, lay.lse_shape)
+    if not given:
+        out_strides = lay.out_strides
+    else:
+        out_strides = _Q3.pack(*((0, out.stride(1), out.stride(0)) if packed else out.stride()[:3]))
+    workspace, wp, wn = _workspace(workspace, lay.need, q)
+    _call("kvevict_window_attention", q.get_device(), b"".join((
+        lay.head, _PTRS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr()),
+        lay.strides, out_strides, _TAIL.pack(*starts, wp, wn, _error_word(error_word, q)))))
+    return out if lse is None else (out, lse)
+
+
+def _window_layout(q, k, v, n_sink, window, scale, q_starts, max_q, max_k) -> _Layout:
     dt = _dtype(q, "q")
     packed = q_starts is not None
     dims = 3 if packed else 4
@@ -150,33 +197,32 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sin
     d = q.shape[-1]
     if k.shape[-1] != d:
         raise ValueError(f"k: head_dim {k.shape[-1]}, q has {d}")
+    lay = _Layout()
     if packed:
-        if k_starts is None or max_q is None or max_k is None or q_lens is not None or kv_lens is not None:
+        if max_q is None or max_k is None:
             raise ValueError("packed: give q_starts, k_starts, max_q and max_k, and no lengths")
         B = q_starts.shape[0] - 1
         N, Hq, M, Hkv = q.shape[0], q.shape[1], k.shape[0], k.shape[1]
-        qs, ks = (0, q.stride(1), q.stride(0)), (0, k.stride(1), k.stride(0))
-        vs = (0, v.stride(1), v.stride(0))
-        lse_shape = q.shape[:2]
+        strides = [(0, t.stride(1), t.stride(0)) for t in (q, k, v)]
+        dense = (0, d, Hq * d)
+        lay.lse_shape = q.shape[:2]
     else:
-        if k_starts is not None:
-            raise ValueError("k_starts: goes with q_starts")
         B, Hq, N = q.shape[:3]
         if k.shape[0] != B:
             raise ValueError(f"k: {k.shape[0]} sequences, q has {B}")
         Hkv, M = k.shape[1], k.shape[2]
-        qs, ks, vs = q.stride()[:3], k.stride()[:3], v.stride()[:3]
+        strides = [t.stride()[:3] for t in (q, k, v)]
+        dense = (Hq * N * d, N * d, d)
         max_q = max_k = 0
-        lse_shape = q.shape[:3]
-    out, lse = _outputs(q, out, lse, return_lse, lse_shape)
-    os = (0, out.stride(1), out.stride(0)) if packed else out.stride()[:3]
+        lay.lse_shape = q.shape[:3]
     shape = (dt, d, Hq, Hkv, B, n_sink, min(window, 2**31 - 1), max_q, max_k, _scale(scale), N, M)
-    workspace, wp, wn = _workspace(workspace, _need("kvevict_window_attention", _ATTN, shape, packed), q)
-    _call("kvevict_window_attention", q, _ATTN.pack(
-        *shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-        *qs, *ks, *vs, *os, _ints(q_starts, B + 1, q, "q_starts"), _ints(k_starts, B + 1, q, "k_starts"),
-        _ints(q_lens, B, q, "q_lens"), _ints(kv_lens, B, q, "kv_lens"), wp, wn, _error_word(error_word, q)))
-    return out if lse is None else (out, lse)
+    lay.batch = B
+    lay.head = _HEAD.pack(*shape)
+    lay.strides = _Q9.pack(*strides[0], *strides[1], *strides[2])
+    lay.out_strides = _Q3.pack(*dense)
+    # (of the starts only their presence counts for the size)
+    lay.need = _workspace_need("kvevict_window_attention", _ATTN.pack(*shape, *(0,) * 17, *((16, 16) if packed else (0, 0)), 0, 0, 0, 0, 0))
+    return lay
 
 
 def shared_prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, k: torch.Tensor,
@@ -188,6 +234,22 @@ def shared_prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: t
     [B][Hkv][M][d], of kv_lens rows (int32 [B] on the device; None: M). The
     prefix is read once for the batch. P and M may be 0. Returns out (as q), or
     (out, lse [B][Hq])."""
+    key = (q.dtype, k.dtype, v.dtype, k_prefix.dtype, v_prefix.dtype, q.get_device(), k.get_device(), v.get_device(),
+           k_prefix.get_device(), v_prefix.get_device(), q.shape, k.shape, v.shape, k_prefix.shape, v_prefix.shape, q.stride(),
+           k.stride(), v.stride(), k_prefix.stride(), v_prefix.stride(), scale)
+    lay = _layouts.get(key) or _remember(key, _shared_layout(q, k_prefix, v_prefix, k, v, scale))
+    given = out is not None
+    out, lse = _outputs(q, out, lse, return_lse, lay.lse_shape)
+    out_strides = _Q3.pack(out.stride(0), out.stride(1), 0) if given else lay.out_strides
+    workspace, wp, wn = _workspace(workspace, lay.need, q)
+    _call("kvevict_shared_prefix_attention", q.get_device(), b"".join((
+        lay.head, _PTRS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr()),
+        lay.strides, out_strides, _TAIL.pack(0, 0, 0, _ints(kv_lens, lay.batch, q, "kv_lens"), wp, wn, _error_word(error_word, q)),
+        _P2.pack(k_prefix.data_ptr(), v_prefix.data_ptr()), lay.tail)))
+    return out if lse is None else (out, lse)
+
+
+def _shared_layout(q, k_prefix, v_prefix, k, v, scale) -> _Layout:
     dt = _dtype(q, "q")
     _like(q, q, 3, "q")
     _like(k_prefix, q, 3, "k_prefix")
@@ -198,17 +260,18 @@ def shared_prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: t
     Hkv, M = k.shape[1], k.shape[2]
     if k.shape[0] != B or k.shape[3] != d or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != d:
         raise ValueError(f"k, k_prefix: need [{B}][Hkv][M][{d}] and [Hkv][P][{d}], got {tuple(k.shape)} and {tuple(k_prefix.shape)}")
-    out, lse = _outputs(q, out, lse, return_lse, q.shape[:2])
     P = k_prefix.shape[1]
     shape = (dt, d, Hq, Hkv, B, 0, 0, 0, 0, _scale(scale), 1, M)
-    need = _need("kvevict_shared_prefix_attention", _SHARED, shape, False, 0, 0, 0, 0, 0, 0, P)
-    workspace, wp, wn = _workspace(workspace, need, q)
-    _call("kvevict_shared_prefix_attention", q, _SHARED.pack(
-        *shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-        q.stride(0), q.stride(1), 0, *k.stride()[:3], *v.stride()[:3], out.stride(0), out.stride(1), 0, 0, 0, 0,
-        _ints(kv_lens, B, q, "kv_lens"), wp, wn, _error_word(error_word, q), k_prefix.data_ptr(), v_prefix.data_ptr(),
-        *k_prefix.stride()[:2], *v_prefix.stride()[:2], P))
-    return out if lse is None else (out, lse)
+    lay = _Layout()
+    lay.batch = B
+    lay.lse_shape = q.shape[:2]
+    lay.head = _HEAD.pack(*shape)
+    lay.strides = _Q9.pack(q.stride(0), q.stride(1), 0, *k.stride()[:3], *v.stride()[:3])
+    lay.out_strides = _Q3.pack(Hq * d, d, 0)
+    tail = (*k_prefix.stride()[:2], *v_prefix.stride()[:2], P)
+    lay.tail = struct.pack("@5q", *tail)
+    lay.need = _workspace_need("kvevict_shared_prefix_attention", _SHARED.pack(*shape, *(0,) * 24, 0, 0, *tail))
+    return lay
 
 
 def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -262,6 +325,40 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
     token's position. inv_freq: fp64 on the device (rotary_frequencies).
     q_out / k_out may be q / k: in place. inverse: by the negative angle, the
     gradient of the forward call. Returns (q_out, k_out), or q_out without k."""
+    key = (q.dtype, q.get_device(), q.shape, q.stride(), None if k is None else (k.dtype, k.get_device(), k.shape, k.stride()),
+           None if isinstance(positions, int) else (positions.dtype, positions.get_device(), positions.shape, positions.stride()),
+           inv_freq.shape, interleaved, inverse)
+    lay = _layouts.get(key) or _remember(key, _rotary_layout(q, k, positions, inv_freq, interleaved, inverse))
+    if q_out is None and k_out is None:
+        q_out, strides = torch.empty(q.shape, dtype=q.dtype, device=q.device), lay.strides
+        if k is not None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    else:
+        dims = q.dim()
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _like(q_out, q, dims, "q_out", q.shape)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            _like(k_out, q, dims, "k_out", k.shape)
+        strides = _Q12.pack(*_heads(q), *_heads(q_out), *((0,) * 6 if k is None else (*_heads(k), *_heads(k_out))))
+    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq: need a contiguous float64 vector on {q.device}")
+    pp, start = (0, positions) if isinstance(positions, int) else (positions.data_ptr(), 0)
+    kp, kop = (0, 0) if k is None else (k.data_ptr(), k_out.data_ptr())
+    _call("kvevict_rotary", q.get_device(), b"".join((
+        lay.head, _P4.pack(q.data_ptr(), kp, q_out.data_ptr(), kop), strides,
+        _ROT_TAIL.pack(pp, *lay.tail, start, inv_freq.data_ptr(), scale))))
+    return q_out if k is None else (q_out, k_out)
+
+
+def _heads(t: torch.Tensor) -> tuple:
+    """Strides of sequence, head, token."""
+    return (0, t.stride(1), t.stride(0)) if t.dim() == 3 else t.stride()[:3]
+
+
+def _rotary_layout(q, k, positions, inv_freq, interleaved, inverse) -> _Layout:
     dt = _dtype(q, "q")
     dims = q.dim()
     if dims not in (3, 4):
@@ -270,33 +367,19 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
     d = q.shape[-1]
     if dims == 3:
         B, N, Hq = 1, q.shape[0], q.shape[1]
+        dense = [(0, d, Hq * d)]
     else:
         B, Hq, N = q.shape[:3]
-
-    def st(t):
-        return (0, t.stride(1), t.stride(0)) if dims == 3 else t.stride()[:3]
-
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _like(q_out, q, dims, "q_out", q.shape)
+        dense = [(Hq * N * d, N * d, d)]
+    Hk = 0
     if k is not None:
         _like(k, q, dims, "k")
         Hk = k.shape[1]
         if k.shape[-1] != d or k.shape[0] != q.shape[0] or (dims == 4 and k.shape[2] != N):
             raise ValueError(f"k: {tuple(k.shape)} does not go with q {tuple(q.shape)}")
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        else:
-            _like(k_out, q, dims, "k_out", k.shape)
-        kp, kop, kst, kost = k.data_ptr(), k_out.data_ptr(), st(k), st(k_out)
-    else:
-        Hk, kp, kop, kst, kost = 0, 0, 0, (0, 0, 0), (0, 0, 0)
-    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError(f"inv_freq: need a contiguous float64 vector on {q.device}")
-    if isinstance(positions, int):
-        pp, p64, ps, start = 0, 0, (0, 0), positions
-    else:
+        dense.append((0, d, Hk * d) if dims == 3 else (Hk * N * d, N * d, d))
+    p64, ps = 0, (0, 0)
+    if not isinstance(positions, int):
         if positions.get_device() != q.get_device() or positions.dtype not in (torch.int32, torch.int64):
             raise ValueError(f"positions: need int32 or int64 on {q.device}, got {positions.dtype} on {positions.device}")
         if positions.shape == (N,):
@@ -305,8 +388,9 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
             ps = positions.stride()
         else:
             raise ValueError(f"positions: {tuple(positions.shape)} does not go with q {tuple(q.shape)}")
-        pp, p64, start = positions.data_ptr(), int(positions.dtype == torch.int64), 0
-    _call("kvevict_rotary", q, _ROT.pack(
-        dt, d, 2 * inv_freq.shape[0], int(interleaved), int(inverse), p64, Hq, Hk, B, N, q.data_ptr(), kp, q_out.data_ptr(), kop,
-        *st(q), *st(q_out), *kst, *kost, pp, *ps, start, inv_freq.data_ptr(), scale))
-    return q_out if k is None else (q_out, k_out)
+        p64 = int(positions.dtype == torch.int64)
+    lay = _Layout()
+    lay.head = _ROT_HEAD.pack(dt, d, 2 * inv_freq.shape[0], int(interleaved), int(inverse), p64, Hq, Hk, B, N)
+    lay.strides = _Q12.pack(*_heads(q), *dense[0], *((0,) * 6 if k is None else (*_heads(k), *dense[1])))
+    lay.tail = ps
+    return lay

@@ -31,6 +31,13 @@ def test_struct_layouts(tmp_path):
     assert got == [ops._ATTN.size, ops._SHARED.size, ops._ROT.size, 224, ops._ATTN.size, 208]
 
 
+def test_pieces_make_the_structs():
+    from kv_cache_eviction_decode_gb300 import ops
+    attn = ops._HEAD.size + ops._PTRS.size + ops._Q9.size + ops._Q3.size + ops._TAIL.size
+    assert attn == ops._ATTN.size and attn + ops._P2.size + 40 == ops._SHARED.size
+    assert ops._ROT_HEAD.size + ops._P4.size + ops._Q12.size + ops._ROT_TAIL.size == ops._ROT.size
+
+
 F = dict(dtype=1, d=128, hq=8, hkv=2, batch=2, n_sink=4, window=64, max_q=0, max_k=0, scale=0.0, q_rows=300, k_rows=300,
          q=4096, k=4096, v=4096, out=4096, lse=0, qs=(8 * 300 * 128, 300 * 128, 128), ks=(2 * 300 * 128, 300 * 128, 128),
          vs=(2 * 300 * 128, 300 * 128, 128), os=(8 * 300 * 128, 300 * 128, 128), q_starts=0, k_starts=0, q_lens=0, kv_lens=0,
