@@ -64,6 +64,7 @@ extern "C" {
  *              sequence has more than max_q queries; max_k, the most keys, only
  *              steers the launch. Rows outside every sequence are left as they
  *              were. lse is dense [q_rows][n_q_heads].
+ *   out and lse must not overlap q, k or v.
  *   V rows that no query of the sequence sees may hold anything, infinities
  *              and NaN included; K likewise. Rows that one query sees and
  *              another does not must be finite for the other's sake.
@@ -76,7 +77,9 @@ extern "C" {
  *              keys: the keys are split over CTAs and the parts joined by a
  *              second kernel. Contents need not be kept or cleared; calls that
  *              may overlap on the GPU need one each.
- *   error_word: device uint32 that error bits are OR-ed into, or NULL.
+ *   error_word: device uint32 that error bits are OR-ed into (BAD_LENGTH, and
+ *              WAIT_TIMEOUT: a pipeline wait gave up, the results are not valid),
+ *              or NULL.
  */
 typedef struct {
     int32_t dtype, head_dim, n_q_heads, n_kv_heads, batch, n_sink, window;
@@ -146,8 +149,7 @@ int kvevict_shared_prefix_attention(const kvevict_shared_prefix_args *a, void *c
  *   positions: device, int64 (positions_64 = 1) or int32, element
  *              [b * pos_stride[0] + token * pos_stride[1]]; any value,
  *              negative ones too. NULL: pos_start + token for every sequence.
- *   inv_freq:  device fp64 [rotary_dim / 2], radians per position, each within
- *              +-pi.
+ *   inv_freq:  device fp64 [rotary_dim / 2], radians per position, finite.
  *              The angle is formed as a 64-bit binary fraction of a turn
  *              (position times frequency modulo 2^64), so its error is below
  *              2^-53 turns times |pos| and far positions keep full accuracy.

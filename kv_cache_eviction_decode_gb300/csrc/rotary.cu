@@ -65,8 +65,9 @@ __device__ __forceinline__ uint4 pack16(const float (&v)[8])
 
 __device__ __forceinline__ float2 rot_cos_sin(double freq, long long pos, float scale, bool inverse)
 {
-    // freq in [-pi, pi]: half a turn at most, so the fraction fits a signed 64-bit integer
-    const long long f = __double2ll_rn(freq * (0.15915494309189535 * 18446744073709551616.0));
+    // whole turns a position drop out; half a turn at most is left, and fits a signed 64-bit integer
+    const double turns = freq * 0.15915494309189535;
+    const long long f = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
     const long long frac = static_cast<long long>(static_cast<unsigned long long>(pos) * static_cast<unsigned long long>(f));
     const float half_turns = static_cast<float>(frac) * 1.0842021724855044e-19f;  // 2^-63
     float s, c;

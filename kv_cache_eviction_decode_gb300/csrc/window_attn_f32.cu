@@ -8,9 +8,9 @@
 // walks the key tiles of 64 that the rows see; each thread owns R/16 rows x 4
 // keys of the logits and R/16 rows x D/16 columns of the output. FFMA bound at
 // R = 64: per 64 FFMA a warp issues 8 shared-memory loads (12 wavefronts, below
-// the 16 cycles that the FFMAs take at four warps a cycle). K and V take turns
-// in one buffer, so that two CTAs fit an SM and one computes while the other
-// loads.
+// the 16 cycles that the FFMAs take at four warps a cycle). V is copied while
+// the logits are made and the next K during the product with V (cp.async, no
+// registers between).
 #include <cmath>
 
 #include "launch.h"
@@ -28,9 +28,19 @@ constexpr float kLn2 = 0.69314718055994531f;
 template <int D, int R> struct F32Layout {
     static constexpr int kQ = D + 4;    // padded rows: four floats apart, 8 rows cover the 32 banks
     static constexpr int kP = kBK + 4;
-    static constexpr int kFloats = R * kQ + kBK * kQ + R * kP;
+    static constexpr int kFloats = R * kQ + 2 * kBK * kQ + R * kP;
     static constexpr int kBytes = kFloats * 4;
+    static constexpr int kCtas = kBytes <= 113 * 1024 ? 2 : 1;  // that an SM holds
 };
+
+// 16 bytes global -> shared without a register between, or 16 zero bytes.
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All groups but the newest N have landed (this thread's own; a barrier makes them everyone's).
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
@@ -50,13 +60,13 @@ __device__ __forceinline__ float half_sum(float v)
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_constant__ AttnParams ap)
+__global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f32_kernel(const __grid_constant__ AttnParams ap)
 {
     using L = F32Layout<D, R>;
     constexpr int RM = R / 16;      // rows of a thread
     constexpr int CV = D / 64;      // float4 columns of a thread's output
     extern __shared__ float fsm[];
-    float *sQ = fsm, *sK = sQ + R * L::kQ, *sP = sK + kBK * L::kQ;
+    float *sQ = fsm, *sK = sQ + R * L::kQ, *sV = sK + kBK * L::kQ, *sP = sV + kBK * L::kQ;
 
     grid_dependency_wait();
     int item = blockIdx.x;
@@ -114,21 +124,24 @@ __global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_c
         for (int c = 0; c < CV; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 
-    auto load_tile = [&](const float *base, long long stride, int j0) {
+    // Copies a K or V tile into shared memory, one group; the keys that no row of this tile of rows
+    // sees are not read (their rows: zeros).
+    auto load_tile = [&](float *dst, const float *base, long long stride, int j0) {
         for (int e = tid; e < kBK * (D / 4); e += kThreadsF32) {
             const int r = e / (D / 4), c = (e - r * (D / 4)) * 4;
             const int j = j0 + r;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            // only keys that a row of this tile sees are read
-            if (j < keys.sink || (j >= keys.lo && j < keys.hi)) v = load4(base + j * stride + c);
-            *reinterpret_cast<float4 *>(sK + r * L::kQ + c) = v;
+            const bool seen = j < keys.sink || (j >= keys.lo && j < keys.hi);
+            copy16(dst + r * L::kQ + c, seen ? base + j * stride + c : base, seen);
         }
+        copies_close();
     };
+    if (i_lo < i_hi) load_tile(sK, kb, p.ks[2], attn_tile_at(keys, i_lo) * kBK);
 
     for (int i = i_lo; i < i_hi; ++i) {
         const int j0 = attn_tile_at(keys, i) * kBK;
         __syncthreads();  // the previous tile's V has been used
-        load_tile(kb, p.ks[2], j0);
+        load_tile(sV, vb, p.vs[2], j0);
+        copies_wait<1>();  // K; V lands while the logits are made
         __syncthreads();
         float s[RM][4];
 #pragma unroll
@@ -178,8 +191,13 @@ __global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_c
                 o[a][c].x *= f; o[a][c].y *= f; o[a][c].z *= f; o[a][c].w *= f;
             }
         }
-        __syncthreads();  // every thread has used K
-        load_tile(vb, p.vs[2], j0);
+        __syncthreads();  // every thread has used K and written its probabilities
+        if (i + 1 < i_hi) {
+            load_tile(sK, kb, p.ks[2], attn_tile_at(keys, i + 1) * kBK);  // lands during the product with V
+            copies_wait<1>();
+        } else {
+            copies_wait<0>();
+        }
         __syncthreads();
 #pragma unroll 4
         for (int j = 0; j < kBK; j += 4) {
@@ -190,7 +208,7 @@ __global__ void __launch_bounds__(kThreadsF32, 2) attn_f32_kernel(const __grid_c
             for (int jj = 0; jj < 4; ++jj) {
 #pragma unroll
                 for (int c = 0; c < CV; ++c) {
-                    const float4 v = *reinterpret_cast<const float4 *>(sK + (j + jj) * L::kQ + tx * 4 + c * 64);
+                    const float4 v = *reinterpret_cast<const float4 *>(sV + (j + jj) * L::kQ + tx * 4 + c * 64);
 #pragma unroll
                     for (int a = 0; a < RM; ++a) {
                         const float w = jj == 0 ? pv[a].x : jj == 1 ? pv[a].y : jj == 2 ? pv[a].z : pv[a].w;
