@@ -121,7 +121,8 @@ void cut_for(Plan &w, AttnProblem &q, int64_t max_k, double other = 0)
         // (one key tile at most: nothing to share, the second tile stays without rows)
         q.pair = pair && key_tiles(max_k, q.n_sink, q.causal ? q.window : 0, q.max_q, kAttnTcKeys) > 1;
     } else {
-        cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows, kAttnF32Keys, max_k, other);
+        cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows,
+            w.few ? kAttnF32FewKeys : kAttnF32Keys, max_k, other);
     }
 }
 
@@ -202,7 +203,7 @@ int plan_shared(const kvevict_shared_prefix_args *s, Plan &w, bool outside)
     y.rs[0] = p.Hq; y.rs[1] = 1; y.rs[2] = 0;
     w.tensor = a->dtype == KVEVICT_BF16;
     w.few = few_rows(p.G, p.Hkv, a->batch);
-    const double keys = w.tensor ? kAttnTcKeys : kAttnF32Keys;
+    const double keys = w.tensor ? kAttnTcKeys : w.few ? kAttnF32FewKeys : kAttnF32Keys;
     const double yt = outside ? 0 : static_cast<double>(a->batch) * p.Hkv * std::ceil(y.k_rows / keys);
     const double xt = p.Hkv * std::ceil(x.k_rows / keys);
     cut_for(w, x, x.k_rows, yt);

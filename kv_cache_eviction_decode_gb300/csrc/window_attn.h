@@ -42,7 +42,7 @@ struct AttnParams {
     uint32_t *err;      // may be null
 };
 
-constexpr int kAttnF32Rows = 64, kAttnF32FewRows = 16, kAttnF32Keys = 64;
+constexpr int kAttnF32Rows = 64, kAttnF32FewRows = 16, kAttnF32Keys = 64, kAttnF32FewKeys = 32;
 
 // Tensor maps of one problem: q as (d, group head, token, KV head, sequence),
 // boxes of 64 x G x (128 / G) tokens; k and v as (d, key, KV head, sequence),

@@ -4,13 +4,19 @@
 // out_i = sum_j 2^(z_ij - M_i) v_j / sum_j 2^(z_ij - M_i), z = q . k * scale *
 // log2(e), M the running maximum of one pass over the key tiles (each new
 // maximum rescales the sum and the output by 2^(old - new)). A CTA of 16 x 16
-// threads holds a tile of R query rows (64, or 16 where a unit has few) and
-// walks the key tiles of 64 that the rows see; each thread owns R/16 rows x 4
-// keys of the logits and R/16 rows x D/16 columns of the output. FFMA bound at
-// R = 64: per 64 FFMA a warp issues 8 shared-memory loads (12 wavefronts, below
-// the 16 cycles that the FFMAs take at four warps a cycle). V is copied while
-// the logits are made and the next K during the product with V (cp.async, no
-// registers between).
+// threads holds a tile of R query rows and walks the key tiles that the rows
+// see; each thread owns R/16 rows x (tile / 16) keys of the logits and R/16 rows
+// x D/16 columns of the output. V is copied while the logits are made and the
+// next K during the product with V (cp.async, no registers between).
+//
+// R = 64, tiles of 64 keys: FFMA bound; per 64 FFMA a warp issues 8
+// shared-memory loads (12 wavefronts, below the 16 cycles that the FFMAs take at
+// four warps a cycle). 8 heads of 2048 x 128, causal: 407 us, 21 TFLOP/s (518
+// with K and V loaded in turn into one buffer).
+// R = 16, tiles of 32 keys, four CTAs an SM: for few rows, where K and V are read
+// for little arithmetic. 8 sequences of 8 heads, one token over 8000 keys of 128:
+// 98 us, 5.4 TB/s (285 while the warps without rows computed theirs too: bound by
+// shared-memory reads).
 #include <cmath>
 
 #include "launch.h"
@@ -21,16 +27,16 @@ namespace kvevict {
 
 namespace {
 
-constexpr int kBK = kAttnF32Keys;
 constexpr int kThreadsF32 = 256;
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D, int R> struct F32Layout {
+    static constexpr int kBK = R == kAttnF32FewRows ? kAttnF32FewKeys : kAttnF32Keys;
     static constexpr int kQ = D + 4;    // padded rows: four floats apart, 8 rows cover the 32 banks
     static constexpr int kP = kBK + 4;
     static constexpr int kFloats = R * kQ + 2 * kBK * kQ + R * kP;
     static constexpr int kBytes = kFloats * 4;
-    static constexpr int kCtas = kBytes <= 113 * 1024 ? 2 : 1;  // that an SM holds
+    static constexpr int kCtas = kBytes <= 56 * 1024 ? 4 : kBytes <= 113 * 1024 ? 2 : 1;  // that an SM holds
 };
 
 // 16 bytes global -> shared without a register between, or 16 zero bytes.
@@ -63,7 +69,9 @@ template <int D, int R>
 __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f32_kernel(const __grid_constant__ AttnParams ap)
 {
     using L = F32Layout<D, R>;
+    constexpr int kBK = L::kBK;
     constexpr int RM = R / 16;      // rows of a thread
+    constexpr int KM = kBK / 16;    // keys of a thread
     constexpr int CV = D / 64;      // float4 columns of a thread's output
     extern __shared__ float fsm[];
     float *sQ = fsm, *sK = sQ + R * L::kQ, *sV = sK + kBK * L::kQ, *sP = sV + kBK * L::kQ;
@@ -114,6 +122,9 @@ __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f3
         top[i] = ty * RM + i < nrows ? pos : -1;
         low[i] = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
     }
+    // a warp whose rows (two of the 16 row groups) all lie behind the last one only helps copying:
+    // with a single row the others' shared-memory reads were what bound the loop
+    const bool busy = (tid >> 5) * 2 * RM < nrows;
     float m[RM], l[RM];
     float4 o[RM][CV];
 #pragma unroll
@@ -143,52 +154,54 @@ __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f3
         load_tile(sV, vb, p.vs[2], j0);
         copies_wait<1>();  // K; V lands while the logits are made
         __syncthreads();
-        float s[RM][4];
-#pragma unroll
-        for (int a = 0; a < RM; ++a)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[a][c] = 0.f;
-#pragma unroll 4
-        for (int d = 0; d < D; d += 4) {
-            float4 qv[RM], kv[4];
-#pragma unroll
-            for (int a = 0; a < RM; ++a) qv[a] = *reinterpret_cast<const float4 *>(sQ + (ty * RM + a) * L::kQ + d);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) kv[c] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * c) * L::kQ + d);
+        if (busy) {
+            float s[RM][KM];
 #pragma unroll
             for (int a = 0; a < RM; ++a)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    s[a][c] = fmaf(qv[a].x, kv[c].x, s[a][c]);
-                    s[a][c] = fmaf(qv[a].y, kv[c].y, s[a][c]);
-                    s[a][c] = fmaf(qv[a].z, kv[c].z, s[a][c]);
-                    s[a][c] = fmaf(qv[a].w, kv[c].w, s[a][c]);
+                for (int c = 0; c < KM; ++c) s[a][c] = 0.f;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                float4 qv[RM], kv[KM];
+#pragma unroll
+                for (int a = 0; a < RM; ++a) qv[a] = *reinterpret_cast<const float4 *>(sQ + (ty * RM + a) * L::kQ + d);
+#pragma unroll
+                for (int c = 0; c < KM; ++c) kv[c] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * c) * L::kQ + d);
+#pragma unroll
+                for (int a = 0; a < RM; ++a)
+#pragma unroll
+                    for (int c = 0; c < KM; ++c) {
+                        s[a][c] = fmaf(qv[a].x, kv[c].x, s[a][c]);
+                        s[a][c] = fmaf(qv[a].y, kv[c].y, s[a][c]);
+                        s[a][c] = fmaf(qv[a].z, kv[c].z, s[a][c]);
+                        s[a][c] = fmaf(qv[a].w, kv[c].w, s[a][c]);
+                    }
+            }
+#pragma unroll
+            for (int a = 0; a < RM; ++a) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < KM; ++c) {
+                    const int j = j0 + tx + 16 * c;
+                    if (!(j <= top[a] && (j < p.n_sink || j >= low[a]))) s[a][c] = -INFINITY;
+                    mx = fmaxf(mx, s[a][c]);
                 }
-        }
+                const float mn = fmaxf(m[a], half_max(mx));
+                const float ms = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[a] - ms);
+                m[a] = mn;
+                float sum = 0.f;
 #pragma unroll
-        for (int a = 0; a < RM; ++a) {
-            float mx = -INFINITY;
+                for (int c = 0; c < KM; ++c) {
+                    const float e = exp2f(s[a][c] - ms);
+                    sum += e;
+                    sP[(ty * RM + a) * L::kP + tx + 16 * c] = e;
+                }
+                l[a] = l[a] * f + half_sum(sum);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int j = j0 + tx + 16 * c;
-                if (!(j <= top[a] && (j < p.n_sink || j >= low[a]))) s[a][c] = -INFINITY;
-                mx = fmaxf(mx, s[a][c]);
-            }
-            const float mn = fmaxf(m[a], half_max(mx));
-            const float ms = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m[a] - ms);
-            m[a] = mn;
-            float sum = 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float e = exp2f(s[a][c] - ms);
-                sum += e;
-                sP[(ty * RM + a) * L::kP + tx + 16 * c] = e;
-            }
-            l[a] = l[a] * f + half_sum(sum);
-#pragma unroll
-            for (int c = 0; c < CV; ++c) {
-                o[a][c].x *= f; o[a][c].y *= f; o[a][c].z *= f; o[a][c].w *= f;
+                for (int c = 0; c < CV; ++c) {
+                    o[a][c].x *= f; o[a][c].y *= f; o[a][c].z *= f; o[a][c].w *= f;
+                }
             }
         }
         __syncthreads();  // every thread has used K and written its probabilities
@@ -199,6 +212,7 @@ __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f3
             copies_wait<0>();
         }
         __syncthreads();
+        if (!busy) continue;
 #pragma unroll 4
         for (int j = 0; j < kBK; j += 4) {
             float4 pv[RM];
