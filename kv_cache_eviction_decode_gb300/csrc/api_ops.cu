@@ -62,15 +62,18 @@ int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens, int key
 
 // Cuts a problem into items: tiles of `rows` rows, and parts of the key range
 // where the tiles alone would leave SMs idle. An SM works on one item after
-// another (two on the CUDA cores side by side); with `tiles` key tiles an item,
-// p parts and items * p over the SMs in w waves, the launch takes about
-// w * (tiles / p + kItemCost): an item's start and end, and its part's output
-// and join, cost as much as kItemCost key tiles (on the tensor cores 4.9 us for
-// an item of 5.7 tiles that would stream in 2.4: 32 sequences, 8 KV heads, window
-// 2044). `other`: key tiles of a problem in the same launch.
+// another (on the CUDA cores a few side by side). In key tiles: an item of t
+// takes t + kItemCost for its start and end (32 sequences, 8 KV heads, window
+// 2044: 4.9 us an item of 5.7 tiles that would stream in 2.4), and with several
+// parts rows * 4 / (tile keys * element bytes) more for writing and reading its
+// part's fp32 output: little for the rows of a decoded token, four tiles for 256
+// rows (a causal prompt of 4096, 32 heads over 8: 197 us in two parts, 117 in one).
+// Items of equal work run in whole waves; those of a causal prompt start with the
+// longest, and beside another problem's items the SMs are shared evenly: the
+// longest item, or the work over the SMs. `other`: that problem's key tiles.
 constexpr double kItemCost = 1.8;
 
-void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int64_t max_k, double other)
+void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int elem, int64_t max_k, double other)
 {
     const int per = rows / G;
     p.q_tiles = (p.max_q + per - 1) / per;
@@ -79,12 +82,14 @@ void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int64_t max_k, doub
     p.pair = 0;
     if (items == 0 || items >= 4 * kSMs) return;
     const int64_t tiles = key_tiles(max_k, p.n_sink, p.causal ? p.window : 0, std::min(per, p.max_q), keys);
+    const double out = std::min<double>(rows, static_cast<double>(p.max_q) * G) * 4 / (keys * elem);
+    const bool ramp = p.causal && !p.window && p.q_tiles > 1;
     double best = 0;
     for (int64_t s = 1; s <= std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (tiles + 1) / 2)); ++s) {
-        const double part = static_cast<double>((tiles + s - 1) / s) + kItemCost;
-        // alone, in whole waves; beside another problem's items the SMs are shared evenly
-        const double load = other > 0 ? std::max(part, (static_cast<double>(items * s) * part + other) / kSMs)
-                                      : static_cast<double>((items * s + kSMs - 1) / kSMs) * part;
+        const double cost = kItemCost + (s > 1 ? out : 0), part = static_cast<double>((tiles + s - 1) / s) + cost;
+        const double all = static_cast<double>(items * s);
+        const double load = ramp || other > 0 ? std::max(part, (all * (ramp ? part / 2 + cost / 2 : part) + other) / kSMs)
+                                              : std::ceil(all / kSMs) * part;
         if (s == 1 || load < best * 0.97) {
             best = load;
             p.splits = static_cast<int>(s);
@@ -117,12 +122,12 @@ void cut_for(Plan &w, AttnProblem &q, int64_t max_k, double other = 0)
     const int G = w.p.G;
     if (w.tensor) {
         const bool pair = q.max_q <= kAttnTcRows / G;
-        cut(q, G, w.p.Hkv, (pair ? 1 : 2) * (kAttnTcRows / G) * G, kAttnTcKeys, max_k, other);
+        cut(q, G, w.p.Hkv, (pair ? 1 : 2) * (kAttnTcRows / G) * G, kAttnTcKeys, 2, max_k, other);
         // (one key tile at most: nothing to share, the second tile stays without rows)
         q.pair = pair && key_tiles(max_k, q.n_sink, q.causal ? q.window : 0, q.max_q, kAttnTcKeys) > 1;
     } else {
         cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows,
-            w.few ? kAttnF32FewKeys : kAttnF32Keys, max_k, other);
+            w.few ? kAttnF32FewKeys : kAttnF32Keys, 4, max_k, other);
     }
 }
 
