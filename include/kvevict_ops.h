@@ -27,7 +27,8 @@ extern "C" {
 #endif
 
 /* A length or start on the device was out of range (negative, decreasing,
- * beyond the tensor, a sequence longer than max_q): it was clamped. */
+ * beyond the tensor, a sequence longer than max_q): it was clamped, and a
+ * sequence that starts before its predecessor does was left out. */
 #define KVEVICT_DEV_BAD_LENGTH 0x10u
 
 /*

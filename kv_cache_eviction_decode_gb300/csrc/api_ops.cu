@@ -60,7 +60,7 @@ int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens, int key
     return std::min(all, (static_cast<int64_t>(n_sink) + keys - 1) / keys + (window + tokens - 1 + keys - 1) / keys + 1);
 }
 
-// Cuts a problem into items: tiles of `rows` rows, and parts of the key range
+// How a problem is cut into items: tiles of rows, and parts of the key range
 // where the tiles alone would leave SMs idle. An SM works on one item after
 // another (on the CUDA cores a few side by side). In key tiles: an item of t
 // takes t + kItemCost for its start and end (32 sequences, 8 KV heads, window
@@ -68,31 +68,91 @@ int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens, int key
 // parts rows * 4 / (tile keys * element bytes) more for writing and reading its
 // part's fp32 output: little for the rows of a decoded token, four tiles for 256
 // rows (a causal prompt of 4096, 32 heads over 8: 197 us in two parts, 117 in one).
-// Items of equal work run in whole waves; those of a causal prompt start with the
-// longest, and beside another problem's items the SMs are shared evenly: the
-// longest item, or the work over the SMs. `other`: that problem's key tiles.
 constexpr double kItemCost = 1.8;
 
-void cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int elem, int64_t max_k, double other)
+struct Cut {
+    int64_t items = 0, tiles = 0;  // tiles of rows over all units; key tiles one sees at most
+    double out = 0;
+    bool ramp = false;             // a causal prompt: from all keys down to few
+
+    double length(int64_t parts) const
+    {
+        return static_cast<double>((tiles + parts - 1) / parts) + kItemCost + (parts > 1 ? out : 0);
+    }
+    int64_t most() const { return items >= 4 * kSMs ? 1 : std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (tiles + 1) / 2)); }
+};
+
+Cut cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int elem, int64_t max_k)
 {
+    Cut c;
     const int per = rows / G;
     p.q_tiles = (p.max_q + per - 1) / per;
-    const int64_t items = static_cast<int64_t>(p.batch) * Hkv * p.q_tiles;
     p.splits = 1;
     p.pair = 0;
-    if (items == 0 || items >= 4 * kSMs) return;
-    const int64_t tiles = key_tiles(max_k, p.n_sink, p.causal ? p.window : 0, std::min(per, p.max_q), keys);
-    const double out = std::min<double>(rows, static_cast<double>(p.max_q) * G) * 4 / (keys * elem);
-    const bool ramp = p.causal && !p.window && p.q_tiles > 1;
-    double best = 0;
-    for (int64_t s = 1; s <= std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (tiles + 1) / 2)); ++s) {
-        const double cost = kItemCost + (s > 1 ? out : 0), part = static_cast<double>((tiles + s - 1) / s) + cost;
-        const double all = static_cast<double>(items * s);
-        const double load = ramp || other > 0 ? std::max(part, (all * (ramp ? part / 2 + cost / 2 : part) + other) / kSMs)
-                                              : std::ceil(all / kSMs) * part;
-        if (s == 1 || load < best * 0.97) {
-            best = load;
-            p.splits = static_cast<int>(s);
+    c.items = static_cast<int64_t>(p.batch) * Hkv * p.q_tiles;
+    c.tiles = key_tiles(max_k, p.n_sink, p.causal ? p.window : 0, std::min(per, p.max_q), keys);
+    c.out = std::min<double>(rows, static_cast<double>(p.max_q) * G) * 4 / (keys * elem);
+    c.ramp = p.causal && !p.window && p.q_tiles > 1;
+    return c;
+}
+
+// Parts of a problem alone: items of equal work run in whole waves; those of a
+// causal prompt start with the longest and take the longest item, or the work
+// over the SMs.
+int parts_alone(const Cut &c)
+{
+    int best = 1;
+    double least = 0;
+    for (int64_t s = 1; s <= c.most(); ++s) {
+        const double all = static_cast<double>(c.items * s), len = c.length(s), cost = kItemCost + (s > 1 ? c.out : 0);
+        const double load = c.ramp ? std::max(len, all * (len + cost) / 2 / kSMs) : std::ceil(all / kSMs) * len;
+        if (s == 1 || load < least * 0.97) {
+            least = load;
+            best = static_cast<int>(s);
+        }
+    }
+    return best;
+}
+
+// Parts of two problems in one launch, the first one's items first: those take
+// whole waves and, for the rest of the last one, `long_sms` SMs; the second one's
+// items then fill up. A key tile of the first costs `weight` (its products, where
+// both row tiles are full: 3,300 cycles against 2,750 that a streamed tile takes;
+// 1.5 fits the measurements: 64 sequences behind 32768 tokens took 154, 135, 141
+// and 151 us with 4, 6, 8 and 16 parts, 32 behind 8192, whose rows fill one row tile,
+// 72, 62, 64 and 73 with 2, 3, 6 and 8). `share`: of the second's keys expected
+// (their lengths are on the device).
+void parts_together(const Cut &a, const Cut &b, double weight, double share, int &pa, int &pb)
+{
+    static constexpr int kTry[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64};
+    double least = 0;
+    pa = pb = 1;
+    for (const int sb : {1, 2, 3, 4, 6, 8}) {
+        if (sb > b.most()) break;
+        const double lb = (b.length(sb) - kItemCost) * share + kItemCost;
+        const double nb = static_cast<double>(b.items * sb);
+        for (const int sa : kTry) {
+            if (sa > a.most()) break;
+            const double la = a.length(sa) + (weight - 1) * static_cast<double>((a.tiles + sa - 1) / sa);
+            const int64_t na = a.items * sa;
+            const double base = static_cast<double>(na / kSMs) * la;
+            const int64_t long_sms = na % kSMs;
+            // the least end at which the SMs have had room for the second's items
+            double end = base + (long_sms ? la : 0);
+            const double whole = std::ceil(std::max(0.0, (nb * lb - (kSMs * (end - base) - long_sms * la)) / (kSMs * lb)) - 1) * lb;
+            for (double t = end + std::max(0.0, whole);; t += lb / 4) {
+                const double room = std::floor((t - base) / lb + 1e-9) * (kSMs - long_sms) +
+                                    std::floor((t - base - la) / lb + 1e-9) * (t - base >= la ? long_sms : 0);
+                if (room >= nb) {
+                    end = t;
+                    break;
+                }
+            }
+            if (least == 0 || end < least * 0.98) {
+                least = end;
+                pa = sa;
+                pb = sb;
+            }
         }
     }
 }
@@ -116,19 +176,17 @@ bool few_rows(int G, int64_t units, int64_t max_q)
 
 // Cuts a problem for the kernel of the plan's type. The tensor cores take two
 // tiles of 128 rows an item, or one (with alternate key tiles) where the rows
-// fit one: then only parts of two key tiles or more make sense.
-void cut_for(Plan &w, AttnProblem &q, int64_t max_k, double other = 0)
+// fit one.
+Cut cut_for(Plan &w, AttnProblem &q, int64_t max_k)
 {
     const int G = w.p.G;
-    if (w.tensor) {
-        const bool pair = q.max_q <= kAttnTcRows / G;
-        cut(q, G, w.p.Hkv, (pair ? 1 : 2) * (kAttnTcRows / G) * G, kAttnTcKeys, 2, max_k, other);
-        // (one key tile at most: nothing to share, the second tile stays without rows)
-        q.pair = pair && key_tiles(max_k, q.n_sink, q.causal ? q.window : 0, q.max_q, kAttnTcKeys) > 1;
-    } else {
-        cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows,
-            w.few ? kAttnF32FewKeys : kAttnF32Keys, 4, max_k, other);
-    }
+    if (!w.tensor)
+        return cut(q, G, w.p.Hkv, w.few ? kAttnF32FewRows : kAttnF32Rows, w.few ? kAttnF32FewKeys : kAttnF32Keys, 4, max_k);
+    const bool fits = q.max_q <= kAttnTcRows / G;
+    const Cut c = cut(q, G, w.p.Hkv, (fits ? 1 : 2) * (kAttnTcRows / G) * G, kAttnTcKeys, 2, max_k);
+    // (one key tile at most: nothing to share, the second tile stays without rows)
+    q.pair = fits && c.tiles > 1;
+    return c;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -180,7 +238,7 @@ int plan_window(const kvevict_attention_args *a, Plan &w)
     }
     w.tensor = a->dtype == KVEVICT_BF16;
     w.few = few_rows(p.G, static_cast<int64_t>(q.batch) * p.Hkv, q.max_q);
-    cut_for(w, q, max_k);
+    q.splits = parts_alone(cut_for(w, q, max_k));
     return finish(w, a->head_dim);
 }
 
@@ -208,12 +266,14 @@ int plan_shared(const kvevict_shared_prefix_args *s, Plan &w, bool outside)
     y.rs[0] = p.Hq; y.rs[1] = 1; y.rs[2] = 0;
     w.tensor = a->dtype == KVEVICT_BF16;
     w.few = few_rows(p.G, p.Hkv, a->batch);
-    const double keys = w.tensor ? kAttnTcKeys : w.few ? kAttnF32FewKeys : kAttnF32Keys;
-    const double yt = outside ? 0 : static_cast<double>(a->batch) * p.Hkv * std::ceil(y.k_rows / keys);
-    const double xt = p.Hkv * std::ceil(x.k_rows / keys);
-    cut_for(w, x, x.k_rows, yt);
-    if (outside) y.splits = 1;  // no items
-    else cut_for(w, y, y.k_rows, xt);
+    const Cut cx = cut_for(w, x, x.k_rows);
+    if (outside) {
+        x.splits = parts_alone(cx);
+        y.splits = 1;  // no items
+    } else {
+        const Cut cy = cut_for(w, y, y.k_rows);
+        parts_together(cx, cy, w.tensor && !x.pair ? 1.5 : 1.0, 0.8, x.splits, y.splits);
+    }
     return finish(w, a->head_dim);
 }
 

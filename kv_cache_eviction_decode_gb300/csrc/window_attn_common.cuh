@@ -35,6 +35,10 @@ __device__ __forceinline__ AttnSeq attn_sequence(const AttnProblem &p, int b)
         const int k1 = min(max(c1, s.k0), p.k_rows);
         s.m = k1 - s.k0;
         s.bad = s.q0 != a0 || q1 != a1 || s.n != q1 - s.q0 || s.k0 != c0 || k1 != c1;
+        if (b > 0 && p.q_starts[b - 1] > a0) {  // its rows would be an earlier sequence's
+            s.n = 0;
+            s.bad = true;
+        }
     } else {
         s.q0 = s.k0 = 0;
         const int n = p.q_lens ? p.q_lens[b] : p.q_rows, m = p.k_lens ? p.k_lens[b] : p.k_rows;

@@ -850,16 +850,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     // write where nothing was seen: its weight is 0)
                     float4 *dst = reinterpret_cast<float4 *>(ap.part_o + slot * D);
 #pragma unroll 1
-                    for (int q = 0; q < D; q += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + 128u * s + q, o);
+                    for (int q = 0; q < D; q += 64) {
+                        uint32_t o[2][32];
+                        tmem_ld32(tO + 128u * s + q, o[0]);
+                        tmem_ld32(tO + 128u * s + q + 32, o[1]);
                         tc_wait_ld();
-                        if (q + 32 == D) release();
+                        if (q + 64 == D) release();
                         if (mine && any) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                dst[(q + e) / 4] = make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
-                                                               __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+                            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    dst[(q + 32 * g + e) / 4] =
+                                        make_float4(__uint_as_float(o[g][e]) * f, __uint_as_float(o[g][e + 1]) * f,
+                                                    __uint_as_float(o[g][e + 2]) * f, __uint_as_float(o[g][e + 3]) * f);
                         }
                     }
                 } else {

@@ -137,3 +137,16 @@ def test_capture_and_stream(cuda_device):
     pos += 9
     g.replay()
     assert torch.equal(y, kv.rotary(x, None, pos, f)) and not torch.equal(y, want)
+
+
+def test_offsets_beyond_32_bits(cuda_device):
+    """Rows of a tensor of more than 2^31 elements, in place and out of it."""
+    f, _ = kv.rotary_frequencies(64)
+    big = torch.empty(3 * 2**30 + 4096, device="cuda", dtype=torch.bfloat16)
+    x = big.as_strided((3, 2, 64), (3 * 2**29, 64, 1))
+    x.copy_(torch.randn(3, 2, 64, device="cuda", generator=torch.Generator(device="cuda").manual_seed(19)))
+    pos = torch.tensor([5, 6, 70000], device="cuda")
+    want = kv.rotary(x.contiguous(), None, pos, f)
+    assert torch.equal(kv.rotary(x, None, pos, f), want)
+    kv.rotary(x, None, pos, f, q_out=x)
+    assert torch.equal(x, want)

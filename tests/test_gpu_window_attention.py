@@ -222,3 +222,39 @@ def test_same_call_same_bits(cuda_device, dtype):
     for _ in range(4):
         b = kv.window_attention(q, k, v, n_sink=4, window=2000, return_lse=True)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_bad_starts_are_clamped_and_flagged(cuda_device, dtype):
+    """Starts that go back, or beyond the tensors, or a sequence above max_q: nothing outside is touched, the rows of the
+    sound sequence are right, the error word says so."""
+    g = gen(13)
+    q = torch.randn(40, 4, 64, generator=g, device="cuda", dtype=dtype)
+    k, v = (torch.randn(50, 2, 64, generator=g, device="cuda", dtype=dtype) for _ in range(2))
+    for qs, ks, max_q, good in (([0, 20, 10, 40], [0, 25, 25, 50], 40, 0), ([0, 20, 30, 99], [0, 20, 30, 99], 40, 1),
+                                ([-7, 0, 20, 30], [-3, 0, 20, 30], 40, 1), ([0, 30, 40, 40], [0, 30, 50, 50], 20, 1)):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, 7.0)
+        a, b = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (qs, ks))
+        kv.window_attention(q, k, v, q_starts=a, k_starts=b, max_q=max_q, max_k=50, out=out, error_word=err)
+        assert int(err) == 0x10
+        qq, kk, vv = (x[s[good]:s[good + 1]].transpose(0, 1) for x, s in ((q, qs), (k, ks), (v, ks)))
+        r, l, A = ref.sequence(qq, kk, vv, 0, None, 0.125)
+        tol, _ = ref.bounds(dtype, qq, kk, 50, 0.125, r, A, l)
+        ref.assert_close(out[qs[good]:qs[good + 1]].transpose(0, 1), r, tol, "out")
+
+
+def test_offsets_beyond_32_bits(cuda_device):
+    """A cache of more than 2^31 elements: the last sequence's keys and the last head's."""
+    B, Hkv, m, d = 70, 8, 30000, 128
+    k, v = (torch.empty(B, Hkv, m, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    g = gen(17)
+    assert k.numel() > 2**31
+    q = torch.randn(B, 16, 1, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lens[-1] = m
+    for t in (k, v):
+        t[-1].normal_(generator=g)
+    out, lse = kv.window_attention(q, k, v, n_sink=4, window=3000, kv_lens=lens, return_lse=True)
+    assert (out[:-1] == 0).all() and (lse[:-1] == -math.inf).all()
+    check(q[-1:], k[-1:], v[-1:], out[-1:], lse[-1:], 4, 3000)
