@@ -210,6 +210,7 @@ __device__ __forceinline__ void tc_mask32(uint32_t (&r)[32], int top, int low, i
     const uint32_t near = low <= 0 ? 0xffffffffu : low >= 32 ? 0u : ~((1u << low) - 1u);
     const uint32_t first = sink >= 32 ? 0xffffffffu : sink <= 0 ? 0u : (1u << sink) - 1u;
     seen &= near | first;
+    if (__all_sync(0xffffffffu, seen == 0xffffffffu)) return;  // most chunks of a border tile
 #pragma unroll
     for (int e = 0; e < 32; ++e) r[e] = (seen >> e) & 1u ? r[e] : 0xff800000u;
 }
