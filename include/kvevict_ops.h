@@ -27,8 +27,9 @@ extern "C" {
 #endif
 
 /* A length or start on the device was out of range (negative, decreasing,
- * beyond the tensor, a sequence longer than max_q): it was clamped, and a
- * sequence that starts before its predecessor does was left out. */
+ * beyond the tensor, a sequence longer than max_q): it was clamped. Where the
+ * starts of a packed batch go back, the sequence that would end before it
+ * starts and every one behind it were left out. */
 #define KVEVICT_DEV_BAD_LENGTH 0x10u
 
 /*

@@ -3,6 +3,8 @@
 // range of query positions sees.
 #pragma once
 
+#include <climits>
+
 #include "device_common.cuh"
 #include "kvevict_ops.h"
 #include "window_attn.h"
@@ -14,6 +16,9 @@ __device__ __forceinline__ void attn_flag(uint32_t *err, uint32_t bit)
     if (err) atomicOr(err, bit);
 }
 
+__host__ __device__ __forceinline__ int attn_min(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int attn_max(int a, int b) { return a > b ? a : b; }
+
 // One sequence: where its rows start (token index), how many there are, and
 // the position of its first query (negative where there are more queries than
 // keys). Values from the device are clamped to the tensors.
@@ -22,28 +27,52 @@ struct AttnSeq {
     bool bad;
 };
 
-__device__ __forceinline__ AttnSeq attn_sequence(const AttnProblem &p, int b)
+// Whether sequence j of a packed batch ends before it starts.
+__host__ __device__ __forceinline__ bool attn_falls(const AttnProblem &p, int j) { return p.q_starts[j] > p.q_starts[j + 1]; }
+
+// The first of the sequences 0 .. upto that does, or INT_MAX; by a whole warp.
+__device__ __forceinline__ int attn_first_fall(const AttnProblem &p, int upto, int lane)
+{
+    for (int j0 = 0; j0 <= upto; j0 += 128) {
+        int at = INT_MAX;
+#pragma unroll
+        for (int u = 3; u >= 0; --u) {
+            const int j = j0 + 32 * u + lane;
+            if (j <= upto && attn_falls(p, j)) at = j;
+        }
+        at = __reduce_min_sync(0xffffffffu, at);
+        if (at != INT_MAX) return at;
+    }
+    return INT_MAX;
+}
+
+// `sound`: none of the sequences 0 .. b of a packed batch falls. Otherwise b is
+// left out: its rows could be an earlier sequence's, and a comparison with its
+// neighbours alone would not show that (starts 0, 20, 10, 15, 40: the last one
+// ascends again, inside the first one's rows). The rows of sound sequences are
+// disjoint, because their starts ascend.
+__host__ __device__ __forceinline__ AttnSeq attn_sequence(const AttnProblem &p, int b, bool sound)
 {
     AttnSeq s;
     s.bad = false;
     if (p.q_starts) {
         const int a0 = p.q_starts[b], a1 = p.q_starts[b + 1], c0 = p.k_starts[b], c1 = p.k_starts[b + 1];
-        s.q0 = min(max(a0, 0), p.q_rows);
-        const int q1 = min(max(a1, s.q0), p.q_rows);
-        s.n = min(q1 - s.q0, p.max_q);
-        s.k0 = min(max(c0, 0), p.k_rows);
-        const int k1 = min(max(c1, s.k0), p.k_rows);
+        s.q0 = attn_min(attn_max(a0, 0), p.q_rows);
+        const int q1 = attn_min(attn_max(a1, s.q0), p.q_rows);
+        s.n = attn_min(q1 - s.q0, p.max_q);
+        s.k0 = attn_min(attn_max(c0, 0), p.k_rows);
+        const int k1 = attn_min(attn_max(c1, s.k0), p.k_rows);
         s.m = k1 - s.k0;
         s.bad = s.q0 != a0 || q1 != a1 || s.n != q1 - s.q0 || s.k0 != c0 || k1 != c1;
-        if (b > 0 && p.q_starts[b - 1] > a0) {  // its rows would be an earlier sequence's
+        if (!sound) {
             s.n = 0;
             s.bad = true;
         }
     } else {
         s.q0 = s.k0 = 0;
         const int n = p.q_lens ? p.q_lens[b] : p.q_rows, m = p.k_lens ? p.k_lens[b] : p.k_rows;
-        s.n = min(max(n, 0), p.q_rows);
-        s.m = min(max(m, 0), p.k_rows);
+        s.n = attn_min(attn_max(n, 0), p.q_rows);
+        s.m = attn_min(attn_max(m, 0), p.k_rows);
         s.bad = s.n != n || s.m != m;
     }
     s.p0 = s.m - s.n;

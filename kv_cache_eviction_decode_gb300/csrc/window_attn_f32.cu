@@ -87,7 +87,13 @@ __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f3
     const int tile = item % p.q_tiles;
     const int unit = item / p.q_tiles;
     const int b = unit / ap.Hkv, kvh = unit - b * ap.Hkv;
-    const AttnSeq sq = attn_sequence(p, b);
+    bool sound = true;
+    if (p.q_starts) {
+        bool falls = false;
+        for (int j = threadIdx.x; j <= b; j += kThreadsF32) falls = falls || attn_falls(p, j);
+        sound = !__syncthreads_or(falls);
+    }
+    const AttnSeq sq = attn_sequence(p, b, sound);
     if (sq.bad && threadIdx.x == 0) attn_flag(ap.err, KVEVICT_DEV_BAD_LENGTH);
     const int per = R / G;          // tokens of a tile
     const int t0 = tile * per;
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         const int h = static_cast<int>(w % ap.Hq);
         const long long bt = w / ap.Hq;
         const int b = static_cast<int>(bt / p.max_q), t0 = static_cast<int>(bt - static_cast<long long>(b) * p.max_q);
-        const AttnSeq sq = attn_sequence(p, b);
+        const AttnSeq sq = attn_sequence(p, b, !p.q_starts || attn_first_fall(p, b, lane) == INT_MAX);
         if (t0 >= sq.n) continue;
         const int t = sq.q0 + t0;
         const long long row = b * p.rs[0] + h * p.rs[1] + t * p.rs[2];

@@ -315,7 +315,8 @@ __device__ __forceinline__ int tc_keys_in(const AttnKeys &keys, bool sink_tile, 
     return min(kBN, (last - j0 + 15) & ~15);
 }
 
-__device__ __forceinline__ void tc_make_item(const AttnTcParams &tp, int idx, TcItem &it)
+// `sound`: a packed batch's sequences before the first one that falls.
+__device__ __forceinline__ void tc_make_item(const AttnTcParams &tp, int idx, int sound, TcItem &it)
 {
     const AttnParams &ap = tp.a;
     it.prob = idx >= ap.pr[0].n_items ? 1 : 0;
@@ -334,7 +335,7 @@ __device__ __forceinline__ void tc_make_item(const AttnTcParams &tp, int idx, Tc
     }
     it.b = unit / ap.Hkv;
     it.kvh = unit - it.b * ap.Hkv;
-    const AttnSeq sq = attn_sequence(p, it.b);
+    const AttnSeq sq = attn_sequence(p, it.b, it.b < sound);
     it.q0 = sq.q0;
     it.k0 = sq.k0;
     it.p0 = sq.p0;
@@ -451,6 +452,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             // -------------------------------------------------------- scheduler
             // The grid has a block for every item, in the order of tc_make_item; a block that runs
             // takes over one after another of those that have not started.
+            const int sound = ap.pr[0].q_starts ? attn_first_fall(ap.pr[0], ap.pr[0].batch - 1, lane) : INT_MAX;
             if (lane == 0) {
                 int idx = blockIdx.x;
                 uint32_t asked = 0;
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     if (i > 0) idx = next();
                     // (an item whose rows lie behind its sequence's last has nothing to do)
                     while (idx >= 0) {
-                        tc_make_item(tp, idx, items[slot]);
+                        tc_make_item(tp, idx, sound, items[slot]);
                         if (items[slot].bad) attn_flag(ap.err, KVEVICT_DEV_BAD_LENGTH);
                         if (items[slot].sub[0].nt > 0) break;
                         idx = next();
