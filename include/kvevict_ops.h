@@ -27,9 +27,12 @@ extern "C" {
 #endif
 
 /* A length or start on the device was out of range (negative, decreasing,
- * beyond the tensor, a sequence longer than max_q): it was clamped. Where the
- * starts of a packed batch go back, the sequence that would end before it
- * starts and every one behind it were left out. */
+ * beyond the tensor, a sequence longer than max_q): it was clamped. Of a
+ * sequence with more queries than there are rows, or than max_q, the first ones
+ * are computed, at the positions that the given number of queries puts them at;
+ * the other rows are left as they were. Where the starts of a packed batch go
+ * back, the sequence that would end before it starts and every one behind it
+ * were left out. */
 #define KVEVICT_DEV_BAD_LENGTH 0x10u
 
 /*

@@ -20,8 +20,10 @@ __host__ __device__ __forceinline__ int attn_min(int a, int b) { return a < b ? 
 __host__ __device__ __forceinline__ int attn_max(int a, int b) { return a > b ? a : b; }
 
 // One sequence: where its rows start (token index), how many there are, and
-// the position of its first query (negative where there are more queries than
-// keys). Values from the device are clamped to the tensors.
+// the position of the first (negative where there are more queries than keys).
+// Values from the device are clamped to the tensors and to max_q; the position
+// is counted from the queries given, so that the rows of a sequence cut at its
+// end see no key that lies behind them.
 struct AttnSeq {
     int q0, n, k0, m, p0;
     bool bad;
@@ -55,11 +57,13 @@ __host__ __device__ __forceinline__ AttnSeq attn_sequence(const AttnProblem &p, 
 {
     AttnSeq s;
     s.bad = false;
+    long long given;  // queries from the first row to the end given
     if (p.q_starts) {
         const int a0 = p.q_starts[b], a1 = p.q_starts[b + 1], c0 = p.k_starts[b], c1 = p.k_starts[b + 1];
         s.q0 = attn_min(attn_max(a0, 0), p.q_rows);
         const int q1 = attn_min(attn_max(a1, s.q0), p.q_rows);
         s.n = attn_min(q1 - s.q0, p.max_q);
+        given = static_cast<long long>(a1) - s.q0;
         s.k0 = attn_min(attn_max(c0, 0), p.k_rows);
         const int k1 = attn_min(attn_max(c1, s.k0), p.k_rows);
         s.m = k1 - s.k0;
@@ -74,8 +78,11 @@ __host__ __device__ __forceinline__ AttnSeq attn_sequence(const AttnProblem &p, 
         s.n = attn_min(attn_max(n, 0), p.q_rows);
         s.m = attn_min(attn_max(m, 0), p.k_rows);
         s.bad = s.n != n || s.m != m;
+        given = n;
     }
-    s.p0 = s.m - s.n;
+    // (a position below -2^30 sees nothing, nor does any of the 2^30 rows behind it)
+    given = given < 0 ? 0 : given;
+    s.p0 = s.m - given < -(1ll << 30) ? -(1 << 30) : static_cast<int>(s.m - given);
     return s;
 }
 

@@ -155,6 +155,9 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sin
     sequences): q [T][Hq][d], k and v [S][Hkv][d]. Any strides, d contiguous.
     Returns out (as q), or (out, lse) with return_lse or an lse tensor: fp32
     [B][Hq][N], or [T][Hq] packed. A row that sees nothing gives 0 and -inf.
+    Rows behind q_lens, outside the starts or beyond max_q are not written (in
+    an output made here they hold anything). Lengths and starts out of range are
+    clamped and set the bit 0x10 of error_word (int32 on the device).
     """
     packed = q_starts is not None
     key = (q.dtype, k.dtype, v.dtype, q.get_device(), k.get_device(), v.get_device(), q.shape, k.shape, v.shape, q.stride(),

@@ -71,3 +71,27 @@ def test_starts_that_go_back_in_a_long_batch(cuda_device, dtype):
     for b in (0, 127, 128, 149, 150, 199):
         check_rows(q, k, v, out, lse, b, 1, 3 * b, 3)
     assert (out[200:] == 7).all() and (lse[200:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_more_queries_than_max_q(cuda_device, dtype):
+    """The rows that are computed see what they would see with all of them; the others are not written."""
+    q, k, v, out, lse, err = packed([0, 30, 40], [0, 30, 50], dtype, 20)
+    assert err == 0x10
+    check_rows(q, k, v, out, lse, 0, 20, 0, 30, n_given=30)
+    check_rows(q, k, v, out, lse, 30, 10, 30, 20)
+    assert (out[20:30] == 7).all() and (lse[20:30] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m", [30, 5000])
+def test_more_queries_than_rows(cuda_device, m, dtype):
+    """Padded: q_lens beyond the rows; with many keys split and joined."""
+    n, given, d = 8, 11, 64
+    g = torch.Generator(device="cuda").manual_seed(22)
+    q = torch.randn(1, 4, n, d, generator=g, device="cuda", dtype=dtype)
+    k, v = (torch.randn(1, 2, m, d, generator=g, device="cuda", dtype=dtype) for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = kv.window_attention(q, k, v, q_lens=torch.tensor([given], dtype=torch.int32, device="cuda"), error_word=err, return_lse=True)
+    assert int(err) == 0x10
+    check_rows(*(x[0].transpose(0, 1) for x in (q, k, v, out)), lse[0].t(), 0, n, 0, m, n_given=given)

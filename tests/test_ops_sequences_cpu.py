@@ -86,3 +86,19 @@ def test_any_starts_give_every_row_to_one_sequence(sequences):
             for r in range(s["q0"], s["q0"] + s["n"]):
                 assert r < rows and r not in owner, (starts, b, owner.get(r))
                 owner[r] = b
+
+
+def test_rows_of_a_cut_sequence_keep_their_positions(sequences):
+    """Queries beyond max_q or the tensor are left out at their end of the sequence: the others stay where m keys and
+    the given number of queries put them, and see no later key."""
+    (s,) = sequences(1, 30, 30, 20, [0, 30], [0, 30])
+    assert (s["q0"], s["n"], s["m"], s["p0"], s["bad"]) == (0, 20, 30, 0, 1)
+    (s,) = sequences(1, 30, 80, 30, [0, 50], [0, 80])
+    assert (s["n"], s["p0"], s["bad"]) == (30, 30, 1)
+    (s,) = sequences(1, 30, 20, 30, [-7, 10], [0, 20])      # its first seven queries are not there
+    assert (s["q0"], s["n"], s["p0"], s["bad"]) == (0, 10, 10, 1)
+    (s,) = sequences(0, 8, 40, 8, [11], [40])
+    assert (s["n"], s["p0"], s["bad"]) == (8, 29, 1)
+    for packed, a in ((1, [0, 2**31 - 1]), (0, [2**31 - 1]), (1, [-2**31, 2**31 - 1])):
+        s = sequences(packed, 8, 40, 8, a, [0, 40] if packed else [40])[0]
+        assert s["n"] == 8 and s["p0"] == -2**30 and s["bad"]
