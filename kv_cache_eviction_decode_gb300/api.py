@@ -35,7 +35,7 @@ class KVEvictCache:
         check(self._L.kvevict_state_bytes(ctypes.byref(self.cfg), ctypes.byref(nbytes)), "kvevict_state_bytes")
         self.device = torch.device(device if device is not None else "cuda")
         self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
-        self.state = torch.empty(nbytes.value, dtype=torch.uint8, device=self.device)
+        self.state = self._new((nbytes.value,), torch.uint8)
         self.h = ctypes.c_void_p()
         check(self._L.kvevict_create(ctypes.byref(self.h), ctypes.byref(self.cfg), _ptr(self.state), nbytes.value,
                                      self.stream.cuda_stream), "kvevict_create")
@@ -63,6 +63,19 @@ class KVEvictCache:
             self.close()
         except Exception:
             pass
+
+    # --------------------------------------------------------------- tensors
+    def _new(self, shape, dtype: torch.dtype) -> torch.Tensor:
+        """A tensor for work on the handle's stream. It is taken from the allocator in that stream's order: a block
+        handed out on the current stream may still be in use by what is queued there, which the handle's kernels do
+        not wait for. The caller reads it on the current stream, so it is held for that one too."""
+        if ops._raw_stream(self.stream.device_index) == self.stream.cuda_stream:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        current = torch.cuda.current_stream(self.stream.device)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(current)
+        return t
 
     # ---------------------------------------------------------------- checks
     def _dev(self, t: torch.Tensor, shape, name: str, dtype=None) -> torch.Tensor:
@@ -102,7 +115,7 @@ class KVEvictCache:
         self._dev(V, (self.B, self.Hkv, n, self.D), "V")
         need = self.prefill_scored_workspace_bytes(n)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            workspace = self._new((need,), torch.uint8)
         if workspace.device != self.device or workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace: need {need} bytes on {self.device}")
         check(self._L.kvevict_prefill_scored(self.h, layer, _ptr(Q), _ptr(K), _ptr(V), n, _ptr(workspace),
@@ -131,7 +144,7 @@ class KVEvictCache:
         self._dev(V, (self.B, self.Hkv, n, self.D), "V")
         need = self.prefill_snapkv_workspace_bytes(n, w)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            workspace = self._new((need,), torch.uint8)
         if workspace.device != self.device or workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace: need {need} bytes on {self.device}")
         check(self._L.kvevict_prefill_snapkv(self.h, layer, _ptr(Q_obs), _ptr(K), _ptr(V), n, w, k_per_head,
@@ -148,8 +161,7 @@ class KVEvictCache:
         if need == 0:
             return None, None, 0
         if workspace is None:
-            with torch.cuda.stream(self.stream):  # so that the allocator hands it on in this stream's order
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            workspace = self._new((need,), torch.uint8)
         size = workspace.numel() * workspace.element_size()
         if workspace.device != self.device or not workspace.is_contiguous() or size < need:
             raise ValueError(f"workspace: need {need} contiguous bytes on {self.device}")
@@ -167,10 +179,10 @@ class KVEvictCache:
         self._dev(K, (self.B, self.Hkv, n, self.D), "K")
         self._dev(V, (self.B, self.Hkv, n, self.D), "V")
         if out is None:
-            out = torch.empty_like(Q)
+            out = self._new(Q.shape, self.dtype)
         self._dev(out, Q.shape, "out")
         if lse is None and return_lse:
-            lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=self.device)
+            lse = self._new(Q.shape[:3], torch.float32)
         if lse is not None:
             self._dev(lse, Q.shape[:3], "lse", torch.float32)
         need = ctypes.c_size_t()
@@ -209,7 +221,7 @@ class KVEvictCache:
         self._dev(k_prefix, (self.Hkv, P, self.D), "k_prefix")
         self._dev(v_prefix, (self.Hkv, P, self.D), "v_prefix")
         if out is None:
-            out = torch.empty((self.B, self.Hq, self.D), dtype=self.dtype, device=self.device)
+            out = self._new((self.B, self.Hq, self.D), self.dtype)
         self._dev(out, (self.B, self.Hq, self.D), "out")
         need = ctypes.c_size_t()
         check(self._L.kvevict_decode_step_shared_workspace_bytes(self.h, P, ctypes.byref(need)),
@@ -225,7 +237,7 @@ class KVEvictCache:
         self._dev(k_new, (self.B, self.Hkv, self.D), "k_new")
         self._dev(v_new, (self.B, self.Hkv, self.D), "v_new")
         if out is None:
-            out = torch.empty((self.B, self.Hq, self.D), dtype=self.dtype, device=self.device)
+            out = self._new((self.B, self.Hq, self.D), self.dtype)
         self._dev(out, (self.B, self.Hq, self.D), "out")
         check(self._L.kvevict_decode_step(self.h, layer, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out)),
               "kvevict_decode_step")
@@ -261,7 +273,7 @@ class KVEvictCache:
     def slot_positions(self, layer: int, out: torch.Tensor | None = None) -> torch.Tensor:
         shp = (self.B, self.Hkv, self.capacity)
         if out is None:
-            out = torch.empty(shp, dtype=torch.int32, device=self.device)
+            out = self._new(shp, torch.int32)
         on_dev = out.device.type == "cuda"
         if on_dev:
             self._dev(out, shp, "out", torch.int32)
@@ -271,7 +283,7 @@ class KVEvictCache:
     def scores(self, layer: int, out: torch.Tensor | None = None) -> torch.Tensor:
         shp = (self.B, self.Hkv, self.capacity)
         if out is None:
-            out = torch.empty(shp, dtype=torch.float32, device=self.device)
+            out = self._new(shp, torch.float32)
         on_dev = out.device.type == "cuda"
         if on_dev:
             self._dev(out, shp, "out", torch.float32)
@@ -283,7 +295,7 @@ class KVEvictCache:
         these fp32 scores [batch][n_kv_heads][C] (-1: no candidate)."""
         self._dev(scores, (self.B, self.Hkv, self.capacity), "scores", torch.float32)
         if out is None:
-            out = torch.empty((self.B, self.Hkv), dtype=torch.int32, device=self.device)
+            out = self._new((self.B, self.Hkv), torch.int32)
         self._dev(out, (self.B, self.Hkv), "out", torch.int32)
         check(self._L.kvevict_select_victims(self.h, layer, _ptr(scores), _ptr(out)), "kvevict_select_victims")
         return out
@@ -323,7 +335,7 @@ class KVEvictCache:
         """Every unit's evicted score mass (fp64, [batch][n_kv_heads])."""
         shp = (self.B, self.Hkv)
         if out is None:
-            out = torch.empty(shp, dtype=torch.float64, device=self.device)
+            out = self._new(shp, torch.float64)
         on_dev = out.device.type == "cuda"
         if on_dev:
             self._dev(out, shp, "out", torch.float64)
@@ -334,7 +346,7 @@ class KVEvictCache:
         """INT8 score storage: every unit's scale (its largest score / 255)."""
         shp = (self.B, self.Hkv)
         if out is None:
-            out = torch.empty(shp, dtype=torch.float32, device=self.device)
+            out = self._new(shp, torch.float32)
         on_dev = out.device.type == "cuda"
         if on_dev:
             self._dev(out, shp, "out", torch.float32)
@@ -345,7 +357,7 @@ class KVEvictCache:
         """Two-pool H2O: 0 recent pool, 1 heavy-hitter pool per slot (where a token is held)."""
         shp = (self.B, self.Hkv, self.capacity)
         if out is None:
-            out = torch.empty(shp, dtype=torch.uint8, device=self.device)
+            out = self._new(shp, torch.uint8)
         on_dev = out.device.type == "cuda"
         if on_dev:
             self._dev(out, shp, "out", torch.uint8)
