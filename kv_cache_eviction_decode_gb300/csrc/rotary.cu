@@ -243,10 +243,14 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_con
     }
 }
 
-bool rot_tensor_ok(const void *x, const void *y, const int64_t (&xs)[3], const int64_t (&ys)[3], int elem)
+// The stride of an axis of one entry is not looked at. Over any other the
+// output's must not be 0: its entries would share a row.
+bool rot_tensor_ok(const void *x, const void *y, const int64_t (&xs)[3], const int64_t (&ys)[3], const int64_t (&sizes)[3], int elem)
 {
     if (!x || !y || (reinterpret_cast<uintptr_t>(x) & 15) || (reinterpret_cast<uintptr_t>(y) & 15)) return false;
     for (int i = 0; i < 3; ++i) {
+        if (sizes[i] <= 1) continue;
+        if (ys[i] == 0) return false;
         if ((xs[i] * elem) % 16 || (ys[i] * elem) % 16) return false;
         if (x == y && xs[i] != ys[i]) return false;
     }
@@ -277,8 +281,9 @@ extern "C" int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream)
     const bool has_q = a->n_q_heads > 0, has_k = a->k != nullptr && a->n_k_heads > 0;
     const long long total = a->batch * a->tokens;
     if (total == 0 || (!has_q && !has_k)) return KVEVICT_OK;
-    if (has_q && !rot_tensor_ok(a->q, a->q_out, a->q_stride, a->q_out_stride, elem)) return KVEVICT_ERR_INVALID_ARG;
-    if (has_k && !rot_tensor_ok(a->k, a->k_out, a->k_stride, a->k_out_stride, elem)) return KVEVICT_ERR_INVALID_ARG;
+    const int64_t qn[3] = {a->batch, a->n_q_heads, a->tokens}, kn[3] = {a->batch, a->n_k_heads, a->tokens};
+    if (has_q && !rot_tensor_ok(a->q, a->q_out, a->q_stride, a->q_out_stride, qn, elem)) return KVEVICT_ERR_INVALID_ARG;
+    if (has_k && !rot_tensor_ok(a->k, a->k_out, a->k_stride, a->k_out_stride, kn, elem)) return KVEVICT_ERR_INVALID_ARG;
     if (a->positions && (reinterpret_cast<uintptr_t>(a->positions) & (a->positions_64 ? 7 : 3))) return KVEVICT_ERR_INVALID_ARG;
     RotParams p{};
     p.x[0] = a->q; p.y[0] = a->q_out;

@@ -150,3 +150,21 @@ def test_offsets_beyond_32_bits(cuda_device):
     assert torch.equal(kv.rotary(x, None, pos, f), want)
     kv.rotary(x, None, pos, f, q_out=x)
     assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_strides_of_single_entries(cuda_device, dtype):
+    """The stride of an axis of one entry says nothing: one token, one head, one sequence, in any strides, also in place
+    through two views that differ in them."""
+    f, _ = kv.rotary_frequencies(64)
+    g = torch.Generator(device="cuda").manual_seed(23)
+    for shape, odd in (((2, 4, 1, 64), 2), ((2, 1, 5, 64), 1), ((1, 4, 5, 64), 0), ((1, 1, 1, 64), 2)):
+        x = torch.randn(shape, generator=g, device="cuda", dtype=dtype)
+        want = kv.rotary(x, None, 9, f)
+        check(want, x, torch.arange(9, 9 + shape[2], device="cuda")[None].expand(shape[0], -1), f, False, 1.0, False)
+        strides = list(x.stride())
+        strides[odd] = 3
+        view = x.as_strided(shape, strides)
+        assert torch.equal(kv.rotary(view, None, 9, f), want)
+        kv.rotary(view, None, 9, f, q_out=x)
+        assert torch.equal(x, want)

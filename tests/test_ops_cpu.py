@@ -176,3 +176,12 @@ def test_frequencies():
                 dict(rotary_dim=64, scaling="other"), dict(rotary_dim=2, scaling="ntk")):
         with pytest.raises(ValueError):
             kv.rotary_frequencies(device="cpu", **bad)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(qos=(10240, 0, 128)), dict(qos=(10240, 1280, 0)), dict(kos=(2560, 1280, 0)), dict(batch=2, qos=(0, 1280, 128)),
+    dict(qo=4096, qs=(10240, 0, 128), qos=(10240, 0, 128)),
+])
+def test_rotary_outputs_that_share_rows_refused(L, bad):
+    """An output stride of 0 over an axis of several entries: they would all write the same row."""
+    assert L.kvevict_rotary(rot(**{"qo": 1 << 20, "ko": 1 << 21, **bad}), None) == -1
