@@ -174,6 +174,7 @@ class KVEvictCache:
         attention under the tokens the policy keeps in view (SINK_WINDOW: sinks
         and the newest n_recent + 1; else every earlier one), then prefill().
         Returns out (as Q), or (out, lse [B][Hq][P] fp32)."""
+        ops._forward_only("prefill_attend", Q, K, V, out)
         n = K.shape[2]
         self._dev(Q, (self.B, self.Hq, n, self.D), "Q")
         self._dev(K, (self.B, self.Hkv, n, self.D), "K")
@@ -214,6 +215,7 @@ class KVEvictCache:
         """decode_step with a prefix that all sequences share in front of the cache,
         k_prefix and v_prefix [Hkv][P][d]: one softmax over prefix, retained tokens
         and the new one (SINK_WINDOW and RANDOM)."""
+        ops._forward_only("decode_step_shared", q, k_new, v_new, k_prefix, v_prefix, out)
         P = k_prefix.shape[1]
         self._dev(q, (self.B, self.Hq, self.D), "q")
         self._dev(k_new, (self.B, self.Hkv, self.D), "k_new")

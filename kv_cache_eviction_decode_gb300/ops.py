@@ -2,7 +2,9 @@
 and marshalling only, every step runs in the library's kernels.
 
 Work is queued on the current stream of the tensors' device. Nothing here
-waits for the GPU, and every call can be captured in a CUDA graph.
+waits for the GPU, and every call can be captured in a CUDA graph. All of them
+are forward only: tensors that require gradients are refused where gradients
+are enabled (the gradient of rotary() is rotary() with inverse=True).
 """
 from __future__ import annotations
 
@@ -48,6 +50,13 @@ def _like(t: torch.Tensor, q: torch.Tensor, dims: int, name: str, shape=None) ->
         raise ValueError(f"{name}: need a {q.dtype} tensor of {dims if shape is None else tuple(shape)} "
                          f"{'axes' if shape is None else ''} on {q.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     raise ValueError(f"{name}: the last axis must be contiguous")
+
+
+def _forward_only(name: str, *tensors) -> None:
+    """Refuses tensors whose gradient would be lost: the operators have no backward pass."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{name}: forward only, there is no backward pass: detach the tensors that require gradients, or call "
+                         f"it under torch.no_grad()")
 
 
 def _ints(t, n: int, q: torch.Tensor, name: str) -> int:
@@ -159,6 +168,8 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sin
     an output made here they hold anything). Lengths and starts out of range are
     clamped and set the bit 0x10 of error_word (int32 on the device).
     """
+    if q.requires_grad or k.requires_grad or v.requires_grad or (out is not None and out.requires_grad):
+        _forward_only("window_attention", q, k, v, out)
     packed = q_starts is not None
     key = (q.dtype, k.dtype, v.dtype, q.get_device(), k.get_device(), v.get_device(), q.shape, k.shape, v.shape, q.stride(),
            k.stride(), v.stride(), n_sink, window, scale, max_q, max_k, q_starts.shape if packed else None)
@@ -237,6 +248,9 @@ def shared_prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: t
     [B][Hkv][M][d], of kv_lens rows (int32 [B] on the device; None: M). The
     prefix is read once for the batch. P and M may be 0. Returns out (as q), or
     (out, lse [B][Hq])."""
+    if q.requires_grad or k_prefix.requires_grad or v_prefix.requires_grad or k.requires_grad or v.requires_grad or \
+            (out is not None and out.requires_grad):
+        _forward_only("shared_prefix_attention", q, k_prefix, v_prefix, k, v, out)
     key = (q.dtype, k.dtype, v.dtype, k_prefix.dtype, v_prefix.dtype, q.get_device(), k.get_device(), v.get_device(),
            k_prefix.get_device(), v_prefix.get_device(), q.shape, k.shape, v.shape, k_prefix.shape, v_prefix.shape, q.stride(),
            k.stride(), v.stride(), k_prefix.stride(), v_prefix.stride(), scale)
@@ -328,6 +342,8 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
     token's position. inv_freq: fp64 on the device (rotary_frequencies).
     q_out / k_out may be q / k: in place. inverse: by the negative angle, the
     gradient of the forward call. Returns (q_out, k_out), or q_out without k."""
+    if q.requires_grad or (k is not None and k.requires_grad) or q_out is not None or k_out is not None:
+        _forward_only("rotary", q, k, q_out, k_out)
     key = (q.dtype, q.get_device(), q.shape, q.stride(), None if k is None else (k.dtype, k.get_device(), k.shape, k.stride()),
            None if isinstance(positions, int) else (positions.dtype, positions.get_device(), positions.shape, positions.stride()),
            inv_freq.shape, interleaved, inverse)

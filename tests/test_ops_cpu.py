@@ -185,3 +185,36 @@ def test_frequencies():
 def test_rotary_outputs_that_share_rows_refused(L, bad):
     """An output stride of 0 over an axis of several entries: they would all write the same row."""
     assert L.kvevict_rotary(rot(**{"qo": 1 << 20, "ko": 1 << 21, **bad}), None) == -1
+
+
+def test_inputs_that_require_gradients_refused():
+    """The operators have no backward pass: an output without a graph would lose the gradient without a word."""
+    import kv_cache_eviction_decode_gb300 as kv
+    q = torch.zeros(1, 2, 3, 64)
+    w = torch.zeros(1, 2, 3, 64, requires_grad=True)
+    f = torch.zeros(32, dtype=torch.float64)
+    for call in (lambda x: kv.window_attention(x, q, q), lambda x: kv.window_attention(q, x, q), lambda x: kv.window_attention(q, q, x),
+                 lambda x: kv.window_attention(q, q, q, out=x), lambda x: kv.rotary(x, None, 0, f), lambda x: kv.rotary(q, x, 0, f),
+                 lambda x: kv.rotary(q, None, 0, f, q_out=x), lambda x: kv.rotary(q, q, 0, f, k_out=x),
+                 lambda x: kv.shared_prefix_attention(x[0], q[0], q[0], q, q), lambda x: kv.shared_prefix_attention(q[0], x[0], q[0], q, q),
+                 lambda x: kv.shared_prefix_attention(q[0], q[0], x[0], q, q), lambda x: kv.shared_prefix_attention(q[0], q[0], q[0], x, q),
+                 lambda x: kv.shared_prefix_attention(q[0], q[0], q[0], q, x),
+                 lambda x: kv.shared_prefix_attention(q[0], q[0], q[0], q, q, out=x[0])):
+        with pytest.raises(ValueError, match="no backward"):
+            call(w)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # the next check
+            call(w)
+
+
+def test_cache_inputs_that_require_gradients_refused():
+    from kv_cache_eviction_decode_gb300 import KVEvictCache
+    c = object.__new__(KVEvictCache)
+    c.B, c.Hq, c.Hkv, c.D, c.dtype, c.device = 1, 2, 2, 64, torch.float32, torch.device("cpu")
+    q = torch.zeros(1, 2, 3, 64)
+    w = torch.zeros(1, 2, 3, 64, requires_grad=True)
+    for i in range(3):
+        with pytest.raises(ValueError, match="no backward"):
+            c.prefill_attend(0, *(w if j == i else q for j in range(3)))
+    for i in range(5):
+        with pytest.raises(ValueError, match="no backward"):
+            c.decode_step_shared(0, *((w if j == i else q)[:, :, 0] if j < 3 else (w if j == i else q)[0] for j in range(5)))
