@@ -15,7 +15,9 @@
  *
  * Tensors have their last axis (head_dim) contiguous; every other axis has a
  * stride of its own, in elements, given in the order sequence, head, token.
- * Base addresses are 16-byte aligned and strides multiples of 16 bytes.
+ * Base addresses are 16-byte aligned and strides positive multiples of 16 bytes
+ * (the inputs of kvevict_rotary: any multiples). The stride of an axis of one
+ * entry is not looked at.
  */
 #ifndef KVEVICT_OPS_H
 #define KVEVICT_OPS_H
@@ -148,9 +150,9 @@ int kvevict_shared_prefix_attention(const kvevict_shared_prefix_args *a, void *c
  * the other.
  *   dtype:     KVEVICT_F32 or KVEVICT_BF16; computed in fp32.
  *   head_dim:  a multiple of 8, at most 1024; rotary_dim even, 2 .. head_dim.
- *   q, q_out:  [batch][n_q_heads][tokens], any strides (q_out's not 0); q_out may be q
- *              itself (with q's strides: in place), else must not overlap it. k, k_out
- *              likewise with n_k_heads; k NULL: queries only.
+ *   q, q_out:  [batch][n_q_heads][tokens], any strides (q_out's not 0);
+ *              q_out may be q itself (with q's strides: in place), else must not
+ *              overlap it. k, k_out likewise with n_k_heads; k NULL: queries only.
  *   positions: device, int64 (positions_64 = 1) or int32, element
  *              [b * pos_stride[0] + token * pos_stride[1]]; any value,
  *              negative ones too. NULL: pos_start + token for every sequence.

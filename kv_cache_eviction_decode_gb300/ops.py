@@ -52,6 +52,15 @@ def _like(t: torch.Tensor, q: torch.Tensor, dims: int, name: str, shape=None) ->
     raise ValueError(f"{name}: the last axis must be contiguous")
 
 
+def _strides(t: torch.Tensor, name: str, least: int = 1) -> None:
+    """Over axes of several entries the strides are positive (0 for tensors that are only read by rotary) multiples of
+    16 bytes."""
+    for size, stride in zip(t.shape[:-1], t.stride()):
+        if size > 1 and (stride < least or stride * t.element_size() % 16) and t.numel() > 0:
+            raise ValueError(f"{name}: need strides that are {'positive ' if least else ''}multiples of 16 bytes, got {stride} elements over "
+                             f"an axis of {size} (expanded tensors and rows off 16-byte boundaries have to be made contiguous)")
+
+
 def _forward_only(name: str, *tensors) -> None:
     """Refuses tensors whose gradient would be lost: the operators have no backward pass."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
@@ -80,6 +89,7 @@ def _outputs(q, out, lse, return_lse, lse_shape):
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
         _like(out, q, q.dim(), "out", q.shape)
+        _strides(out, "out")
     if lse is None:
         if return_lse:
             lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
@@ -161,7 +171,9 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sin
     Padded: q [B][Hq][N][d], k and v [B][Hkv][M][d]; q_lens and kv_lens (int32
     [B] on the device) say how many rows are real. Packed (q_starts and
     k_starts, int32 [B + 1] on the device, with max_q and max_k the longest
-    sequences): q [T][Hq][d], k and v [S][Hkv][d]. Any strides, d contiguous.
+    sequences): q [T][Hq][d], k and v [S][Hkv][d]. d is contiguous, the other
+    axes have any strides that are positive multiples of 16 bytes (so no expanded
+    tensors); out overlaps no input.
     Returns out (as q), or (out, lse) with return_lse or an lse tensor: fp32
     [B][Hq][N], or [T][Hq] packed. A row that sees nothing gives 0 and -inf.
     Rows behind q_lens, outside the starts or beyond max_q are not written (in
@@ -202,6 +214,9 @@ def _window_layout(q, k, v, n_sink, window, scale, q_starts, max_q, max_k) -> _L
     _like(q, q, dims, "q")
     _like(k, q, dims, "k")
     _like(v, q, dims, "v", k.shape)
+    if q.numel() > 0:  # (else nothing is read)
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            _strides(t, name)
     if window is None:
         window = 0
     elif window < 1:
@@ -273,6 +288,9 @@ def _shared_layout(q, k_prefix, v_prefix, k, v, scale) -> _Layout:
     _like(v_prefix, q, 3, "v_prefix", k_prefix.shape)
     _like(k, q, 4, "k")
     _like(v, q, 4, "v", k.shape)
+    if q.numel() > 0:  # (else nothing is read)
+        for t, name in ((q, "q"), (k_prefix, "k_prefix"), (v_prefix, "v_prefix"), (k, "k"), (v, "v")):
+            _strides(t, name)
     B, Hq, d = q.shape
     Hkv, M = k.shape[1], k.shape[2]
     if k.shape[0] != B or k.shape[3] != d or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != d:
@@ -357,10 +375,12 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         _like(q_out, q, dims, "q_out", q.shape)
+        _strides(q_out, "q_out")
         if k is not None:
             if k_out is None:
                 k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
             _like(k_out, q, dims, "k_out", k.shape)
+            _strides(k_out, "k_out")
         strides = _Q12.pack(*_heads(q), *_heads(q_out), *((0,) * 6 if k is None else (*_heads(k), *_heads(k_out))))
     if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq: need a contiguous float64 vector on {q.device}")
@@ -383,6 +403,7 @@ def _rotary_layout(q, k, positions, inv_freq, interleaved, inverse) -> _Layout:
     if dims not in (3, 4):
         raise ValueError(f"q: need [T][H][d] or [B][H][N][d], got {tuple(q.shape)}")
     _like(q, q, dims, "q")
+    _strides(q, "q", 0)
     d = q.shape[-1]
     if dims == 3:
         B, N, Hq = 1, q.shape[0], q.shape[1]
@@ -393,6 +414,7 @@ def _rotary_layout(q, k, positions, inv_freq, interleaved, inverse) -> _Layout:
     Hk = 0
     if k is not None:
         _like(k, q, dims, "k")
+        _strides(k, "k", 0)
         Hk = k.shape[1]
         if k.shape[-1] != d or k.shape[0] != q.shape[0] or (dims == 4 and k.shape[2] != N):
             raise ValueError(f"k: {tuple(k.shape)} does not go with q {tuple(q.shape)}")

@@ -218,3 +218,56 @@ def test_cache_inputs_that_require_gradients_refused():
     for i in range(5):
         with pytest.raises(ValueError, match="no backward"):
             c.decode_step_shared(0, *((w if j == i else q)[:, :, 0] if j < 3 else (w if j == i else q)[0] for j in range(5)))
+
+
+@pytest.fixture
+def as_if_on_gpu(monkeypatch, L):
+    """Lets the binding's checks see CPU tensors as the device's; what passes them all would launch, and stops here."""
+    from kv_cache_eviction_decode_gb300 import ops
+    monkeypatch.setattr(ops, "_dtype", lambda t, name: ops._DT[t.dtype])
+
+    def launch(*a):
+        raise RuntimeError("launched")
+    monkeypatch.setattr(ops, "_call", launch)
+    monkeypatch.setattr(ops, "_layouts", {})
+
+
+BAD_STRIDES = {"expanded": lambda t: t[:, :1].expand(t.shape), "unaligned": lambda t: torch.empty(*t.shape[:-1], 67).bfloat16()[..., :64]}
+
+
+@pytest.mark.parametrize("how", list(BAD_STRIDES))
+def test_strides_refused_by_name(as_if_on_gpu, how):
+    """Expanded tensors, and rows that start off a 16-byte boundary: refused with the tensor's name."""
+    import kv_cache_eviction_decode_gb300 as kv
+    bad = BAD_STRIDES[how]
+    q, k, p, s = (torch.zeros(x, dtype=torch.bfloat16) for x in ((2, 4, 3, 64), (2, 2, 9, 64), (2, 5, 64), (2, 4, 64)))
+    f = torch.zeros(32, dtype=torch.float64)
+    starts = torch.zeros(3, dtype=torch.int32)
+    packed = dict(q_starts=starts, k_starts=starts, max_q=1, max_k=1)
+    for name, call in (("q", lambda: kv.window_attention(bad(q), k, k)), ("k", lambda: kv.window_attention(q, bad(k), k)),
+                       ("v", lambda: kv.window_attention(q, k, bad(k))), ("out", lambda: kv.window_attention(q, k, k, out=bad(q))),
+                       ("v", lambda: kv.window_attention(s, p, bad(p), **packed)), ("k", lambda: kv.window_attention(s, bad(p), p, **packed)),
+                       ("q", lambda: kv.shared_prefix_attention(bad(s), p, p, k, k)),
+                       ("k_prefix", lambda: kv.shared_prefix_attention(s, bad(p), p, k, k)),
+                       ("v_prefix", lambda: kv.shared_prefix_attention(s, p, bad(p), k, k)),
+                       ("k", lambda: kv.shared_prefix_attention(s, p, p, bad(k), k)), ("v", lambda: kv.shared_prefix_attention(s, p, p, k, bad(k))),
+                       ("out", lambda: kv.shared_prefix_attention(s, p, p, k, k, out=bad(s))),
+                       ("q_out", lambda: kv.rotary(q, None, 0, f, q_out=bad(q))), ("k_out", lambda: kv.rotary(q, q, 0, f, k_out=bad(q)))):
+        with pytest.raises(ValueError, match=f"^{name}: .*16 bytes"):
+            call()
+    if how == "unaligned":
+        for name, call in (("q", lambda: kv.rotary(bad(q), None, 0, f)), ("k", lambda: kv.rotary(q, bad(q), 0, f))):
+            with pytest.raises(ValueError, match=f"^{name}: .*16 bytes"):
+                call()
+
+
+def test_strides_accepted(as_if_on_gpu):
+    """Axes of one entry in any stride, tensors without entries, and (rotary only reads them) expanded inputs."""
+    import kv_cache_eviction_decode_gb300 as kv
+    q, k, f = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 9, 64, dtype=torch.bfloat16), torch.zeros(32, dtype=torch.float64)
+    odd = torch.zeros(1000, dtype=torch.bfloat16).as_strided((2, 4, 1, 64), (256, 64, 3, 1))
+    none = torch.zeros(2, 1, 1, 64, dtype=torch.bfloat16).expand(2, 2, 9, 64)[:, :, :0]
+    for call in (lambda: kv.window_attention(odd, k, k), lambda: kv.window_attention(q, none, none), lambda: kv.window_attention(q, k, k, out=odd),
+                 lambda: kv.rotary(odd, odd[:, :1].expand(2, 4, 1, 64), 0, f, q_out=odd)):
+        with pytest.raises(RuntimeError, match="launched"):
+            call()
