@@ -10,7 +10,7 @@
  * current one. As with kvevict.h, argument errors are found on the host
  * before anything is launched and returned as a negative kvevict_status;
  * anomalies found on the GPU set bits of a device error word, here one that
- * the caller may pass. No call allocates device memory or waits for the GPU;
+ * the caller may pass, else the device's, which kvevict_operator_errors reads. No call allocates device memory or waits for the GPU;
  * each can be captured in a CUDA graph.
  *
  * Tensors have their last axis (head_dim) contiguous; every other axis has a
@@ -86,7 +86,7 @@ extern "C" {
  *              may overlap on the GPU need one each.
  *   error_word: device uint32 that error bits are OR-ed into (BAD_LENGTH, and
  *              WAIT_TIMEOUT: a pipeline wait gave up, the results are not valid),
- *              or NULL.
+ *              or NULL: then into the device's (kvevict_operator_errors).
  */
 typedef struct {
     int32_t dtype, head_dim, n_q_heads, n_kv_heads, batch, n_sink, window;
@@ -109,6 +109,13 @@ typedef struct {
  * or strides. */
 int kvevict_window_attention_workspace_bytes(const kvevict_attention_args *a, size_t *bytes);
 int kvevict_window_attention(const kvevict_attention_args *a, void *cuda_stream);
+
+/*
+ * The error bits that calls without an error_word have set on the current
+ * device since the last time; waits for the device, and clears them. OK,
+ * DEVICE where there are any, CUDA; INVALID_ARG for NULL. Not while a stream of
+ * the device is being captured. */
+int kvevict_operator_errors(uint32_t *device_error);
 
 /*
  * Decode attention, one token of every sequence, over a prefix that all

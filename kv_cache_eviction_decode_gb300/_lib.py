@@ -15,7 +15,7 @@ H2O, SINK_WINDOW, RANDOM, H2O_BLOCK, H2O_POOLS = 0, 1, 2, 3, 4
 F32, BF16 = 0, 1
 
 OK, ERR_INVALID_ARG, ERR_CAPACITY, ERR_STATE, ERR_CUDA, ERR_DEVICE = 0, -1, -2, -3, -4, -5
-DEV_NONFINITE, DEV_NO_CANDIDATE, DEV_WAIT_TIMEOUT, DEV_BAD_SLOT = 0x1, 0x2, 0x4, 0x8
+DEV_NONFINITE, DEV_NO_CANDIDATE, DEV_WAIT_TIMEOUT, DEV_BAD_SLOT, DEV_BAD_LENGTH = 0x1, 0x2, 0x4, 0x8, 0x10
 
 
 class Config(ctypes.Structure):
@@ -98,6 +98,8 @@ def lib() -> ctypes.CDLL:
             for n in ("kvevict_window_attention_workspace_bytes", "kvevict_shared_prefix_attention_workspace_bytes"):
                 getattr(L, n).argtypes = [ctypes.c_char_p, ctypes.POINTER(SZ)]
                 getattr(L, n).restype = I
+            L.kvevict_operator_errors.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
+            L.kvevict_operator_errors.restype = I
             L.kvevict_prefill_attend_workspace_bytes.argtypes = [P, I, ctypes.POINTER(SZ)]
             L.kvevict_prefill_attend.argtypes = [P, I, P, P, P, I, P, P, P, SZ]
             L.kvevict_decode_step_shared_workspace_bytes.argtypes = [P, I, ctypes.POINTER(SZ)]

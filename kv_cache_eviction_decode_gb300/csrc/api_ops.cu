@@ -429,6 +429,18 @@ extern "C" int kvevict_window_attention(const kvevict_attention_args *a, void *c
     return run(a, w, static_cast<cudaStream_t>(cuda_stream));
 }
 
+extern "C" int kvevict_operator_errors(uint32_t *device_error)
+{
+    if (!device_error) return KVEVICT_ERR_INVALID_ARG;
+    uint32_t tc = 0, f32 = 0;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = attn_tc_errors(&tc);
+    if (e == cudaSuccess) e = attn_f32_errors(&f32);
+    if (e != cudaSuccess) return KVEVICT_ERR_CUDA;
+    *device_error = tc | f32;
+    return *device_error ? KVEVICT_ERR_DEVICE : KVEVICT_OK;
+}
+
 extern "C" int kvevict_shared_prefix_attention_workspace_bytes(const kvevict_shared_prefix_args *s, size_t *bytes)
 {
     int rc = check_shared(s);

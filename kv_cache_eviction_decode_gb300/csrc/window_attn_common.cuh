@@ -11,9 +11,18 @@
 
 namespace kvevict {
 
-__device__ __forceinline__ void attn_flag(uint32_t *err, uint32_t bit)
+// The errors of calls that give no word of their own; one a translation unit
+// with kernels, read by kvevict_operator_errors.
+static __device__ uint32_t g_attn_errors;
+
+__device__ __forceinline__ void attn_flag(uint32_t *err, uint32_t bit) { atomicOr(err ? err : &g_attn_errors, bit); }
+
+// Reads and clears this translation unit's word on the current device.
+static inline cudaError_t attn_take_errors(uint32_t *bits)
 {
-    if (err) atomicOr(err, bit);
+    const uint32_t none = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_attn_errors, sizeof none);
+    return e == cudaSuccess ? cudaMemcpyToSymbol(g_attn_errors, &none, sizeof none) : e;
 }
 
 __host__ __device__ __forceinline__ int attn_min(int a, int b) { return a < b ? a : b; }

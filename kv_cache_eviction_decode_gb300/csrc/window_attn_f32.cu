@@ -343,4 +343,6 @@ cudaError_t launch_attn_join(const AttnParams &p, int head_dim, bool bf16, cudaS
     return head_dim == 64 ? launch_join<float, 64>(p, st) : launch_join<float, 128>(p, st);
 }
 
+cudaError_t attn_f32_errors(uint32_t *bits) { return attn_take_errors(bits); }
+
 }  // namespace kvevict

@@ -944,4 +944,6 @@ cudaError_t launch_attn_tc(const AttnTcParams &p, int head_dim, cudaStream_t st)
     return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
 }
 
+cudaError_t attn_tc_errors(uint32_t *bits) { return attn_take_errors(bits); }
+
 }  // namespace kvevict

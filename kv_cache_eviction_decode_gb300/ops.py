@@ -14,7 +14,7 @@ import struct
 
 import torch
 
-from ._lib import BF16, F32, OK, check, lib
+from ._lib import BF16, ERR_DEVICE, F32, OK, check, lib
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -117,6 +117,19 @@ def _error_word(t, q: torch.Tensor) -> int:
     return t.data_ptr()
 
 
+def operator_errors(device=None) -> int:
+    """Waits for the device (None: the current one); returns the error bits that calls without an error_word have set
+    on it since the last time (0: clean; DEV_BAD_LENGTH, DEV_WAIT_TIMEOUT), and clears them."""
+    if device is not None and torch.device(device).type != "cuda":
+        raise ValueError(f"operator_errors: need a CUDA device, got {device}")
+    w = ctypes.c_uint32(0)
+    with torch.cuda.device(device):
+        rc = lib().kvevict_operator_errors(w)
+    if rc not in (OK, ERR_DEVICE):
+        check(rc, "kvevict_operator_errors")
+    return w.value
+
+
 _entry = {}  # the library's entry points, looked up once
 
 
@@ -178,7 +191,8 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sin
     [B][Hq][N], or [T][Hq] packed. A row that sees nothing gives 0 and -inf.
     Rows behind q_lens, outside the starts or beyond max_q are not written (in
     an output made here they hold anything). Lengths and starts out of range are
-    clamped and set the bit 0x10 of error_word (int32 on the device).
+    clamped and set DEV_BAD_LENGTH in error_word (int32 on the device; None: see
+    operator_errors).
     """
     if q.requires_grad or k.requires_grad or v.requires_grad or (out is not None and out.requires_grad):
         _forward_only("window_attention", q, k, v, out)

@@ -95,3 +95,30 @@ def test_more_queries_than_rows(cuda_device, m, dtype):
     out, lse = kv.window_attention(q, k, v, q_lens=torch.tensor([given], dtype=torch.int32, device="cuda"), error_word=err, return_lse=True)
     assert int(err) == 0x10
     check_rows(*(x[0].transpose(0, 1) for x in (q, k, v, out)), lse[0].t(), 0, n, 0, m, n_given=given)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_errors_without_a_word_of_the_callers(cuda_device, dtype):
+    """They are kept on the device until they are asked for."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+    q = torch.randn(2, 4, 3, 64, generator=g, device="cuda", dtype=dtype)
+    k, v = (torch.randn(2, 2, 20, 64, generator=g, device="cuda", dtype=dtype) for _ in range(2))
+    good, bad = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([20, 7], [20, 70]))
+    assert kv.operator_errors() == 0
+    kv.window_attention(q, k, v, kv_lens=good)
+    assert kv.operator_errors() == 0
+    kv.window_attention(q, k, v, kv_lens=bad)
+    kv.window_attention(q, k, v, kv_lens=good)
+    assert kv.operator_errors() == kv.DEV_BAD_LENGTH and kv.operator_errors() == 0
+    kv.shared_prefix_attention(q[:, :, 0], k[0], v[0], k, v, bad)
+    assert kv.operator_errors(q.device) == kv.DEV_BAD_LENGTH and kv.operator_errors() == 0
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv.window_attention(q, k, v, kv_lens=bad, error_word=err)
+    assert int(err) == kv.DEV_BAD_LENGTH and kv.operator_errors() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv.window_attention(q, k, v, kv_lens=good)
+    assert kv.operator_errors() == 0
+    good.copy_(bad)
+    graph.replay()
+    assert kv.operator_errors() == kv.DEV_BAD_LENGTH

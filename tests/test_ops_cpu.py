@@ -271,3 +271,10 @@ def test_strides_accepted(as_if_on_gpu):
                  lambda: kv.rotary(odd, odd[:, :1].expand(2, 4, 1, 64), 0, f, q_out=odd)):
         with pytest.raises(RuntimeError, match="launched"):
             call()
+
+
+def test_operator_errors_refused(L):
+    import kv_cache_eviction_decode_gb300 as kv
+    assert L.kvevict_operator_errors(None) == -1
+    with pytest.raises(ValueError, match="CUDA"):
+        kv.operator_errors("cpu")
