@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -19,6 +20,34 @@ constexpr int kSMs = 152;
 constexpr int64_t kMaxRows = int64_t{1} << 30;
 constexpr int kMaxGroup = 64;
 constexpr int kMaxParts = 64;  // parts a unit's keys are split into at most
+
+// The errors of calls that give no word of their own. (The kernels get one in
+// any case: with a test for null beside each of their waits a causal prompt of
+// 8192, 32 heads over 8, took 404 us, without 396.)
+__device__ uint32_t g_errors;
+
+// Its address on the current device, looked up once; also during a capture,
+// where the lookup may have to load the library's kernels first.
+cudaError_t errors_address(uint32_t **out)
+{
+    static std::atomic<uint32_t *> known[256] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    void *p = dev < 256 ? known[dev].load() : nullptr;
+    if (!p) {
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        e = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return e;
+        e = cudaGetSymbolAddress(&p, g_errors);
+        const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e == cudaSuccess) e = back;
+        if (e != cudaSuccess) return e;
+        if (dev < 256) known[dev].store(static_cast<uint32_t *>(p));
+    }
+    *out = static_cast<uint32_t *>(p);
+    return cudaSuccess;
+}
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -364,7 +393,8 @@ int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
     p.lse = a->lse;
     p.err = a->error_word;
     const bool bf16 = a->dtype == KVEVICT_BF16;
-    cudaError_t e;
+    cudaError_t e = p.err ? cudaSuccess : errors_address(&p.err);
+    if (e != cudaSuccess) return KVEVICT_ERR_CUDA;
     if (w.tensor) {
         for (int i = 0; i < p.n_problems; ++i) {
             const int rc = make_maps(w.tc.maps[i], p.pr[i], p.G, p.Hkv, a->head_dim);
@@ -432,12 +462,13 @@ extern "C" int kvevict_window_attention(const kvevict_attention_args *a, void *c
 extern "C" int kvevict_operator_errors(uint32_t *device_error)
 {
     if (!device_error) return KVEVICT_ERR_INVALID_ARG;
-    uint32_t tc = 0, f32 = 0;
-    cudaError_t e = cudaDeviceSynchronize();
-    if (e == cudaSuccess) e = attn_tc_errors(&tc);
-    if (e == cudaSuccess) e = attn_f32_errors(&f32);
+    const uint32_t none = 0;
+    uint32_t *word = nullptr;
+    cudaError_t e = errors_address(&word);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpy(device_error, word, sizeof none, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess) e = cudaMemcpy(word, &none, sizeof none, cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return KVEVICT_ERR_CUDA;
-    *device_error = tc | f32;
     return *device_error ? KVEVICT_ERR_DEVICE : KVEVICT_OK;
 }
 

@@ -39,7 +39,7 @@ struct AttnParams {
     float *part_l;      // [slots][rows] log2 normalisers, where slots > 1
     long long rows;     // query rows in all
     int slots;
-    uint32_t *err;      // null: the word of the kernel's own that the functions below read
+    uint32_t *err;
 };
 
 constexpr int kAttnF32Rows = 64, kAttnF32FewRows = 16, kAttnF32Keys = 64, kAttnF32FewKeys = 32;
@@ -66,8 +66,5 @@ cudaError_t launch_attn_tc(const AttnTcParams &p, int head_dim, cudaStream_t st)
 cudaError_t launch_attn_f32(const AttnParams &p, int head_dim, bool few, cudaStream_t st);
 // Joins the slots: out = sum_s 2^(l_s - l) o_s, l = log2 sum_s 2^(l_s).
 cudaError_t launch_attn_join(const AttnParams &p, int head_dim, bool bf16, cudaStream_t st);
-// Read and clear the errors of calls without an error word, on the current device.
-cudaError_t attn_tc_errors(uint32_t *bits);
-cudaError_t attn_f32_errors(uint32_t *bits);
 
 }  // namespace kvevict

@@ -11,19 +11,7 @@
 
 namespace kvevict {
 
-// The errors of calls that give no word of their own; one a translation unit
-// with kernels, read by kvevict_operator_errors.
-static __device__ uint32_t g_attn_errors;
-
-__device__ __forceinline__ void attn_flag(uint32_t *err, uint32_t bit) { atomicOr(err ? err : &g_attn_errors, bit); }
-
-// Reads and clears this translation unit's word on the current device.
-static inline cudaError_t attn_take_errors(uint32_t *bits)
-{
-    const uint32_t none = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_attn_errors, sizeof none);
-    return e == cudaSuccess ? cudaMemcpyToSymbol(g_attn_errors, &none, sizeof none) : e;
-}
+__device__ __forceinline__ void attn_flag(uint32_t *err, uint32_t bit) { atomicOr(err, bit); }
 
 __host__ __device__ __forceinline__ int attn_min(int a, int b) { return a < b ? a : b; }
 __host__ __device__ __forceinline__ int attn_max(int a, int b) { return a > b ? a : b; }
@@ -66,13 +54,13 @@ __host__ __device__ __forceinline__ AttnSeq attn_sequence(const AttnProblem &p, 
 {
     AttnSeq s;
     s.bad = false;
-    long long given;  // queries from the first row to the end given
+    int given;  // queries from the first row to the end given
     if (p.q_starts) {
         const int a0 = p.q_starts[b], a1 = p.q_starts[b + 1], c0 = p.k_starts[b], c1 = p.k_starts[b + 1];
         s.q0 = attn_min(attn_max(a0, 0), p.q_rows);
-        const int q1 = attn_min(attn_max(a1, s.q0), p.q_rows);
+        given = attn_max(a1, s.q0) - s.q0;
+        const int q1 = attn_min(s.q0 + given, p.q_rows);
         s.n = attn_min(q1 - s.q0, p.max_q);
-        given = static_cast<long long>(a1) - s.q0;
         s.k0 = attn_min(attn_max(c0, 0), p.k_rows);
         const int k1 = attn_min(attn_max(c1, s.k0), p.k_rows);
         s.m = k1 - s.k0;
@@ -87,11 +75,10 @@ __host__ __device__ __forceinline__ AttnSeq attn_sequence(const AttnProblem &p, 
         s.n = attn_min(attn_max(n, 0), p.q_rows);
         s.m = attn_min(attn_max(m, 0), p.k_rows);
         s.bad = s.n != n || s.m != m;
-        given = n;
+        given = attn_max(n, 0);
     }
     // (a position below -2^30 sees nothing, nor does any of the 2^30 rows behind it)
-    given = given < 0 ? 0 : given;
-    s.p0 = s.m - given < -(1ll << 30) ? -(1 << 30) : static_cast<int>(s.m - given);
+    s.p0 = attn_max(s.m - given, -(1 << 30));
     return s;
 }
 

@@ -87,13 +87,13 @@ __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f3
     const int tile = item % p.q_tiles;
     const int unit = item / p.q_tiles;
     const int b = unit / ap.Hkv, kvh = unit - b * ap.Hkv;
-    bool sound = true;
+    AttnSeq sq = attn_sequence(p, b, true);
     if (p.q_starts) {
+        // (1,024 sequences of up to two tokens, 8 heads, the dearest case seen: 92 us, 85 without this)
         bool falls = false;
         for (int j = threadIdx.x; j <= b; j += kThreadsF32) falls = falls || attn_falls(p, j);
-        sound = !__syncthreads_or(falls);
+        if (__syncthreads_or(falls)) sq = attn_sequence(p, b, false);
     }
-    const AttnSeq sq = attn_sequence(p, b, sound);
     if (sq.bad && threadIdx.x == 0) attn_flag(ap.err, KVEVICT_DEV_BAD_LENGTH);
     const int per = R / G;          // tokens of a tile
     const int t0 = tile * per;
@@ -342,7 +342,5 @@ cudaError_t launch_attn_join(const AttnParams &p, int head_dim, bool bf16, cudaS
     if (bf16) return head_dim == 64 ? launch_join<__nv_bfloat16, 64>(p, st) : launch_join<__nv_bfloat16, 128>(p, st);
     return head_dim == 64 ? launch_join<float, 64>(p, st) : launch_join<float, 128>(p, st);
 }
-
-cudaError_t attn_f32_errors(uint32_t *bits) { return attn_take_errors(bits); }
 
 }  // namespace kvevict

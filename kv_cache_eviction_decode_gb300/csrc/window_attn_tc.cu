@@ -36,6 +36,7 @@
 // sinks and a window of 1021: 155 us; a token of 32 sequences over 2,048 keys, 64
 // query heads over 8: 66 us, 4.1 TB/s with the join.
 #include <atomic>
+#include <climits>
 #include <cmath>
 
 #include "launch.h"
@@ -943,7 +944,5 @@ cudaError_t launch_attn_tc(const AttnTcParams &p, int head_dim, cudaStream_t st)
 {
     return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
 }
-
-cudaError_t attn_tc_errors(uint32_t *bits) { return attn_take_errors(bits); }
 
 }  // namespace kvevict
