@@ -164,9 +164,10 @@ int kvevict_shared_prefix_attention(const kvevict_shared_prefix_args *a, void *c
  *              [b * pos_stride[0] + token * pos_stride[1]]; any value,
  *              negative ones too. NULL: pos_start + token for every sequence.
  *   inv_freq:  device fp64 [rotary_dim / 2], radians per position, finite.
- *              The angle is formed as a 64-bit binary fraction of a turn
- *              (position times frequency modulo 2^64), so its error is below
- *              2^-53 turns times |pos| and far positions keep full accuracy.
+ *              The angle is formed as a 64-bit binary fraction of a turn, the
+ *              frequency's (from an fp64 product) times the position modulo 2^64.
+ *              Its error is below 2^-52 |inv_freq / 2 pi| + 2^-64 turns times
+ *              |pos|: for inv_freq <= 1 less than 2^-54 turns a position.
  */
 typedef struct {
     int32_t dtype, head_dim, rotary_dim, interleaved, inverse, positions_64;

@@ -5,10 +5,11 @@
 // is the same for every head, so a CTA takes one token, forms its cosines and
 // sines once in shared memory and applies them to all heads of q and k. The
 // angle itself is formed in turns as a 64-bit binary fraction: with F =
-// round(inv_freq / 2 pi * 2^64), pos * F mod 2^64 is the angle modulo one turn,
-// exactly up to F's own rounding -- an integer multiply does the range
-// reduction, for any position, where an fp32 product would have lost the
-// fraction past a few thousand turns.
+// round(inv_freq / 2 pi * 2^64), pos * F mod 2^64 is the angle modulo one turn
+// but for F's error -- an integer multiply does the range reduction, for any
+// position, where an fp32 product would have lost the fraction past a few
+// thousand turns. F's error is that of the fp64 product inv_freq * (1 / 2 pi),
+// 1.6 * 2^-53 of it at most, and that of its last bit, 2^-64 at most.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -168,3 +168,24 @@ def test_strides_of_single_entries(cuda_device, dtype):
         assert torch.equal(kv.rotary(view, None, 9, f), want)
         kv.rotary(view, None, 9, f, q_out=x)
         assert torch.equal(x, want)
+
+
+def test_angle_error_grows_with_the_frequency(cuda_device):
+    """The fraction of a turn per position comes from one fp64 product with a rounded 1 / 2 pi: off by at most 2^-53 for the
+    rounding and 0.557 * 2^-53 for the constant, relative, and by 2^-64 for its own last bit; that times the position.
+    Frequencies picked where the product rounds badly, against exact fractions."""
+    from fractions import Fraction
+    inv_2pi = Fraction(10**100, 2 * 31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679)
+    freqs = [float.fromhex(x) for x in ("0x1.ffe300998c775p-1", "0x1.91d6b0e0f714ap+2", "0x1.3fa61ea9c18cdp+3", "0x1.8f4bc22623ca6p+6")]
+    positions = [1, 2**20 + 7, 2**33 + 11, -2**33 - 5]
+    f = torch.tensor(freqs, dtype=torch.float64, device="cuda")
+    x = torch.randn(1, 3, 4, 8, device="cuda", generator=torch.Generator(device="cuda").manual_seed(29))
+    got = kv.rotary(x, None, torch.tensor([positions], device="cuda"), f).double()
+    turns = torch.tensor([[float(Fraction(p) * Fraction(w) * inv_2pi % 1) for w in freqs] for p in positions], dtype=torch.float64, device="cuda")
+    c, s = torch.cos(2 * torch.pi * turns), torch.sin(2 * torch.pi * turns)
+    a, b = x.double().split(4, -1)
+    want = torch.cat([a * c - b * s, a * s + b * c], -1)
+    pos = torch.tensor(positions, dtype=torch.float64, device="cuda").abs()[:, None]
+    angle = 2 * torch.pi * pos * (2.0 ** -52 * f / (2 * torch.pi) + 2.0 ** -64)
+    size = (a.abs() + b.abs()).repeat(1, 1, 1, 2)
+    assert ((got - want).abs() <= (2.0 ** -20 + angle.repeat(1, 2)) * size + 2.0 ** -24 * want.abs()).all()
