@@ -300,6 +300,7 @@ struct TcItem {
     TcSub sub[2];
 };
 constexpr int kItemSlots = 4;
+constexpr int kMaxSkipped = 4096;  // empty items in a row that are not posted
 
 __device__ __forceinline__ bool tc_active(const TcItem &it, int n, int s)
 {
@@ -481,11 +482,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         break;
                     }
                     if (i > 0) idx = next();
-                    // (an item whose rows lie behind its sequence's last has nothing to do)
-                    while (idx >= 0) {
+                    // (an item whose rows lie behind its sequence's last has nothing to do; at 1.25 us each,
+                    // one of kMaxSkipped goes to the other warps all the same, before their waits run out)
+                    for (int skipped = 0; idx >= 0; ++skipped) {
                         tc_make_item(tp, idx, sound, items[slot]);
                         if (items[slot].bad) attn_flag(ap.err, KVEVICT_DEV_BAD_LENGTH);
-                        if (items[slot].sub[0].nt > 0) break;
+                        if (items[slot].sub[0].nt > 0 || skipped >= kMaxSkipped) break;
                         idx = next();
                     }
                     if (idx < 0) items[slot].prob = -1;

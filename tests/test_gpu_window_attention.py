@@ -258,3 +258,22 @@ def test_offsets_beyond_32_bits(cuda_device):
     out, lse = kv.window_attention(q, k, v, n_sink=4, window=3000, kv_lens=lens, return_lse=True)
     assert (out[:-1] == 0).all() and (lse[:-1] == -math.inf).all()
     check(q[-1:], k[-1:], v[-1:], out[-1:], lse[-1:], 4, 3000)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_short_sequences_and_one_long(cuda_device, dtype):
+    """A packed batch in which nearly all row tiles that max_q allows are empty: tens of thousands for every SM."""
+    B, n, H, d = 20000, 1500, 4, 64
+    starts = torch.cat([torch.arange(B, dtype=torch.int32), torch.tensor([B - 1 + n], dtype=torch.int32)]).cuda()
+    g = gen(37)
+    q, k, v = (torch.randn(B - 1 + n, H, d, generator=g, device="cuda", dtype=dtype) for _ in range(3))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = kv.window_attention(q, k, v, n_sink=2, window=100, q_starts=starts, k_starts=starts, max_q=4096, max_k=n, error_word=err,
+                                   return_lse=True)
+    assert int(err) == 0
+    assert torch.equal(out[:B - 1], v[:B - 1])  # one key: its probability is 1
+    qq, kk, vv = (x[B - 1:].transpose(0, 1) for x in (q, k, v))
+    r, l, A = ref.sequence(qq, kk, vv, 2, 100, 0.125)
+    tol, tol_l = ref.bounds(dtype, qq, kk, n, 0.125, r, A, l)
+    ref.assert_close(out[B - 1:].transpose(0, 1), r, tol, "out")
+    ref.assert_close(lse[B - 1:].t(), l, tol_l, "lse")
