@@ -16,6 +16,7 @@ import torch
 
 from ._lib import BF16, ERR_DEVICE, F32, OK, check, lib
 
+_INT_MAX = 2**31 - 1
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
 # The argument structs of include/kvevict_ops.h, as their fields in order.
@@ -244,6 +245,9 @@ def _window_layout(q, k, v, n_sink, window, scale, q_starts, max_q, max_k) -> _L
     if packed:
         if max_q is None or max_k is None:
             raise ValueError("packed: give q_starts, k_starts, max_q and max_k, and no lengths")
+        if max_q < 0 or max_k < 0:
+            raise ValueError("max_q, max_k: need 0 or more")
+        max_q, max_k = min(max_q, _INT_MAX), min(max_k, _INT_MAX)
         B = q_starts.shape[0] - 1
         N, Hq, M, Hkv = q.shape[0], q.shape[1], k.shape[0], k.shape[1]
         strides = [(0, t.stride(1), t.stride(0)) for t in (q, k, v)]
@@ -258,7 +262,7 @@ def _window_layout(q, k, v, n_sink, window, scale, q_starts, max_q, max_k) -> _L
         dense = (Hq * N * d, N * d, d)
         max_q = max_k = 0
         lay.lse_shape = q.shape[:3]
-    shape = (dt, d, Hq, Hkv, B, n_sink, min(window, 2**31 - 1), max_q, max_k, _scale(scale), N, M)
+    shape = (dt, d, Hq, Hkv, B, min(n_sink, _INT_MAX), min(window, _INT_MAX), max_q, max_k, _scale(scale), N, M)
     lay.batch = B
     lay.head = _HEAD.pack(*shape)
     lay.strides = _Q9.pack(*strides[0], *strides[1], *strides[2])

@@ -278,3 +278,16 @@ def test_operator_errors_refused(L):
     assert L.kvevict_operator_errors(None) == -1
     with pytest.raises(ValueError, match="CUDA"):
         kv.operator_errors("cpu")
+
+
+def test_counts_beyond_32_bits(as_if_on_gpu):
+    """More sinks, a longer window or longest sequence than any tensor holds is as much as all of it."""
+    import kv_cache_eviction_decode_gb300 as kv
+    q, k, s = (torch.zeros(x, dtype=torch.bfloat16) for x in ((2, 4, 3, 64), (2, 2, 9, 64), (7, 4, 64)))
+    starts = torch.tensor([0, 7], dtype=torch.int32)
+    for call in (lambda: kv.window_attention(q, k, k, n_sink=2**40), lambda: kv.window_attention(q, k, k, window=2**40),
+                 lambda: kv.window_attention(s, s, s, q_starts=starts, k_starts=starts, max_q=2**40, max_k=2**40)):
+        with pytest.raises(RuntimeError, match="launched"):
+            call()
+    with pytest.raises(ValueError, match="max_q"):
+        kv.window_attention(s, s, s, q_starts=starts, k_starts=starts, max_q=-1, max_k=7)
