@@ -65,7 +65,10 @@ __device__ __forceinline__ float half_sum(float v)
     return v;
 }
 
-template <int D, int R>
+// kPacked: starts give the sequences; apart, because their check costs a spill at
+// 64 registers (8 x 8 heads, one token over 8000 keys of 128: 101.5 us with it in
+// every kernel, 99 without).
+template <int D, int R, bool kPacked>
 __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f32_kernel(const __grid_constant__ AttnParams ap)
 {
     using L = F32Layout<D, R>;
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f3
     const int unit = item / p.q_tiles;
     const int b = unit / ap.Hkv, kvh = unit - b * ap.Hkv;
     AttnSeq sq = attn_sequence(p, b, true);
-    if (p.q_starts) {
+    if constexpr (kPacked) {
         // (1,024 sequences of up to two tokens, 8 heads, the dearest case seen: 92 us, 85 without this)
         bool falls = false;
         for (int j = threadIdx.x; j <= b; j += kThreadsF32) falls = falls || attn_falls(p, j);
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 
 template <int D, int R> cudaError_t launch_f32(const AttnParams &p, cudaStream_t st)
 {
-    auto kern = attn_f32_kernel<D, R>;
+    auto kern = p.pr[0].q_starts ? attn_f32_kernel<D, R, true> : attn_f32_kernel<D, R, false>;
     constexpr int bytes = F32Layout<D, R>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
