@@ -126,8 +126,10 @@ Cut cut(AttnProblem &p, int G, int Hkv, int rows, int keys, int elem, int64_t ma
 }
 
 // Parts of a problem alone: items of equal work run in whole waves; those of a
-// causal prompt start with the longest and take the longest item, or the work
-// over the SMs.
+// causal prompt take the longest item, or the work over the SMs, as where they
+// start with the longest and one runs on an SM. That is the tensor-core kernel's
+// way. The fp32 kernel starts with the shortest and has up to four CTAs an SM:
+// for its causal prompts the estimate is too low, more so the fewer the items.
 int parts_alone(const Cut &c)
 {
     int best = 1;

@@ -9,13 +9,16 @@
 // x D/16 columns of the output. V is copied while the logits are made and the
 // next K during the product with V (cp.async, no registers between).
 //
-// R = 64, tiles of 64 keys: FFMA bound; per 64 FFMA a warp issues 8
-// shared-memory loads (12 wavefronts, below the 16 cycles that the FFMAs take at
-// four warps a cycle). 8 heads of 2048 x 128, causal: 407 us, 21 TFLOP/s (518
-// with K and V loaded in turn into one buffer).
+// R = 64, tiles of 64 keys: per 64 FFMA a warp issues 8 shared-memory loads (12
+// wavefronts, below the 16 cycles that the FFMAs take at four warps a cycle). 8
+// heads of 2048 x 128, causal: 415 us, 21 TFLOP/s, a quarter of the FP32 rate
+// (518 with K and V loaded in turn into one buffer). With one CTA of 8 warps an SM
+// (118,784 bytes of shared memory) the FMA pipe is busy in 48% of the cycles of an
+// SM at work; and over the launch in 28%, because blocks start with a prompt's
+// shortest tiles and the end waits for the longest.
 // R = 16, tiles of 32 keys, four CTAs an SM: for few rows, where K and V are read
 // for little arithmetic. 8 sequences of 8 heads, one token over 8000 keys of 128:
-// 98 us, 5.4 TB/s (285 while the warps without rows computed theirs too: bound by
+// 99 us, 5.3 TB/s (285 while the warps without rows computed theirs too: bound by
 // shared-memory reads).
 #include <cmath>
 

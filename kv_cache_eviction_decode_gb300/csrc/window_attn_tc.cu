@@ -32,9 +32,10 @@
 // sub (about 3,300 cycles a tile of 128 x 128 for both subs, 2,048 of them MMAs;
 // shared memory is read by Q K^T at its full rate meanwhile); decoding, bytes and
 // the start and end of items. Causal prompt of 8192, 32 query heads over 8, d
-// 128: 400 us, 1,375 TFLOP/s (71% of the cuBLAS rate); 2 x 32 heads x 4096, 4
-// sinks and a window of 1021: 155 us; a token of 32 sequences over 2,048 keys, 64
-// query heads over 8: 66 us, 4.1 TB/s with the join.
+// 128: 396 us, 1,390 TFLOP/s (72% of the cuBLAS rate; 412 us a call, one after
+// another); 2 x 32 heads x 4096, 4 sinks and a window of 1021: 150 us; a token of
+// 32 sequences over 2,048 keys, 64 query heads over 8: 63 us, 4.2 TB/s with the
+// join.
 #include <atomic>
 #include <climits>
 #include <cmath>
