@@ -10,8 +10,9 @@
  * current one. As with kvevict.h, argument errors are found on the host
  * before anything is launched and returned as a negative kvevict_status;
  * anomalies found on the GPU set bits of a device error word, here one that
- * the caller may pass, else the device's, which kvevict_operator_errors reads. No call allocates device memory or waits for the GPU;
- * each can be captured in a CUDA graph.
+ * the caller may pass, else the device's, which kvevict_operator_errors reads.
+ * No call allocates device memory; none but that one waits for the GPU, and each
+ * of the others can be captured in a CUDA graph.
  *
  * Tensors have their last axis (head_dim) contiguous; every other axis has a
  * stride of its own, in elements, given in the order sequence, head, token.

@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "api_internal.h"
 #include "kvevict_ops.h"
@@ -24,7 +25,9 @@ constexpr int kMaxParts = 64;  // parts a unit's keys are split into at most
 // The errors of calls that give no word of their own. (The kernels get one in
 // any case: with a test for null beside each of their waits a causal prompt of
 // 8192, 32 heads over 8, took 404 us, without 396.)
-__device__ uint32_t g_errors;
+__device__ uint32_t g_errors, g_errors_taken;
+
+__global__ void take_errors_kernel() { g_errors_taken = atomicExch(&g_errors, 0u); }
 
 // Its address on the current device, looked up once; also during a capture,
 // where the lookup may have to load the library's kernels first.
@@ -149,10 +152,11 @@ int parts_alone(const Cut &c)
 // whole waves and, for the rest of the last one, `long_sms` SMs; the second one's
 // items then fill up. A key tile of the first costs `weight` (its products, where
 // both row tiles are full: 3,300 cycles against 2,750 that a streamed tile takes;
-// 1.5 fits the measurements: 64 sequences behind 32768 tokens took 154, 135, 141
-// and 151 us with 4, 6, 8 and 16 parts, 32 behind 8192, whose rows fill one row tile,
-// 72, 62, 64 and 73 with 2, 3, 6 and 8). `share`: of the second's keys expected
-// (their lengths are on the device).
+// 1.5 fits the measurements that it was chosen by: 64 sequences behind 32768 tokens
+// took 154, 135, 141 and 151 us with 4, 6, 8 and 16 parts, 32 behind 8192, whose
+// rows fill one row tile, 72, 62, 64 and 73 with 2, 3, 6 and 8). `share`: of the
+// second's keys expected. Their lengths are on the device: the caller's 0.8 is an
+// assumption, and fuller or emptier suffixes get a plan that may be slower.
 void parts_together(const Cut &a, const Cut &b, double weight, double share, int &pa, int &pb)
 {
     static constexpr int kTry[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64};
@@ -464,12 +468,13 @@ extern "C" int kvevict_window_attention(const kvevict_attention_args *a, void *c
 extern "C" int kvevict_operator_errors(uint32_t *device_error)
 {
     if (!device_error) return KVEVICT_ERR_INVALID_ARG;
-    const uint32_t none = 0;
-    uint32_t *word = nullptr;
-    cudaError_t e = errors_address(&word);
-    if (e == cudaSuccess) e = cudaDeviceSynchronize();
-    if (e == cudaSuccess) e = cudaMemcpy(device_error, word, sizeof none, cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess) e = cudaMemcpy(word, &none, sizeof none, cudaMemcpyHostToDevice);
+    static std::mutex one;  // (g_errors_taken holds one caller's)
+    const std::lock_guard<std::mutex> lock(one);
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return KVEVICT_ERR_CUDA;
+    take_errors_kernel<<<1, 1>>>();
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(device_error, g_errors_taken, sizeof g_errors_taken);
     if (e != cudaSuccess) return KVEVICT_ERR_CUDA;
     return *device_error ? KVEVICT_ERR_DEVICE : KVEVICT_OK;
 }
