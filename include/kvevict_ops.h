@@ -2,7 +2,8 @@
  * kvevict_ops.h -- operators around the decode step, in libkvevict.so: the
  * prompt's attention under the set of tokens a StreamingLLM cache keeps (or
  * plain causal attention), decode attention of a batch that shares a prefix,
- * and rotary positions for queries and keys.
+ * rotary positions for queries and keys, and norms of their heads before them.
+ * (A paged cache and its attention: kvevict_paged.h.)
  *
  * These calls take no handle unless they say so: the arguments come in one
  * struct, the work is queued on the given stream (a cudaStream_t; NULL: the
@@ -184,6 +185,23 @@ typedef struct {
 } kvevict_rotary_args;
 
 int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream);
+
+/*
+ * The root-mean-square norm of every head, then its rotary positions, in one pass:
+ *   y = x / sqrt(mean_i x_i^2 + eps) * weight,   out = y turned as by kvevict_rotary,
+ * computed in fp32 and rounded once. The arguments are kvevict_rotary's with
+ * inverse = 0; rotary_dim may be 0 (inv_freq and positions then NULL): norms only.
+ *   q_weight, k_weight: [head_dim] in dtype, contiguous, 16-byte aligned;
+ *              k_weight NULL exactly where k is.
+ *   eps:       finite, >= 0. (With eps = 0 a head of zeros gives NaN.)
+ */
+typedef struct {
+    kvevict_rotary_args r;
+    const void *q_weight, *k_weight;
+    float eps;
+} kvevict_norm_rotary_args;
+
+int kvevict_norm_rotary(const kvevict_norm_rotary_args *a, void *cuda_stream);
 
 /*
  * With a handle: the prompt of an empty layer, attended and appended in one

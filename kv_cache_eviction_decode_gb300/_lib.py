@@ -12,10 +12,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvevict.so")
 
 H2O, SINK_WINDOW, RANDOM, H2O_BLOCK, H2O_POOLS = 0, 1, 2, 3, 4
-F32, BF16 = 0, 1
+F32, BF16, Q4 = 0, 1, 2
 
 OK, ERR_INVALID_ARG, ERR_CAPACITY, ERR_STATE, ERR_CUDA, ERR_DEVICE = 0, -1, -2, -3, -4, -5
-DEV_NONFINITE, DEV_NO_CANDIDATE, DEV_WAIT_TIMEOUT, DEV_BAD_SLOT, DEV_BAD_LENGTH = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_NONFINITE, DEV_NO_CANDIDATE, DEV_WAIT_TIMEOUT, DEV_BAD_SLOT, DEV_BAD_LENGTH, DEV_BAD_PAGE = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 
 
 class Config(ctypes.Structure):
@@ -92,10 +92,12 @@ def lib() -> ctypes.CDLL:
             L.kvevict_check.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
             L.kvevict_strerror.argtypes = [I]
             L.kvevict_strerror.restype = ctypes.c_char_p
-            for n in ("kvevict_window_attention", "kvevict_shared_prefix_attention", "kvevict_rotary"):
+            for n in ("kvevict_window_attention", "kvevict_shared_prefix_attention", "kvevict_rotary", "kvevict_norm_rotary",
+                      "kvevict_paged_append", "kvevict_paged_gather", "kvevict_paged_attention"):
                 getattr(L, n).argtypes = [ctypes.c_char_p, P]
                 getattr(L, n).restype = I
-            for n in ("kvevict_window_attention_workspace_bytes", "kvevict_shared_prefix_attention_workspace_bytes"):
+            for n in ("kvevict_window_attention_workspace_bytes", "kvevict_shared_prefix_attention_workspace_bytes",
+                      "kvevict_paged_attention_workspace_bytes"):
                 getattr(L, n).argtypes = [ctypes.c_char_p, ctypes.POINTER(SZ)]
                 getattr(L, n).restype = I
             L.kvevict_operator_errors.argtypes = [ctypes.POINTER(ctypes.c_uint32)]

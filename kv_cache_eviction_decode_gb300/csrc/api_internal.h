@@ -2,6 +2,8 @@
 // library (not part of the C ABI: hidden from the shared library's exports).
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include "kvevict_ops.h"
 
 #define KVEVICT_INTERNAL __attribute__((visibility("hidden")))
@@ -35,3 +37,12 @@ KVEVICT_INTERNAL int kvevict_prefix_part(const kvevict_shared_prefix_args *s, fl
 KVEVICT_INTERNAL int kvevict_prefix_run(const kvevict_shared_prefix_args *s, void *cuda_stream);
 
 }  // extern "C"
+
+namespace kvevict {
+
+// The word on the current device for the errors of operator calls that give none
+// of their own (kvevict_operator_errors). Its address is looked up once; also
+// during a capture, where the lookup may have to load the library's kernels first.
+KVEVICT_INTERNAL cudaError_t operator_errors_address(uint32_t **out);
+
+}  // namespace kvevict

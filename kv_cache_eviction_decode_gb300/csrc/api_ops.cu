@@ -29,29 +29,6 @@ __device__ uint32_t g_errors, g_errors_taken;
 
 __global__ void take_errors_kernel() { g_errors_taken = atomicExch(&g_errors, 0u); }
 
-// Its address on the current device, looked up once; also during a capture,
-// where the lookup may have to load the library's kernels first.
-cudaError_t errors_address(uint32_t **out)
-{
-    static std::atomic<uint32_t *> known[256] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    void *p = dev < 256 ? known[dev].load() : nullptr;
-    if (!p) {
-        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-        e = cudaThreadExchangeStreamCaptureMode(&mode);
-        if (e != cudaSuccess) return e;
-        e = cudaGetSymbolAddress(&p, g_errors);
-        const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
-        if (e == cudaSuccess) e = back;
-        if (e != cudaSuccess) return e;
-        if (dev < 256) known[dev].store(static_cast<uint32_t *>(p));
-    }
-    *out = static_cast<uint32_t *>(p);
-    return cudaSuccess;
-}
-
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // The stride of an axis of one entry is not looked at; any other is a positive
@@ -399,7 +376,7 @@ int run(const kvevict_attention_args *a, Plan &w, cudaStream_t st)
     p.lse = a->lse;
     p.err = a->error_word;
     const bool bf16 = a->dtype == KVEVICT_BF16;
-    cudaError_t e = p.err ? cudaSuccess : errors_address(&p.err);
+    cudaError_t e = p.err ? cudaSuccess : operator_errors_address(&p.err);
     if (e != cudaSuccess) return KVEVICT_ERR_CUDA;
     if (w.tensor) {
         for (int i = 0; i < p.n_problems; ++i) {
@@ -432,6 +409,27 @@ int check_shared(const kvevict_shared_prefix_args *s)
 }
 
 }  // namespace
+
+cudaError_t kvevict::operator_errors_address(uint32_t **out)
+{
+    static std::atomic<uint32_t *> known[256] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    void *p = dev < 256 ? known[dev].load() : nullptr;
+    if (!p) {
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        e = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return e;
+        e = cudaGetSymbolAddress(&p, g_errors);
+        const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e == cudaSuccess) e = back;
+        if (e != cudaSuccess) return e;
+        if (dev < 256) known[dev].store(static_cast<uint32_t *>(p));
+    }
+    *out = static_cast<uint32_t *>(p);
+    return cudaSuccess;
+}
 
 extern "C" int kvevict_window_attention_workspace_bytes(const kvevict_attention_args *a, size_t *bytes)
 {

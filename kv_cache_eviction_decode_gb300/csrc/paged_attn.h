@@ -1,0 +1,63 @@
+// paged_attn.h -- parameters of the attention kernels on a paged cache
+// (kvevict_paged_attention).
+//
+// A unit is a (sequence, KV head); its query rows are (token, group head) pairs,
+// row = token * G + g, so that the G query heads of a KV head share every key. An
+// item of work is a tile of rows of one unit against one of `splits` parts of the
+// 16-key tiles that those rows see (a tile lies in one page); with more than one
+// part each writes its own normalised output and log2 normaliser to the workspace,
+// and launch_paged_join joins them.
+#pragma once
+
+#include "paged_common.cuh"
+#include "window_attn_common.cuh"
+
+namespace kvevict {
+
+constexpr int kPagedTile = 16;  // keys
+
+struct PagedAttnParams {
+    PagedCache c;
+    AttnProblem mask;  // causal, n_sink, window, and q_starts (what attn_keys and attn_first_fall read)
+    const void *q;
+    void *out;
+    float *lse;        // may be null
+    long long qs[2], os[2];  // strides in elements: head, token
+    int tokens, per, max_q;
+    int G, Hq;
+    float scale_log2;
+    int splits, q_tiles;
+    float *part_o;     // [splits][tokens * Hq][d], and
+    float *part_l;     // [splits][tokens * Hq] log2 normalisers, where splits > 1
+};
+
+// A sequence's new tokens and keys: rows q0 .. q0 + n - 1, the first of them at
+// position p0 (negative where there are more of them than keys), m keys.
+struct PagedSeq {
+    int q0, n, m, p0;
+    bool bad;
+};
+
+// `sound`: none of the starts 0 .. b falls; else the sequence is left out.
+__device__ __forceinline__ PagedSeq paged_sequence(const PagedAttnParams &p, int b, bool sound)
+{
+    const PagedRows r = paged_rows(p.mask.q_starts, b, p.per, p.tokens);
+    PagedSeq s;
+    s.q0 = r.q0;
+    s.n = sound ? paged_min(r.n, p.max_q) : 0;
+    const int len = p.c.kv_lens[b];
+    const long long room = static_cast<long long>(p.c.width) << p.c.log2_s;
+    s.m = paged_max(len, 0);
+    if (s.m > room) s.m = static_cast<int>(room);
+    s.bad = r.bad || !sound || s.n != r.n || s.m != len;
+    s.p0 = paged_max(s.m - r.given, -(1 << 30));
+    return s;
+}
+
+// fp32 arithmetic on the CUDA cores, for every type.
+constexpr int kPagedSimtRows = 8;
+cudaError_t launch_paged_simt(const PagedAttnParams &p, int head_dim, bool bf16, bool q4, cudaStream_t st);
+// Joins the parts: out = sum_s 2^(l_s - l) o_s, l = log2 sum_s 2^(l_s).
+cudaError_t launch_paged_join(const PagedAttnParams &p, int head_dim, bool bf16, cudaStream_t st);
+
+}  // namespace kvevict

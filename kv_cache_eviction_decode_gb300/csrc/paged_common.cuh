@@ -1,0 +1,113 @@
+// paged_common.cuh -- what the kernels on a paged cache share: its parameters,
+// the new tokens of a sequence as read (and clamped) from the device, the place of
+// a token in the pages, and the groups of 4-bit pages.
+#pragma once
+
+#include <climits>
+
+#include "device_common.cuh"
+#include "kvevict_paged.h"
+
+namespace kvevict {
+
+struct PagedCache {
+    char *pages[2];                                             // keys, values
+    long long page_bytes[2], head_bytes[2], token_bytes[2];     // strides (4 bits: no token stride)
+    const int32_t *table, *kv_lens;
+    long long table_stride;
+    uint32_t *err;
+    int Hkv, S, log2_s, batch, width, n_pages;
+};
+
+__host__ __device__ __forceinline__ int paged_min(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int paged_max(int a, int b) { return a > b ? a : b; }
+
+// The rows of new tokens that a sequence owns: `n` of them from row q0 on, the
+// first ones of `given`. Starts out of range are clamped, so that every row lies in
+// the tensor; the rows of sequences whose starts ascend are disjoint.
+struct PagedRows {
+    int q0, n, given;
+    bool bad;
+};
+
+__host__ __device__ __forceinline__ PagedRows paged_rows(const int32_t *starts, int b, int per, int rows)
+{
+    PagedRows r;
+    if (!starts) {
+        r.q0 = b * per;
+        r.n = r.given = per;
+        r.bad = false;
+        return r;
+    }
+    const int a0 = starts[b], a1 = starts[b + 1];
+    r.q0 = paged_min(paged_max(a0, 0), rows);
+    r.given = paged_max(a1, r.q0) - r.q0;
+    r.n = paged_min(r.given, rows - r.q0);
+    r.bad = r.q0 != a0 || r.q0 + r.n != a1;
+    return r;
+}
+
+// The page of token i (>= 0) of sequence b, or -1 where the table names none.
+__device__ __forceinline__ int paged_page(const PagedCache &c, int b, long long i)
+{
+    const int page = c.table[b * c.table_stride + (i >> c.log2_s)];
+    return page >= 0 && page < c.n_pages ? page : -1;
+}
+
+// A whole block of threads, NT of them, finds the sequences of the rows row0 ..
+// row0 + count - 1 of packed tokens: seq[i] is the one that owns row0 + i, or -1.
+// From the first sequence that ends before it starts, the batch is left out (its
+// rows could be an earlier one's). `bits`: set where starts are out of order or
+// range. Uses *fall (shared); ends with a barrier.
+template <int NT>
+__device__ __forceinline__ void paged_owners(const int32_t *starts, int batch, int rows, int row0, int count, int *seq, int *fall,
+                                             uint32_t &bits)
+{
+    for (int i = threadIdx.x; i < count; i += NT) seq[i] = -1;
+    if (threadIdx.x == 0) *fall = INT_MAX;
+    __syncthreads();
+    for (int j0 = 0; j0 < batch; j0 += NT) {
+        const int j = j0 + static_cast<int>(threadIdx.x);
+        if (j < batch && starts[j] > starts[j + 1]) atomicMin(fall, j);
+        __syncthreads();
+        const int first = *fall;
+        if (j < batch && j < first) {
+            const PagedRows r = paged_rows(starts, j, 0, rows);
+            if (r.bad) bits |= KVEVICT_DEV_BAD_LENGTH;
+            const int hi = paged_min(r.q0 + r.n, row0 + count);
+            for (int t = paged_max(r.q0, row0); t < hi; ++t) seq[t - row0] = j;
+        }
+        __syncthreads();
+        if (first != INT_MAX) {
+            bits |= KVEVICT_DEV_BAD_LENGTH;
+            break;
+        }
+    }
+}
+
+// ------------------------------------------------------------- 4-bit groups
+// A group's base and step for values between lo and hi, and the code of a value.
+// In fp32, each operation rounded by itself.
+__device__ __forceinline__ void q4_group(float lo, float hi, bool finite, uint32_t &base_step, float &base, float &step)
+{
+    base = __bfloat162float(__float2bfloat16_rn(__fadd_rn(__fmul_rn(hi, 8.f / 15.f), __fmul_rn(lo, 7.f / 15.f))));
+    step = fmaxf(__fdiv_rn(__fsub_rn(hi, base), 7.f), __fmul_rn(__fsub_rn(base, lo), 0.125f));
+    step = __uint_as_float((__float_as_uint(step) + 0xFFFFu) & 0xFFFF0000u);  // (>= 0: up)
+    if (!finite) {
+        base = __uint_as_float(0x7FC00000u);
+        step = 0.f;
+    }
+    base_step = (__float_as_uint(base) >> 16) | (__float_as_uint(step) & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ uint32_t q4_code(float x, float base, float step)
+{
+    if (!(step > 0.f)) return 8u;
+    const float c = rintf(__fdiv_rn(__fsub_rn(x, base), step)) + 8.f;
+    return static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
+}
+
+__device__ __forceinline__ float q4_base(uint32_t base_step) { return __uint_as_float(base_step << 16); }
+__device__ __forceinline__ float q4_step(uint32_t base_step) { return __uint_as_float(base_step & 0xFFFF0000u); }
+
+}  // namespace kvevict

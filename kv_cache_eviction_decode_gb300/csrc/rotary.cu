@@ -17,64 +17,11 @@
 #include "device_common.cuh"
 #include "kvevict_ops.h"
 #include "launch.h"
+#include "rotary_common.cuh"
 
 namespace kvevict {
 
 namespace {
-
-constexpr int kRotThreads = 256;
-
-struct RotParams {
-    const void *x[2];      // q, k
-    void *y[2];
-    long long xs[2][3], ys[2][3];
-    int heads[2];
-    const void *pos;
-    int pos64;
-    long long ps0, ps1, pos_start;
-    const double *freq;
-    float scale;
-    int D, R, interleaved, inverse;
-    long long tokens, total;  // total = batch * tokens
-    uint32_t tokens_per, heads_per, head_blocks;  // rotary_kernel: a CTA's share
-};
-
-// 16-byte vectors of T as fp32 values.
-template <typename T> struct Vec {
-    static constexpr int N = 16 / sizeof(T);
-};
-
-__device__ __forceinline__ void unpack16(const uint4 &w, float (&v)[4])
-{
-    v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y); v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
-}
-__device__ __forceinline__ void unpack16(const uint4 &w, float (&v)[8])
-{
-    bf16x2_to_f32(w.x, v[0], v[1]);
-    bf16x2_to_f32(w.y, v[2], v[3]);
-    bf16x2_to_f32(w.z, v[4], v[5]);
-    bf16x2_to_f32(w.w, v[6], v[7]);
-}
-__device__ __forceinline__ uint4 pack16(const float (&v)[4])
-{
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-}
-__device__ __forceinline__ uint4 pack16(const float (&v)[8])
-{
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-
-__device__ __forceinline__ float2 rot_cos_sin(double freq, long long pos, float scale, bool inverse)
-{
-    // whole turns a position drop out; half a turn at most is left, and fits a signed 64-bit integer
-    const double turns = freq * 0.15915494309189535;
-    const long long f = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
-    const long long frac = static_cast<long long>(static_cast<unsigned long long>(pos) * static_cast<unsigned long long>(f));
-    const float half_turns = static_cast<float>(frac) * 1.0842021724855044e-19f;  // 2^-63
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    return make_float2(c * scale, inverse ? -s * scale : s * scale);
-}
 
 // Rotary parts whose pairs do not fall into 16-byte chunks (half layout:
 // rotary_dim / 2, interleaved: rotary_dim no multiple of a chunk). One CTA per
@@ -260,33 +207,48 @@ bool rot_tensor_ok(const void *x, const void *y, const int64_t (&xs)[3], const i
 
 }  // namespace
 
-}  // namespace kvevict
-
-using namespace kvevict;
-
-extern "C" int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream)
+long long rot_shares(RotParams &p, uint32_t units)
 {
+    const uint32_t heads = static_cast<uint32_t>(p.heads[0] + p.heads[1]);
+    const long long all = p.total * heads * units;
+    const long long want = std::min<long long>(10 * kRotThreads, std::max<long long>(kRotThreads / 2, all / 304));
+    p.heads_per = static_cast<uint32_t>(std::min<long long>(heads, std::max<long long>(1, want / units)));
+    p.head_blocks = (heads + p.heads_per - 1) / p.heads_per;
+    p.tokens_per = 1;
+    if (p.head_blocks == 1)
+        p.tokens_per = static_cast<uint32_t>(std::max<long long>(1, std::min<long long>(want / (heads * units), 8192 / std::max(p.R, 2))));
+    return (p.total + p.tokens_per - 1) / p.tokens_per * p.head_blocks;
+}
+
+int rot_prepare(const kvevict_rotary_args *a, bool norm, RotParams &p, bool &nothing)
+{
+    nothing = false;
     if (!a) return KVEVICT_ERR_INVALID_ARG;
     if (a->dtype != KVEVICT_F32 && a->dtype != KVEVICT_BF16) return KVEVICT_ERR_INVALID_ARG;
     const int elem = a->dtype == KVEVICT_F32 ? 4 : 2;
-    if (a->head_dim < 8 || a->head_dim > 1024 || a->head_dim % 8 || a->rotary_dim < 2 || a->rotary_dim > a->head_dim ||
+    const bool turns = !norm || a->rotary_dim != 0;
+    if (a->head_dim < 8 || a->head_dim > 1024 || a->head_dim % 8 || a->rotary_dim < (norm ? 0 : 2) || a->rotary_dim > a->head_dim ||
         a->rotary_dim % 2)
         return KVEVICT_ERR_INVALID_ARG;
     if ((a->interleaved | a->inverse | a->positions_64) & ~1) return KVEVICT_ERR_INVALID_ARG;
+    if (norm && a->inverse) return KVEVICT_ERR_INVALID_ARG;
     if (a->batch < 0 || a->tokens < 0 || a->n_q_heads < 0 || a->n_k_heads < 0 || a->n_q_heads > 65535 || a->n_k_heads > 65535)
         return KVEVICT_ERR_INVALID_ARG;
-    if (!std::isfinite(a->scale) || !a->inv_freq || (reinterpret_cast<uintptr_t>(a->inv_freq) & 7))
+    if (!std::isfinite(a->scale) || (turns && !a->inv_freq) || (reinterpret_cast<uintptr_t>(a->inv_freq) & 7))
         return KVEVICT_ERR_INVALID_ARG;
     if (a->batch >= (1LL << 31) || a->tokens >= (1LL << 31) || a->batch * a->tokens >= (1LL << 31))
         return KVEVICT_ERR_INVALID_ARG;
     const bool has_q = a->n_q_heads > 0, has_k = a->k != nullptr && a->n_k_heads > 0;
     const long long total = a->batch * a->tokens;
-    if (total == 0 || (!has_q && !has_k)) return KVEVICT_OK;
+    if (total == 0 || (!has_q && !has_k)) {
+        nothing = true;
+        return KVEVICT_OK;
+    }
     const int64_t qn[3] = {a->batch, a->n_q_heads, a->tokens}, kn[3] = {a->batch, a->n_k_heads, a->tokens};
     if (has_q && !rot_tensor_ok(a->q, a->q_out, a->q_stride, a->q_out_stride, qn, elem)) return KVEVICT_ERR_INVALID_ARG;
     if (has_k && !rot_tensor_ok(a->k, a->k_out, a->k_stride, a->k_out_stride, kn, elem)) return KVEVICT_ERR_INVALID_ARG;
     if (a->positions && (reinterpret_cast<uintptr_t>(a->positions) & (a->positions_64 ? 7 : 3))) return KVEVICT_ERR_INVALID_ARG;
-    RotParams p{};
+    p = RotParams{};
     p.x[0] = a->q; p.y[0] = a->q_out;
     p.x[1] = a->k; p.y[1] = a->k_out;
     for (int i = 0; i < 3; ++i) {
@@ -308,22 +270,26 @@ extern "C" int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream)
     p.inverse = a->inverse;
     p.tokens = a->tokens;
     p.total = total;
+    return KVEVICT_OK;
+}
+
+}  // namespace kvevict
+
+using namespace kvevict;
+
+extern "C" int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream)
+{
+    RotParams p;
+    bool nothing;
+    const int rc = rot_prepare(a, false, p, nothing);
+    if (rc != KVEVICT_OK || nothing) return rc;
+    const int elem = a->dtype == KVEVICT_F32 ? 4 : 2;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const int n = 16 / elem;  // elements of a chunk
     cudaError_t e;
     if (a->interleaved ? p.R % n == 0 : p.R / 2 % n == 0) {
-        const uint32_t heads = static_cast<uint32_t>(p.heads[0] + p.heads[1]);
         const uint32_t units = static_cast<uint32_t>(a->interleaved ? p.D / n : p.R / 2 / n + (p.D - p.R) / n);
-        // A CTA's units: ten for each of its threads, or, where that would leave SMs idle, what gives
-        // every SM two CTAs, but a unit for every second thread at least.
-        const long long all = total * heads * units;
-        const long long want = std::min<long long>(10 * kRotThreads, std::max<long long>(kRotThreads / 2, all / 304));
-        p.heads_per = static_cast<uint32_t>(std::min<long long>(heads, std::max<long long>(1, want / units)));
-        p.head_blocks = (heads + p.heads_per - 1) / p.heads_per;
-        p.tokens_per = 1;
-        if (p.head_blocks == 1)
-            p.tokens_per = static_cast<uint32_t>(std::max<long long>(1, std::min<long long>(want / (heads * units), 8192 / p.R)));
-        const long long blocks = (total + p.tokens_per - 1) / p.tokens_per * p.head_blocks;
+        const long long blocks = rot_shares(p, units);
         if (blocks >= (1LL << 31)) return KVEVICT_ERR_INVALID_ARG;
         const unsigned g = static_cast<unsigned>(blocks);
         const size_t smem = static_cast<size_t>(p.tokens_per) * (p.R / 2) * sizeof(float2);
@@ -336,8 +302,8 @@ extern "C" int kvevict_rotary(const kvevict_rotary_args *a, void *cuda_stream)
         }
     } else {
         const size_t smem = static_cast<size_t>(p.R / 2) * sizeof(float2);
-        if (elem == 4) e = launch_dependent(rotary_any_kernel<float>, static_cast<unsigned>(total), kRotThreads, smem, st, p);
-        else e = launch_dependent(rotary_any_kernel<__nv_bfloat16>, static_cast<unsigned>(total), kRotThreads, smem, st, p);
+        if (elem == 4) e = launch_dependent(rotary_any_kernel<float>, static_cast<unsigned>(p.total), kRotThreads, smem, st, p);
+        else e = launch_dependent(rotary_any_kernel<__nv_bfloat16>, static_cast<unsigned>(p.total), kRotThreads, smem, st, p);
     }
     return e == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
 }

@@ -23,9 +23,10 @@ _DT = {torch.float32: F32, torch.bfloat16: BF16}
 _ATTN = struct.Struct("@9if2q5P12q4PPNP")
 _SHARED = struct.Struct("@9if2q5P12q4PPNP2P5q")
 _ROT = struct.Struct("@8i2q4P12qP3qPf4x")
+_NORM = struct.Struct("@8i2q4P12qP3qPf4x2Pf4x")
 # ... and in pieces: shapes, addresses, strides, addresses (all multiples of 8 bytes).
 _HEAD, _PTRS, _Q9, _Q3, _TAIL = (struct.Struct("@" + f) for f in ("9if2q", "5P", "9q", "3q", "4PPNP"))
-_ROT_HEAD, _Q12, _ROT_TAIL, _P2, _P4 = (struct.Struct("@" + f) for f in ("8i2q", "12q", "P3qPf4x", "2P", "4P"))
+_ROT_HEAD, _Q12, _ROT_TAIL, _P2, _P4, _NORM_TAIL = (struct.Struct("@" + f) for f in ("8i2q", "12q", "P3qPf4x", "2P", "4P", "2Pf4x"))
 
 # The handle of a device's current stream as a number (torch.cuda.current_stream
 # builds a Stream object first, ten times the cost), where torch has it.
@@ -380,9 +381,45 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
     gradient of the forward call. Returns (q_out, k_out), or q_out without k."""
     if q.requires_grad or (k is not None and k.requires_grad) or q_out is not None or k_out is not None:
         _forward_only("rotary", q, k, q_out, k_out)
+    q_out, k_out, args = _rotary_args(q, k, positions, inv_freq, interleaved, scale, inverse, q_out, k_out)
+    _call("kvevict_rotary", q.get_device(), args)
+    return q_out if k is None else (q_out, k_out)
+
+
+def norm_rotary(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor, k_weight: torch.Tensor | None, positions=0,
+                inv_freq: torch.Tensor | None = None, *, eps: float = 1e-6, interleaved: bool = False, scale: float = 1.0,
+                q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """The root-mean-square norm of every head, x / sqrt(mean(x^2) + eps) *
+    weight, then rotary() of it, in one pass and rounded once: for models that norm
+    queries and keys per head. q_weight, k_weight: [d] in q's type (k_weight None
+    exactly where k is). inv_freq None: norms only. The other arguments, shapes and
+    results as in rotary()."""
+    if q.requires_grad or (k is not None and k.requires_grad) or q_weight.requires_grad or \
+            (k_weight is not None and k_weight.requires_grad) or q_out is not None or k_out is not None:
+        _forward_only("norm_rotary", q, k, q_weight, k_weight, q_out, k_out)
+    if (k is None) != (k_weight is None):
+        raise ValueError("k_weight: goes with k")
+    if not (eps >= 0 and math.isfinite(eps)):
+        raise ValueError("eps: need a finite number of at least 0")
+    if inv_freq is None:
+        positions = 0
+    q_out, k_out, args = _rotary_args(q, k, positions, inv_freq, interleaved, scale, False, q_out, k_out)
+    wp = [0, 0]
+    for i, (w, name) in enumerate(((q_weight, "q_weight"), (k_weight, "k_weight"))):
+        if w is not None:
+            _like(w, q, 1, name, q.shape[-1:])
+            wp[i] = w.data_ptr()
+            if wp[i] % 16:
+                raise ValueError(f"{name}: need an address that is a multiple of 16 bytes")
+    _call("kvevict_norm_rotary", q.get_device(), args + _NORM_TAIL.pack(*wp, eps))
+    return q_out if k is None else (q_out, k_out)
+
+
+def _rotary_args(q, k, positions, inv_freq, interleaved, scale, inverse, q_out, k_out):
+    """The outputs, made where they are not given, and the argument struct."""
     key = (q.dtype, q.get_device(), q.shape, q.stride(), None if k is None else (k.dtype, k.get_device(), k.shape, k.stride()),
            None if isinstance(positions, int) else (positions.dtype, positions.get_device(), positions.shape, positions.stride()),
-           inv_freq.shape, interleaved, inverse)
+           None if inv_freq is None else inv_freq.shape, interleaved, inverse)
     lay = _layouts.get(key) or _remember(key, _rotary_layout(q, k, positions, inv_freq, interleaved, inverse))
     if q_out is None and k_out is None:
         q_out, strides = torch.empty(q.shape, dtype=q.dtype, device=q.device), lay.strides
@@ -400,14 +437,14 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions, inv_freq: torch.T
             _like(k_out, q, dims, "k_out", k.shape)
             _strides(k_out, "k_out")
         strides = _Q12.pack(*_heads(q), *_heads(q_out), *((0,) * 6 if k is None else (*_heads(k), *_heads(k_out))))
-    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq is not None and (inv_freq.dtype is not torch.float64 or inv_freq.get_device() != q.get_device() or inv_freq.dim() != 1 or
+                                 not inv_freq.is_contiguous()):
         raise ValueError(f"inv_freq: need a contiguous float64 vector on {q.device}")
     pp, start = (0, positions) if isinstance(positions, int) else (positions.data_ptr(), 0)
     kp, kop = (0, 0) if k is None else (k.data_ptr(), k_out.data_ptr())
-    _call("kvevict_rotary", q.get_device(), b"".join((
+    return q_out, k_out, b"".join((
         lay.head, _P4.pack(q.data_ptr(), kp, q_out.data_ptr(), kop), strides,
-        _ROT_TAIL.pack(pp, *lay.tail, start, inv_freq.data_ptr(), scale))))
-    return q_out if k is None else (q_out, k_out)
+        _ROT_TAIL.pack(pp, *lay.tail, start, 0 if inv_freq is None else inv_freq.data_ptr(), scale)))
 
 
 def _heads(t: torch.Tensor) -> tuple:
@@ -449,7 +486,7 @@ def _rotary_layout(q, k, positions, inv_freq, interleaved, inverse) -> _Layout:
             raise ValueError(f"positions: {tuple(positions.shape)} does not go with q {tuple(q.shape)}")
         p64 = int(positions.dtype == torch.int64)
     lay = _Layout()
-    lay.head = _ROT_HEAD.pack(dt, d, 2 * inv_freq.shape[0], int(interleaved), int(inverse), p64, Hq, Hk, B, N)
+    lay.head = _ROT_HEAD.pack(dt, d, 0 if inv_freq is None else 2 * inv_freq.shape[0], int(interleaved), int(inverse), p64, Hq, Hk, B, N)
     lay.strides = _Q12.pack(*_heads(q), *dense[0], *((0,) * 6 if k is None else (*_heads(k), *dense[1])))
     lay.tail = ps
     return lay
