@@ -85,6 +85,7 @@ int check_tokens(int64_t tokens, const int32_t *starts, int batch)
 
 struct Plan {
     PagedAttnParams p{};
+    int rows = 0;  // of an item: with bf16 those of the tensor-core kernel
     int64_t items = 0;
     size_t bytes = 0;
 };
@@ -112,6 +113,26 @@ int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens)
     return std::min(all, (static_cast<int64_t>(n_sink) + kPagedTile - 1) / kPagedTile + (window + tokens - 1 + kPagedTile - 1) / kPagedTile + 1);
 }
 
+// Parts that the keys of a unit are split into: items run in waves of `slots` CTAs,
+// and one takes the tiles of a warp and kItemCost tiles more for its start and end;
+// joining the parts costs kJoinCost.
+constexpr double kItemCost = 4, kJoinCost = 5;
+
+int parts(int64_t units, int64_t tiles, int64_t slots)
+{
+    int best = 1;
+    double least = 0;
+    for (int64_t s = 1; s <= kMaxParts && (s == 1 || s * kPagedMmaWarps <= tiles); ++s) {
+        const double waves = std::ceil(static_cast<double>(units * s) / static_cast<double>(slots));
+        const double cost = waves * (std::ceil(static_cast<double>(tiles) / static_cast<double>(s * kPagedMmaWarps)) + kItemCost) + (s > 1 ? kJoinCost : 0);
+        if (s == 1 || cost < least * 0.97) {
+            least = cost;
+            best = static_cast<int>(s);
+        }
+    }
+    return best;
+}
+
 int plan_attention(const kvevict_paged_attention_args *a, Plan &w)
 {
     PagedAttnParams &p = w.p;
@@ -126,15 +147,17 @@ int plan_attention(const kvevict_paged_attention_args *a, Plan &w)
     p.mask.n_sink = a->n_sink;
     p.mask.window = a->window >= room ? 0 : a->window;  // a window as long as the table hides nothing
     p.mask.q_starts = a->q_starts;
-    p.q_tiles = static_cast<int>((static_cast<int64_t>(p.max_q) * p.G + kPagedSimtRows - 1) / kPagedSimtRows);
-    p.splits = 1;
+    const bool tensor = a->c.dtype == KVEVICT_BF16, q4 = a->c.page_dtype == KVEVICT_Q4;
+    const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
+    w.rows = !tensor ? kPagedSimtRows : rows <= 8 ? 8 : 16;
+    p.q_tiles = static_cast<int>((rows + w.rows - 1) / w.rows);
     const int64_t units = static_cast<int64_t>(a->c.batch) * a->c.n_kv_heads * p.q_tiles;
-    const int64_t tiles = key_tiles(max_k, p.mask.n_sink, p.mask.window, std::min<int64_t>(p.max_q, kPagedSimtRows));
-    if (units > 0) p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kMaxParts, tiles / 8, (6 * kSMs + units - 1) / units})));
+    const int64_t tiles = key_tiles(max_k, p.mask.n_sink, p.mask.window, std::min<int64_t>(p.max_q, (w.rows + p.G - 1) / p.G + 1));
+    p.splits = parts(units, tiles, kSMs * (tensor && !(q4 && w.rows == 8) ? 2 : 3));
     w.items = units * p.splits;
     if (w.items >= (int64_t{1} << 31)) return KVEVICT_ERR_INVALID_ARG;
-    const size_t rows = static_cast<size_t>(a->tokens) * p.Hq;
-    w.bytes = p.splits > 1 ? up256(p.splits * rows * a->c.head_dim * 4) + up256(p.splits * rows * 4) : 0;
+    const size_t slots = static_cast<size_t>(p.splits) * a->tokens * p.Hq;
+    w.bytes = p.splits > 1 ? up256(slots * a->c.head_dim * 4) + up256(slots * 4) : 0;
     return KVEVICT_OK;
 }
 
@@ -263,7 +286,7 @@ extern "C" int kvevict_paged_attention(const kvevict_paged_attention_args *a, vo
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const bool bf16 = a->c.dtype == KVEVICT_BF16, q4 = a->c.page_dtype == KVEVICT_Q4;
-    cudaError_t e = launch_paged_simt(p, a->c.head_dim, bf16, q4, st);
+    cudaError_t e = bf16 ? launch_paged_mma(p, a->c.head_dim, q4, w.rows, st) : launch_paged_simt(p, a->c.head_dim, bf16, q4, st);
     if (e == cudaSuccess && p.splits > 1) e = launch_paged_join(p, a->c.head_dim, bf16, st);
     return e == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
 }
