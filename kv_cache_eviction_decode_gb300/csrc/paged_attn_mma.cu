@@ -9,12 +9,17 @@
 // eight query heads of a KV head fill an instruction. (tcgen05 would want 64 or 128
 // rows.) P^T comes from S^T by transposing 8 x 8 blocks in registers (movmatrix).
 //
-// 4 bits: a code c becomes bf16 128 + c by one mask-and-or, four to a half word.
-//   S_ij = sum_groups step (sum_c (128 + c) q) + (base - 136 step) (sum q),
-// the sums over a group in fp32; for the second product 136 is taken away first,
-// which is exact, the step goes into the probabilities,
+// 4 bits: a code needs a mask and nothing else to be a matrix operand. bf16's bit
+// patterns 0 .. 255 are the values 0 .. 255 times 2^-133 (its subnormals and, with
+// the same spacing, the first normal numbers), so c and 16 c are read off as they
+// lie in a half word, two bits of work a channel. Queries are scaled by a power of
+// two to at most 2^101, a sixteenth of it for every second channel, and
+//   S_ij = sum_groups step (sum_c c q) + (base - 8 step) (sum q),
+// the sums over a group in fp32. In the second product the step goes into the
+// probabilities, which are then rounded to bf16, once, and scaled by a power of two
+// that follows the largest step seen:
 //   O_i = sum_j (p_ij step_j) (c_j - 8) + sum_j p_ij base_j,
-// which are then rounded to bf16 once, and the base's part stays in fp32.
+// the 8 taken off by an instruction with constant codes, the base's part in fp32.
 //
 // The running maximum is moved only where a logit exceeds it by 2^8 or more: then,
 // and only then, sums and outputs are rescaled. Probabilities below 2^8 instead of
@@ -84,15 +89,17 @@ __device__ __forceinline__ float pow2(float x)
     return y;
 }
 
-// Nibble i of both half words as bf16 128 + c.
-__device__ __forceinline__ uint32_t nibbles(uint32_t x, int i) { return ((x >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
-// ... and as c - 8.
-__device__ __forceinline__ uint32_t centred(uint32_t x, int i)
-{
-    uint32_t y;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(nibbles(x, i)), "r"(0x43084308u));
-    return y;
-}
+// Codes of two keys or channels, one in each half word, as bf16: c 2^-133, and
+// from the next nibble 16 c 2^-133.
+__device__ __forceinline__ uint32_t code(uint32_t x) { return x & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t code16(uint32_t x) { return x & 0x00F000F0u; }
+constexpr uint32_t kMinus8 = 0x80088008u, kMinus8x16 = 0x80808080u;  // -8 as such a code
+
+__device__ __forceinline__ float exponent_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // 2^e
+
+constexpr int kMinE = -40;  // of the steps' power of two; the probabilities' is 2^(kProbE - E)
+constexpr int kProbE = 80;
+constexpr int kCodeE = -133;
 
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
@@ -167,13 +174,20 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
     // ------------------------------------------------------------ copies into the ring
     const uint32_t my_ring = smem_u32(ring) + warp * L::kWarpBytes;
     const char *const kbase = c.pages[0] + kvh * c.head_bytes[0], *const vbase = c.pages[1] + kvh * c.head_bytes[1];
+    // 4 bits: what a lane copies. K's rows go in by eights in key_of's order; V's as they are, with the 16-byte chunks of
+    // every second pair of rows swapped (D = 128), so that four rows' parts lie in different banks.
+    constexpr int kPc = L::kParams;  // 16-byte chunks of a tile's groups, of K and of V
+    const int cr = lane / (L::kRow / 16), cch = lane % (L::kRow / 16);
+    const int k_from = ((cr & 8) + key_of(cr & 7)) * L::kRow + cch * 16, v_from = cr * L::kRow + (D == 128 ? cch ^ (cr & 2) : cch) * 16;
+    const int p_from = Q4 ? c.S * L::kRow + lane % max(kPc, 1) * 16 : 0;
     uint32_t bad = 0;  // bit s: stage s holds a tile without a page
+    int next = 0;      // the stage that the next copies go to
     auto issue = [&](int k) {
         if (k < n_mine) {
             if (k && (k & 31) == 0) pages = pages_next;
             if ((k & 31) == 0) pages_next = pages_from(k + 32);
             const int page = __shfl_sync(kAll, pages, k & 31);
-            const int s = k % L::kStages, j0 = attn_tile_at(keys, i_lo + warp + kWarps * k) * kPagedTile, slot0 = j0 & (c.S - 1);
+            const int s = next, j0 = attn_tile_at(keys, i_lo + warp + kWarps * k) * kPagedTile, slot0 = j0 & (c.S - 1);
             const uint32_t dst = my_ring + s * L::kStage;
             bad = page < 0 ? bad | 1u << s : bad & ~(1u << s);
             if (page < 0) {
@@ -182,22 +196,15 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             const char *kp = kbase + max(page, 0) * c.page_bytes[0], *vp = vbase + max(page, 0) * c.page_bytes[1];
             if constexpr (Q4) {
                 if (page >= 0) {
-                    // K: 8-row halves in key_of's order. V: rows as they are, 16-byte chunks swapped for every second pair of
-                    // rows (D = 128), so that four rows' parts lie in different banks.
-                    constexpr int kChunks = L::kRow / 16, kHalf = 8 * kChunks;
-                    const char *kc = kp + slot0 * (D / 2), *vc = vp + slot0 * (D / 2);
+                    const char *kc = kp + slot0 * L::kRow + k_from, *vc = vp + slot0 * L::kRow + v_from;
+                    const char *pc = (lane < kPc ? kp : vp) + slot0 * L::kParams + p_from;
+                    const uint32_t to = dst + lane * 16;
 #pragma unroll
-                    for (int e0 = 0; e0 < 2 * kHalf; e0 += 32) {
-                        const int e = e0 + lane, r = e / kChunks, ch = e % kChunks;
-                        copy16(dst + e * 16, kc + ((r & 8) + key_of(r & 7)) * L::kRow + ch * 16, true);
-                        const int vch = D == 128 ? ch ^ (r & 2) : ch;
-                        copy16(dst + kPagedTile * L::kRow + e * 16, vc + r * L::kRow + vch * 16, true);
+                    for (int e0 = 0; e0 < kPagedTile * L::kRow; e0 += 512) {
+                        copy16(to + e0, kc + e0, true);
+                        copy16(to + kPagedTile * L::kRow + e0, vc + e0, true);
                     }
-                    constexpr int kPc = kPagedTile * L::kParams / 16;  // 16 or 8 chunks of groups each
-                    if (lane < 2 * kPc) {
-                        const char *from = (lane < kPc ? kp : vp) + c.S * (D / 2) + slot0 * L::kParams + lane % kPc * 16;
-                        copy16(dst + 2 * kPagedTile * L::kRow + lane * 16, from, true);
-                    }
+                    if (lane < 2 * kPc) copy16(to + 2 * kPagedTile * L::kRow, pc, true);
                 }
             } else {
                 // 16-byte chunks swapped by row, so that the eight rows of a matrix load lie in different banks
@@ -212,36 +219,58 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 }
             }
         }
+        next = next + 1 == L::kStages ? 0 : next + 1;
         copies_close();
     };
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < L::kStages - 1; ++k) issue(k);
 
     // ---------------------------------------------------------------- queries, row n = 8 a + g
     uint32_t qf[NT][kSteps][2];
-    float qsum[NT][kGroups][2];  // of a group, rows 2 t and 2 t + 1 (4 bits)
+    float qsum[NT][kGroups][2];  // 4 bits: of a group, rows 2 t and 2 t + 1, times 2^-133 like the products
+    float sl2[NT][2];            // what turns those rows' products into logits to base 2
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
         const int r = 8 * a + g, tk = (r0 + r) / p.G, hd = r0 + r - tk * p.G;
         const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(p.q) + (kvh * p.G + hd) * p.qs[0] + (sq.q0 + tk) * p.qs[1];
+        sl2[a][0] = sl2[a][1] = p.scale_log2;
         if constexpr (Q4) {
+            float x[kGroups][8], top = 0.f;
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (r < nr) w = *reinterpret_cast<const uint4 *>(qr + 32 * j + 8 * t);
-                // step 2 j + h: channels (2 h, 4 + 2 h) and (2 h + 1, 5 + 2 h) of the lane's eight
-                qf[a][2 * j][0] = __byte_perm(w.x, w.z, 0x5410);
-                qf[a][2 * j][1] = __byte_perm(w.x, w.z, 0x7632);
-                qf[a][2 * j + 1][0] = __byte_perm(w.y, w.w, 0x5410);
-                qf[a][2 * j + 1][1] = __byte_perm(w.y, w.w, 0x7632);
-                float sum = 0.f, x, y;
+                bf16x2_to_f32(w.x, x[j][0], x[j][1]);
+                bf16x2_to_f32(w.y, x[j][2], x[j][3]);
+                bf16x2_to_f32(w.z, x[j][4], x[j][5]);
+                bf16x2_to_f32(w.w, x[j][6], x[j][7]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    bf16x2_to_f32(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w, x, y);
-                    sum += x + y;
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[j][i]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+            // the row times 2^(100 - e), 2^e the power of two of its largest element (far ones, where fp32 would end, left as they are)
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -20), 90);
+            const float up = exponent_of(100 - e), back = p.scale_log2 * exponent_of(e - 100 - kCodeE);
+            sl2[a][0] = __shfl_sync(kAll, back, 8 * t);
+            sl2[a][1] = __shfl_sync(kAll, back, 8 * t + 4);
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[j][i] *= up;
+                    sum += x[j][i] * exponent_of(-100);
+                }
+                // step 2 j + h: channels (2 h, 4 + 2 h) and, a sixteenth, (2 h + 1, 5 + 2 h) of the lane's eight
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    qf[a][2 * j + h][0] = pack_bf16x2(x[j][2 * h], x[j][4 + 2 * h]);
+                    qf[a][2 * j + h][1] = pack_bf16x2(x[j][2 * h + 1] * 0.0625f, x[j][5 + 2 * h] * 0.0625f);
                 }
                 sum += __shfl_xor_sync(kAll, sum, 1);
                 sum += __shfl_xor_sync(kAll, sum, 2);
+                sum *= exponent_of(100 + kCodeE);
                 qsum[a][j][0] = __shfl_sync(kAll, sum, 8 * t);
                 qsum[a][j][1] = __shfl_sync(kAll, sum, 8 * t + 4);
             }
@@ -254,12 +283,17 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
         }
     }
 
-    float m[NT][2], l[NT][2], o[NT][kSteps][4], ob[NT][kGroups][2];  // ob: sum of p base (4 bits), this lane's keys
+    // nm: minus the running maximum (to base 2); over: the product above which it is moved
+    float nm[NT][2], over[NT][2], l[NT][2], o[NT][kSteps][4], ob[NT][kGroups][2];  // ob: sum of p base (4 bits), this lane's keys
+    int step_e = kMinE;                                                           // 4 bits: 2^e of the largest step seen,
+    uint32_t step_over = 0;                                                       // and the group from which on it is moved
+    float prob = exponent_of(kProbE - kMinE);
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            m[a][i] = -FLT_MAX;
+            nm[a][i] = FLT_MAX;
+            over[a][i] = -INFINITY;
             l[a][i] = 0.f;
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) ob[a][j][i] = 0.f;
@@ -271,12 +305,14 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
     }
     // this lane's keys of a tile: k0 and k0 + 8
     const int k0 = Q4 ? key_of(g) : g;
+    const int kw_at = g * L::kRow + t * (D / 8), vw_at = kPagedTile * L::kRow + t * L::kRow + (D == 128 ? (g >> 1 ^ (t & 2)) * 16 + (g & 1) * 8 : g * 4);
+    const int p_at = 2 * kPagedTile * L::kRow + k0 * L::kParams;
 
-    for (int k = 0; k < n_mine; ++k) {
+#pragma unroll 1
+    for (int k = 0, s = 0; k < n_mine; ++k, s = s + 1 == L::kStages ? 0 : s + 1) {
         copies_wait<L::kStages - 2>();
         __syncwarp();
         issue(k + L::kStages - 1);
-        const int s = k % L::kStages;
         const uint32_t at = my_ring + s * L::kStage;
         const int j0 = attn_tile_at(keys, i_lo + warp + kWarps * k) * kPagedTile;
         // every row sees every key of the tile
@@ -287,28 +323,27 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
         if constexpr (Q4) {
             constexpr int W = D / 32;  // words of codes: an eighth of a row twice
             uint32_t w0[W], w1[W], ps0[kGroups], ps1[kGroups];
-            lds(w0, at + g * L::kRow + t * (D / 8));
-            lds(w1, at + (8 + g) * L::kRow + t * (D / 8));
-            lds(ps0, at + 2 * kPagedTile * L::kRow + k0 * L::kParams);
-            lds(ps1, at + 2 * kPagedTile * L::kRow + (k0 + 8) * L::kParams);
+            lds(w0, at + kw_at);
+            lds(w1, at + kw_at + 8 * L::kRow);
+            lds(ps0, at + p_at);
+            lds(ps1, at + p_at + 8 * L::kParams);
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 // half word j of both eighths: channels 8 t + i below, 8 t + 4 + i above
                 const uint32_t sel = j % 2 ? 0x7632 : 0x5410;
                 const uint32_t x0 = __byte_perm(w0[j / 2], w0[W / 2 + j / 2], sel), x1 = __byte_perm(w1[j / 2], w1[W / 2 + j / 2], sel);
-                const uint32_t a0 = nibbles(x0, 0), a1 = nibbles(x1, 0), a2 = nibbles(x0, 1), a3 = nibbles(x1, 1);
-                const uint32_t a4 = nibbles(x0, 2), a5 = nibbles(x1, 2), a6 = nibbles(x0, 3), a7 = nibbles(x1, 3);
+                const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
                 const float st0 = q4_step(ps0[j]), st1 = q4_step(ps1[j]);
-                const float ba0 = fmaf(-136.f, st0, q4_base(ps0[j])), ba1 = fmaf(-136.f, st1, q4_base(ps1[j]));
+                const float ba0 = fmaf(-8.f, st0, q4_base(ps0[j])), ba1 = fmaf(-8.f, st1, q4_base(ps1[j]));
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
                     float d[4];
-                    mma_first(d, a0, a1, a2, a3, qf[a][2 * j][0], qf[a][2 * j][1]);
-                    mma_next(d, a4, a5, a6, a7, qf[a][2 * j + 1][0], qf[a][2 * j + 1][1]);
+                    mma_first(d, code(x0), code(x1), code16(x0), code16(x1), qf[a][2 * j][0], qf[a][2 * j][1]);
+                    mma_next(d, code(y0), code(y1), code16(y0), code16(y1), qf[a][2 * j + 1][0], qf[a][2 * j + 1][1]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float base = (i < 2 ? ba0 : ba1) * qsum[a][j][i & 1];
-                        z[a][i] = fmaf(i < 2 ? st0 : st1, d[i], j ? z[a][i] + base : base);
+                        const float base = i < 2 ? ba0 : ba1;
+                        z[a][i] = fmaf(i < 2 ? st0 : st1, d[i], j ? fmaf(base, qsum[a][j][i & 1], z[a][i]) : base * qsum[a][j][i & 1]);
                     }
                 }
             }
@@ -338,28 +373,73 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                     if (!see || (bad >> s & 1)) z[a][i] = -INFINITY;
                 }
         }
-        bool over = false;
+        const uint32_t av = at + kPagedTile * L::kRow;
+        uint32_t vs0[kGroups], vs1[kGroups];  // 4 bits: V's groups, keys k0 and k0 + 8
+        bool move = false;
+        if constexpr (Q4) {
+            lds(vs0, at + p_at + 16 * L::kParams);
+            lds(vs1, at + p_at + 24 * L::kParams);
+            if (!whole) {
+                // a row takes nothing of a key that it does not see, whatever that stands for; one that sees NaN gets it
+                const int ja = j0 + k0, jb = ja + 8;
+                const bool none0 = !(ja < keys.sink || (ja >= keys.lo && ja < keys.hi)) || (bad >> s & 1);
+                const bool none1 = !(jb < keys.sink || (jb >= keys.lo && jb < keys.hi)) || (bad >> s & 1);
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t &v = e ? vs1[j] : vs0[j];
+                        if (e ? none1 : none0) v = 0;
+                        if ((v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u) continue;
+                        v = 0;
+#pragma unroll
+                        for (int a = 0; a < NT; ++a)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (z[a][2 * e + i] != -INFINITY) ob[a][j][i] = __uint_as_float(0x7FC00000u);
+                    }
+            }
+            uint32_t largest = max(vs0[0], vs1[0]);
+#pragma unroll
+            for (int j = 1; j < kGroups; ++j) largest = max(largest, max(vs0[j], vs1[j]));
+            move = largest >= step_over;
+        }
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) over = over || fmaxf(z[a][i], z[a][i + 2]) * p.scale_log2 > m[a][i] + kSlack;
-        if (__any_sync(kAll, over)) {
+            for (int i = 0; i < 2; ++i) move = move || fmaxf(z[a][i], z[a][i + 2]) > over[a][i];
+        if (__any_sync(kAll, move)) {
+            float less = 1.f;
+            if constexpr (Q4) {
+                uint32_t largest = 0;
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    const uint32_t e0 = vs0[j] & 0x7F800000u, e1 = vs1[j] & 0x7F800000u;
+                    largest = max(largest, max(e0 == 0x7F800000u ? 0 : e0, e1 == 0x7F800000u ? 0 : e1));
+                }
+                const int e = max(step_e, static_cast<int>(__reduce_max_sync(kAll, largest) >> 23) - 127);
+                less = exponent_of(max(step_e - e, -126));
+                step_e = e;
+                step_over = min(static_cast<uint32_t>(e + 127 + static_cast<int>(kSlack)), 255u) << 23;
+                prob = exponent_of(kProbE - e);
+            }
 #pragma unroll
             for (int a = 0; a < NT; ++a)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float mx = fmaxf(z[a][i], z[a][i + 2]) * p.scale_log2;
+                    float mx = fmaxf(z[a][i], z[a][i + 2]) * sl2[a][i];
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, w));
-                    const float mn = fmaxf(m[a][i], mx), f = pow2(m[a][i] - mn);
-                    m[a][i] = mn;
+                    const float mn = fmaxf(-nm[a][i], mx), f = pow2(-nm[a][i] - mn), fo = f * less;
+                    nm[a][i] = -mn;
+                    over[a][i] = mn == -FLT_MAX ? -INFINITY : (mn + kSlack) / sl2[a][i];
                     l[a][i] *= f;
 #pragma unroll
                     for (int j = 0; j < kGroups; ++j) ob[a][j][i] *= f;
 #pragma unroll
                     for (int s2 = 0; s2 < kSteps; ++s2) {
-                        o[a][s2][i] *= f;
-                        o[a][s2][i + 2] *= f;
+                        o[a][s2][i] *= fo;
+                        o[a][s2][i + 2] *= fo;
                     }
                 }
         }
@@ -367,48 +447,37 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
         for (int a = 0; a < NT; ++a)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                z[a][i] = pow2(fmaf(z[a][i], p.scale_log2, -m[a][i & 1]));
+                z[a][i] = pow2(fmaf(z[a][i], sl2[a][i & 1], nm[a][i & 1]));
                 l[a][i & 1] += z[a][i];
             }
 
         // --------------------------------------------------------- outputs
-        const uint32_t av = at + kPagedTile * L::kRow;
         if constexpr (Q4) {
             constexpr int W = D / 64;  // words of an eighth of a row
-            uint32_t w[4][W], ps0[kGroups], ps1[kGroups];
+            uint32_t w[4][W];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 4 * i + t;
-                const int ch = D == 128 ? (g >> 1 ^ (r & 2)) * 16 + (g & 1) * 8 : g * 4;
-                lds(w[i], av + r * L::kRow + ch);
-            }
-            lds(ps0, at + 2 * kPagedTile * L::kRow + (16 + k0) * L::kParams);
-            lds(ps1, at + 2 * kPagedTile * L::kRow + (24 + k0) * L::kParams);
+            for (int i = 0; i < 4; ++i) lds(w[i], at + vw_at + 4 * i * L::kRow);
+            float zp[NT][4];
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) zp[a][i] = z[a][i] * prob;
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 const uint32_t sel = j % 2 ? 0x7632 : 0x5410;
                 const uint32_t x0 = __byte_perm(w[0][j / 2], w[1][j / 2], sel), x1 = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
-                const float st0 = q4_step(ps0[j]), st1 = q4_step(ps1[j]), ba0 = q4_base(ps0[j]), ba1 = q4_base(ps1[j]);
-                uint32_t b0[NT], b1[NT];
+                const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+                const float st0 = q4_step(vs0[j]), st1 = q4_step(vs1[j]), ba0 = q4_base(vs0[j]), ba1 = q4_base(vs1[j]);
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    float y[4];
+                    const uint32_t b0 = transpose8x8(pack_bf16x2(zp[a][0] * st0, zp[a][1] * st0));
+                    const uint32_t b1 = transpose8x8(pack_bf16x2(zp[a][2] * st1, zp[a][3] * st1));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[i] = z[a][i] * (i < 2 ? st0 : st1);
-                        float add = z[a][i] * (i < 2 ? ba0 : ba1);
-                        // (a row takes nothing of a key that it does not see, whatever that stands for)
-                        if (!whole && z[a][i] == 0.f) y[i] = add = 0.f;
-                        ob[a][j][i & 1] += add;
-                    }
-                    b0[a] = transpose8x8(pack_bf16x2(y[0], y[1]));
-                    b1[a] = transpose8x8(pack_bf16x2(y[2], y[3]));
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t a0 = centred(x0, 2 * h), a1 = centred(x0, 2 * h + 1), a2 = centred(x1, 2 * h), a3 = centred(x1, 2 * h + 1);
-#pragma unroll
-                    for (int a = 0; a < NT; ++a) mma_next(o[a][2 * j + h], a0, a1, a2, a3, b0[a], b1[a]);
+                    for (int i = 0; i < 2; ++i) ob[a][j][i] = fmaf(z[a][i + 2], ba1, fmaf(z[a][i], ba0, ob[a][j][i]));
+                    mma_next(o[a][2 * j], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
+                    mma_next(o[a][2 * j + 1], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
+                    mma_next(o[a][2 * j], code(x0), code16(x0), code(x1), code16(x1), b0, b1);
+                    mma_next(o[a][2 * j + 1], code(y0), code16(y0), code(y1), code16(y1), b0, b1);
                 }
             }
         } else {
@@ -454,11 +523,13 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
 #pragma unroll
             for (int s2 = 0; s2 < kSteps; ++s2) {
                 // 4 bits: tile 2 j + h has channels 32 j + 4 g + 2 h, and the next one
-                if constexpr (Q4) row[32 * (s2 / 2) + 4 * g + 2 * (s2 % 2) + i / 2] = o[a][s2][i] + ob[a][s2 / 2][i & 1];
+                if constexpr (Q4)
+                    row[32 * (s2 / 2) + 4 * g + 2 * (s2 % 2) + i / 2] =
+                        fmaf(o[a][s2][i] * exponent_of((i < 2 ? 0 : -4) - kProbE - kCodeE), exponent_of(step_e), ob[a][s2 / 2][i & 1]);
                 else row[16 * s2 + g + 8 * (i / 2)] = o[a][s2][i];
             }
             if (g == 0 && i < 2) {
-                sm[warp * R + 8 * a + 2 * t + i] = m[a][i];
+                sm[warp * R + 8 * a + 2 * t + i] = -nm[a][i];
                 sl[warp * R + 8 * a + 2 * t + i] = l[a][i];
             }
         }

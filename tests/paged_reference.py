@@ -116,8 +116,8 @@ U = 2.0 ** -23
 
 def attention_bounds(dtype, four, q, k, k_size, k_step, A, A_step, n_keys, scale, ref, lse):
     """Bounds of one sequence's out and lse, as derived in tests/attn_reference.py, for q and k [H][..][d] fp64. 4 bits: the
-    codes enter a product as 128 + code (at most 143), and 136 times the other factor's sum is taken away, in fp32. Of a
-    logit's group of 32: 34 operations, each off by a step of at most (143 + 136) step sum |q|; the bases 32 more of their
+    codes enter a product as they are (at most 15), and 8 times the other factor's sum is taken away, in fp32. Of a
+    logit's group of 32: 34 operations, each off by a step of at most (15 + 8) step sum |q|; the bases 32 more of their
     own size; sum them over the groups. Of an output: 80 operations a run of keys at most, the same with the probabilities,
     which are rounded after they are multiplied with the step. A: p @ |v| (4 bits: |base| + |code - 8| step), A_step: p @ step."""
     d = q.shape[-1]
@@ -125,8 +125,8 @@ def attention_bounds(dtype, four, q, k, k_size, k_step, A, A_step, n_keys, scale
     r_p = half if dtype == torch.bfloat16 else 0.0
     if four:
         S, T = (scale * float((q.abs() @ x.transpose(-1, -2)).max()) if x.numel() and q.numel() else 0.0 for x in (k_size, k_step))
-        dz = U * ((d + 6) * S + 34 * 279 * T)
-        tol = A * (r_p + 2 * dz + n_keys * U + 2.0 ** -20) + 80 * 279 * U * A_step
+        dz = U * ((d + 6) * S + 34 * 23 * T)
+        tol = A * (r_p + 2 * dz + n_keys * U + 2.0 ** -20) + 80 * 23 * U * A_step
     else:
         S = scale * float((q.norm(dim=-1).max() * k.norm(dim=-1).max())) if k.numel() and q.numel() else 0.0
         dz = (d + 6) * U * S
