@@ -153,7 +153,7 @@ int plan_attention(const kvevict_paged_attention_args *a, Plan &w)
     p.q_tiles = static_cast<int>((rows + w.rows - 1) / w.rows);
     const int64_t units = static_cast<int64_t>(a->c.batch) * a->c.n_kv_heads * p.q_tiles;
     const int64_t tiles = key_tiles(max_k, p.mask.n_sink, p.mask.window, std::min<int64_t>(p.max_q, (w.rows + p.G - 1) / p.G + 1));
-    p.splits = parts(units, tiles, kSMs * (tensor && !(q4 && w.rows == 8) ? 2 : 3));
+    p.splits = parts(units, tiles, kSMs * (!tensor || (q4 && w.rows == 8) ? 3 : 2));
     w.items = units * p.splits;
     if (w.items >= (int64_t{1} << 31)) return KVEVICT_ERR_INVALID_ARG;
     const size_t slots = static_cast<size_t>(p.splits) * a->tokens * p.Hq;

@@ -93,13 +93,22 @@ __device__ __forceinline__ float pow2(float x)
 // from the next nibble 16 c 2^-133.
 __device__ __forceinline__ uint32_t code(uint32_t x) { return x & 0x000F000Fu; }
 __device__ __forceinline__ uint32_t code16(uint32_t x) { return x & 0x00F000F0u; }
+__device__ __forceinline__ bool finite_group(uint32_t v) { return (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u; }
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus8x16 = 0x80808080u;  // -8 as such a code
 
 __device__ __forceinline__ float exponent_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // 2^e
 
-constexpr int kMinE = -40;  // of the steps' power of two; the probabilities' is 2^(kProbE - E)
-constexpr int kProbE = 80;
+constexpr int kMinE = -20;  // of the steps' power of two E, from which the maximum is counted kProbE lower (see below)
+constexpr int kProbE = 40;
 constexpr int kCodeE = -133;
+
+// The upper, middle and lower eight bits of an fp32 value (i = 0, 1, 2), or 0.
+__device__ __forceinline__ float bf16_part(float x, int i)
+{
+    const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u), r = x - hi;
+    const float mid = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
+    return i == 0 ? hi : i == 1 ? mid : i == 2 ? r - mid : 0.f;
+}
 
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
@@ -164,62 +173,68 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
     const int n_mine = max(0, (i_hi - i_lo - warp + kWarps - 1) / kWarps);  // tiles i_lo + warp + kWarps k
     const int low_b = p.mask.window > 0 && pb >= p.mask.window ? pb - p.mask.window + 1 : 0;
 
-    // pages of the next 32 of this warp's tiles, one a lane; the 32 after them are on their way
-    auto pages_from = [&](int k0) {
-        const int k = k0 + lane;
-        return k < n_mine ? paged_page(c, b, static_cast<long long>(attn_tile_at(keys, i_lo + warp + kWarps * k)) * kPagedTile) : -1;
+    // Of 32 of this warp's tiles, one a lane: where their pages' blocks are, the first key, and whether every row sees
+    // every key (kWhole) or there is no page (kNoPage). The next 32 tiles' pages are on their way.
+    constexpr int kWhole = 1, kNoPage = 2;
+    auto first_key = [&](int k) { return attn_tile_at(keys, i_lo + warp + kWarps * k) * kPagedTile; };
+    auto page_at = [&](int k) { return k < n_mine ? paged_page(c, b, first_key(k)) : 0; };
+    const char *block[2] = {};
+    int what = 0, page_next = page_at(lane);
+    auto next_tiles = [&](int k) {  // the tiles k .. k + 31
+        const int page = page_next;
+        page_next = page_at(k + 32 + lane);
+        const int j0 = first_key(k + lane);
+        const bool whole = page >= 0 && j0 + kPagedTile - 1 <= min(pa, sq.m - 1) && (j0 + kPagedTile <= p.mask.n_sink || j0 >= low_b);
+        what = j0 | (whole ? kWhole : 0) | (page < 0 ? kNoPage : 0);
+        if (page < 0) atomicOr(c.err, KVEVICT_DEV_BAD_PAGE);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) block[i] = c.pages[i] + max(page, 0) * c.page_bytes[i] + kvh * c.head_bytes[i];
     };
-    int pages = pages_from(0), pages_next = -1;
 
     // ------------------------------------------------------------ copies into the ring
-    const uint32_t my_ring = smem_u32(ring) + warp * L::kWarpBytes;
-    const char *const kbase = c.pages[0] + kvh * c.head_bytes[0], *const vbase = c.pages[1] + kvh * c.head_bytes[1];
+    const uint32_t my_ring = smem_u32(ring) + warp * L::kWarpBytes, ring_end = my_ring + L::kWarpBytes;
     // 4 bits: what a lane copies. K's rows go in by eights in key_of's order; V's as they are, with the 16-byte chunks of
     // every second pair of rows swapped (D = 128), so that four rows' parts lie in different banks.
     constexpr int kPc = L::kParams;  // 16-byte chunks of a tile's groups, of K and of V
     const int cr = lane / (L::kRow / 16), cch = lane % (L::kRow / 16);
     const int k_from = ((cr & 8) + key_of(cr & 7)) * L::kRow + cch * 16, v_from = cr * L::kRow + (D == 128 ? cch ^ (cr & 2) : cch) * 16;
     const int p_from = Q4 ? c.S * L::kRow + lane % max(kPc, 1) * 16 : 0;
-    uint32_t bad = 0;  // bit s: stage s holds a tile without a page
-    int next = 0;      // the stage that the next copies go to
+    uint32_t to = my_ring;  // the stage that the next copies go to
     auto issue = [&](int k) {
         if (k < n_mine) {
-            if (k && (k & 31) == 0) pages = pages_next;
-            if ((k & 31) == 0) pages_next = pages_from(k + 32);
-            const int page = __shfl_sync(kAll, pages, k & 31);
-            const int s = next, j0 = attn_tile_at(keys, i_lo + warp + kWarps * k) * kPagedTile, slot0 = j0 & (c.S - 1);
-            const uint32_t dst = my_ring + s * L::kStage;
-            bad = page < 0 ? bad | 1u << s : bad & ~(1u << s);
-            if (page < 0) {
-                if (lane == 0) atomicOr(c.err, KVEVICT_DEV_BAD_PAGE);
-            }
-            const char *kp = kbase + max(page, 0) * c.page_bytes[0], *vp = vbase + max(page, 0) * c.page_bytes[1];
+            if ((k & 31) == 0) next_tiles(k);
+            const int w = __shfl_sync(kAll, what, k & 31);
+            const char *kb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[0]), k & 31));
+            const char *vb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[1]), k & 31));
+            const int slot0 = w & (c.S - kPagedTile);
             if constexpr (Q4) {
-                if (page >= 0) {
-                    const char *kc = kp + slot0 * L::kRow + k_from, *vc = vp + slot0 * L::kRow + v_from;
-                    const char *pc = (lane < kPc ? kp : vp) + slot0 * L::kParams + p_from;
-                    const uint32_t to = dst + lane * 16;
+                if (!(w & kNoPage)) {
+                    const char *kc = kb + (slot0 * L::kRow + k_from), *vc = vb + (slot0 * L::kRow + v_from);
+                    const char *pc = (lane < kPc ? kb : vb) + (slot0 * L::kParams + p_from);
+                    const uint32_t dst = to + lane * 16;
 #pragma unroll
                     for (int e0 = 0; e0 < kPagedTile * L::kRow; e0 += 512) {
-                        copy16(to + e0, kc + e0, true);
-                        copy16(to + kPagedTile * L::kRow + e0, vc + e0, true);
+                        copy16(dst + e0, kc + e0, true);
+                        copy16(dst + kPagedTile * L::kRow + e0, vc + e0, true);
                     }
-                    if (lane < 2 * kPc) copy16(to + 2 * kPagedTile * L::kRow, pc, true);
+                    if (lane < 2 * kPc) copy16(dst + 2 * kPagedTile * L::kRow, pc, true);
                 }
             } else {
                 // 16-byte chunks swapped by row, so that the eight rows of a matrix load lie in different banks
                 constexpr int kChunks = L::kRow / 16;
+                const int j0 = w & ~(kPagedTile - 1);
 #pragma unroll
                 for (int e0 = 0; e0 < kPagedTile * kChunks; e0 += 32) {
                     const int e = e0 + lane, r = e / kChunks, ch = e % kChunks, j = j0 + r;
-                    const bool real = page >= 0 && (j < keys.sink || (j >= keys.lo && j < keys.hi));
+                    const bool real = !(w & kNoPage) && (j < keys.sink || (j >= keys.lo && j < keys.hi));
                     const uint32_t at = r * L::kRow + ((ch & ~7) | ((ch ^ r) & 7)) * 16;
-                    copy16(dst + at, kp + (slot0 + r) * c.token_bytes[0] + ch * 16, real);
-                    copy16(dst + kPagedTile * L::kRow + at, vp + (slot0 + r) * c.token_bytes[1] + ch * 16, real);
+                    copy16(to + at, kb + (slot0 + r) * c.token_bytes[0] + ch * 16, real);
+                    copy16(to + kPagedTile * L::kRow + at, vb + (slot0 + r) * c.token_bytes[1] + ch * 16, real);
                 }
             }
         }
-        next = next + 1 == L::kStages ? 0 : next + 1;
+        to += L::kStage;
+        if (to == ring_end) to = my_ring;
         copies_close();
     };
 #pragma unroll 1
@@ -227,7 +242,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
 
     // ---------------------------------------------------------------- queries, row n = 8 a + g
     uint32_t qf[NT][kSteps][2];
-    float qsum[NT][kGroups][2];  // 4 bits: of a group, rows 2 t and 2 t + 1, times 2^-133 like the products
+    uint32_t qs[NT][2][2];       // 4 bits: of each group the sum of row g, and -8 of it, in three bf16 parts (see below)
     float sl2[NT][2];            // what turns those rows' products into logits to base 2
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
@@ -254,6 +269,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             const float up = exponent_of(100 - e), back = p.scale_log2 * exponent_of(e - 100 - kCodeE);
             sl2[a][0] = __shfl_sync(kAll, back, 8 * t);
             sl2[a][1] = __shfl_sync(kAll, back, 8 * t + 4);
+            float qg[kGroups];
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 float sum = 0.f;
@@ -270,9 +286,18 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 }
                 sum += __shfl_xor_sync(kAll, sum, 1);
                 sum += __shfl_xor_sync(kAll, sum, 2);
-                sum *= exponent_of(100 + kCodeE);
-                qsum[a][j][0] = __shfl_sync(kAll, sum, 8 * t);
-                qsum[a][j][1] = __shfl_sync(kAll, sum, 8 * t + 4);
+                qg[j] = sum * exponent_of(100 + kCodeE);  // times 2^-133 like the products
+            }
+            // An instruction's 16 channels hold the groups' bases (or steps): D = 128, lane t groups 2 (t & 1) and the next;
+            // they meet the sums' upper parts (t < 2), middle (t >= 2) and, eight further, lower parts (t < 2). D = 64: both
+            // groups in every lane, with the upper, middle and lower part for t = 0, 1, 2.
+            const int pair = D == 128 ? t & 1 : 0, part0 = D == 128 ? t >> 1 : t, part1 = D == 128 && t < 2 ? 2 : 3;
+            const float s0 = pair ? qg[kGroups - 2] : qg[0], s1 = pair ? qg[kGroups - 1] : qg[1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float f = i ? -8.f : 1.f;
+                qs[a][i][0] = pack_bf16x2(f * bf16_part(s0, part0), f * bf16_part(s1, part0));
+                qs[a][i][1] = pack_bf16x2(f * bf16_part(s0, part1), f * bf16_part(s1, part1));
             }
         } else {
 #pragma unroll
@@ -283,11 +308,12 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
         }
     }
 
-    // nm: minus the running maximum (to base 2); over: the product above which it is moved
-    float nm[NT][2], over[NT][2], l[NT][2], o[NT][kSteps][4], ob[NT][kGroups][2];  // ob: sum of p base (4 bits), this lane's keys
-    int step_e = kMinE;                                                           // 4 bits: 2^e of the largest step seen,
-    uint32_t step_over = 0;                                                       // and the group from which on it is moved
-    float prob = exponent_of(kProbE - kMinE);
+    // nm: minus the running maximum (to base 2), 4 bits: counted kProbE - E lower, 2^E the power of two of the largest step
+    // seen, so that probability times step times code stays in range; over: the product above which it is moved. ob: 4 bits,
+    // sums of p base, row g of the product the group g.
+    float nm[NT][2], over[NT][2], l[NT][2], o[NT][kSteps][4], ob[NT][4];
+    int step_e = kMinE;
+    uint32_t step_over = 0;  // the group (as it is stored) from which on E is moved
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
 #pragma unroll
@@ -295,9 +321,9 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             nm[a][i] = FLT_MAX;
             over[a][i] = -INFINITY;
             l[a][i] = 0.f;
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) ob[a][j][i] = 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ob[a][i] = 0.f;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -306,17 +332,20 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
     // this lane's keys of a tile: k0 and k0 + 8
     const int k0 = Q4 ? key_of(g) : g;
     const int kw_at = g * L::kRow + t * (D / 8), vw_at = kPagedTile * L::kRow + t * L::kRow + (D == 128 ? (g >> 1 ^ (t & 2)) * 16 + (g & 1) * 8 : g * 4);
-    const int p_at = 2 * kPagedTile * L::kRow + k0 * L::kParams;
+    constexpr int kParamsAt = 2 * kPagedTile * L::kRow;
+    const int p_at = kParamsAt + k0 * L::kParams, pair_at = kParamsAt + k0 * L::kParams + (D == 128 ? (t & 1) * 8 : 0);
+    const int vb_at = kParamsAt + (kPagedTile + t) * L::kParams + (g & (kGroups - 1)) * 4;
+    uint32_t at = my_ring;
+    int whats = 0;  // of the 32 tiles that the present one is among
 
 #pragma unroll 1
-    for (int k = 0, s = 0; k < n_mine; ++k, s = s + 1 == L::kStages ? 0 : s + 1) {
+    for (int k = 0; k < n_mine; ++k) {
+        if ((k & 31) == 0) whats = what;
         copies_wait<L::kStages - 2>();
         __syncwarp();
         issue(k + L::kStages - 1);
-        const uint32_t at = my_ring + s * L::kStage;
-        const int j0 = attn_tile_at(keys, i_lo + warp + kWarps * k) * kPagedTile;
-        // every row sees every key of the tile
-        const bool whole = j0 + kPagedTile - 1 <= min(pa, sq.m - 1) && (j0 + kPagedTile <= p.mask.n_sink || j0 >= low_b) && !(bad >> s & 1);
+        const int w_ = __shfl_sync(kAll, whats, k & 31), j0 = w_ & ~(kPagedTile - 1);
+        const bool whole = w_ & kWhole;
 
         // ---------------------------------------------------------- logits
         float z[NT][4];
@@ -327,6 +356,17 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             lds(w1, at + kw_at + 8 * L::kRow);
             lds(ps0, at + p_at);
             lds(ps1, at + p_at + 8 * L::kParams);
+            uint32_t p0[2], p1[2];  // this lane's pair of groups
+            lds(p0, at + pair_at);
+            lds(p1, at + pair_at + 8 * L::kParams);
+            // base (sum q) - 8 step (sum q), all groups
+            const uint32_t ba0 = __byte_perm(p0[0], p0[1], 0x5410), ba1 = __byte_perm(p1[0], p1[1], 0x5410);
+            const uint32_t sp0 = __byte_perm(p0[0], p0[1], 0x7632), sp1 = __byte_perm(p1[0], p1[1], 0x7632);
+#pragma unroll
+            for (int a = 0; a < NT; ++a) {
+                mma_first(z[a], ba0, ba1, ba0, ba1, qs[a][0][0], qs[a][0][1]);
+                mma_next(z[a], sp0, sp1, sp0, sp1, qs[a][1][0], qs[a][1][1]);
+            }
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 // half word j of both eighths: channels 8 t + i below, 8 t + 4 + i above
@@ -334,17 +374,13 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 const uint32_t x0 = __byte_perm(w0[j / 2], w0[W / 2 + j / 2], sel), x1 = __byte_perm(w1[j / 2], w1[W / 2 + j / 2], sel);
                 const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
                 const float st0 = q4_step(ps0[j]), st1 = q4_step(ps1[j]);
-                const float ba0 = fmaf(-8.f, st0, q4_base(ps0[j])), ba1 = fmaf(-8.f, st1, q4_base(ps1[j]));
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
                     float d[4];
                     mma_first(d, code(x0), code(x1), code16(x0), code16(x1), qf[a][2 * j][0], qf[a][2 * j][1]);
                     mma_next(d, code(y0), code(y1), code16(y0), code16(y1), qf[a][2 * j + 1][0], qf[a][2 * j + 1][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float base = i < 2 ? ba0 : ba1;
-                        z[a][i] = fmaf(i < 2 ? st0 : st1, d[i], j ? fmaf(base, qsum[a][j][i & 1], z[a][i]) : base * qsum[a][j][i & 1]);
-                    }
+                    for (int i = 0; i < 4; ++i) z[a][i] = fmaf(i < 2 ? st0 : st1, d[i], z[a][i]);
                 }
             }
         } else {
@@ -370,58 +406,38 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 for (int i = 0; i < 4; ++i) {
                     const int j = j0 + k0 + (i < 2 ? 0 : 8), r = min(8 * a + 2 * t + (i & 1), nr - 1), pos = sq.p0 + (r0 + r) / p.G;
                     const bool see = j <= pos && j < sq.m && (p.mask.window <= 0 || j < p.mask.n_sink || j > pos - p.mask.window);
-                    if (!see || (bad >> s & 1)) z[a][i] = -INFINITY;
+                    if (!see || (w_ & kNoPage)) z[a][i] = -INFINITY;
                 }
         }
         const uint32_t av = at + kPagedTile * L::kRow;
-        uint32_t vs0[kGroups], vs1[kGroups];  // 4 bits: V's groups, keys k0 and k0 + 8
-        bool move = false;
+        uint32_t largest = 0;
+        bool move = false, odd = false;  // odd (4 bits): V's groups need a look, one by one
         if constexpr (Q4) {
-            lds(vs0, at + p_at + 16 * L::kParams);
-            lds(vs1, at + p_at + 24 * L::kParams);
-            if (!whole) {
-                // a row takes nothing of a key that it does not see, whatever that stands for; one that sees NaN gets it
-                const int ja = j0 + k0, jb = ja + 8;
-                const bool none0 = !(ja < keys.sink || (ja >= keys.lo && ja < keys.hi)) || (bad >> s & 1);
-                const bool none1 = !(jb < keys.sink || (jb >= keys.lo && jb < keys.hi)) || (bad >> s & 1);
+            // two words a lane (D = 64: one) are all of V's groups
+            uint32_t v[kGroups / 2];
+            lds(v, at + kParamsAt + kPagedTile * L::kParams + lane * (2 * kGroups));
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t &v = e ? vs1[j] : vs0[j];
-                        if (e ? none1 : none0) v = 0;
-                        if ((v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u) continue;
-                        v = 0;
-#pragma unroll
-                        for (int a = 0; a < NT; ++a)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                if (z[a][2 * e + i] != -INFINITY) ob[a][j][i] = __uint_as_float(0x7FC00000u);
-                    }
-            }
-            uint32_t largest = max(vs0[0], vs1[0]);
-#pragma unroll
-            for (int j = 1; j < kGroups; ++j) largest = max(largest, max(vs0[j], vs1[j]));
+            for (int i = 0; i < kGroups / 2; ++i) largest = max(largest, v[i]);
             move = largest >= step_over;
+            odd = !whole;
+            if (odd) {
+                const int j = j0 + (lane >> 1);  // the words' key; one that no row sees does not count
+                if ((w_ & kNoPage) || !(j < keys.sink || (j >= keys.lo && j < keys.hi))) move = false, largest = 0;
+            }
         }
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
             for (int i = 0; i < 2; ++i) move = move || fmaxf(z[a][i], z[a][i + 2]) > over[a][i];
         if (__any_sync(kAll, move)) {
-            float less = 1.f;
+            float lower = 0.f, rise = 0.f;
             if constexpr (Q4) {
-                uint32_t largest = 0;
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    const uint32_t e0 = vs0[j] & 0x7F800000u, e1 = vs1[j] & 0x7F800000u;
-                    largest = max(largest, max(e0 == 0x7F800000u ? 0 : e0, e1 == 0x7F800000u ? 0 : e1));
-                }
-                const int e = max(step_e, static_cast<int>(__reduce_max_sync(kAll, largest) >> 23) - 127);
-                less = exponent_of(max(step_e - e, -126));
-                step_e = e;
-                step_over = min(static_cast<uint32_t>(e + 127 + static_cast<int>(kSlack)), 255u) << 23;
-                prob = exponent_of(kProbE - e);
+                const uint32_t e = largest & 0x7F800000u;  // (infinities and NaN are no measure)
+                const int was = step_e;
+                step_e = max(step_e, static_cast<int>(__reduce_max_sync(kAll, e == 0x7F800000u ? 0u : e) >> 23) - 127);
+                rise = static_cast<float>(step_e - was);
+                step_over = min(static_cast<uint32_t>(step_e + 127 + static_cast<int>(kSlack)), 255u) << 23;
+                lower = static_cast<float>(kProbE - step_e);
             }
 #pragma unroll
             for (int a = 0; a < NT; ++a)
@@ -430,16 +446,16 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                     float mx = fmaxf(z[a][i], z[a][i + 2]) * sl2[a][i];
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, w));
-                    const float mn = fmaxf(-nm[a][i], mx), f = pow2(-nm[a][i] - mn), fo = f * less;
+                    const float mn = fmaxf(rise - nm[a][i], mx - lower), f = pow2(-nm[a][i] - mn);
                     nm[a][i] = -mn;
-                    over[a][i] = mn == -FLT_MAX ? -INFINITY : (mn + kSlack) / sl2[a][i];
+                    over[a][i] = mn == -FLT_MAX ? -INFINITY : (mn + lower + kSlack) / sl2[a][i];
                     l[a][i] *= f;
-#pragma unroll
-                    for (int j = 0; j < kGroups; ++j) ob[a][j][i] *= f;
+                    ob[a][i] *= f;
+                    ob[a][i + 2] *= f;
 #pragma unroll
                     for (int s2 = 0; s2 < kSteps; ++s2) {
-                        o[a][s2][i] *= fo;
-                        o[a][s2][i + 2] *= fo;
+                        o[a][s2][i] *= f;
+                        o[a][s2][i + 2] *= f;
                     }
                 }
         }
@@ -454,26 +470,53 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
         // --------------------------------------------------------- outputs
         if constexpr (Q4) {
             constexpr int W = D / 64;  // words of an eighth of a row
-            uint32_t w[4][W];
+            uint32_t w[4][W], vs0[kGroups], vs1[kGroups], vb[4][1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) lds(w[i], at + vw_at + 4 * i * L::kRow);
-            float zp[NT][4];
+            lds(vs0, at + p_at + 16 * L::kParams);
+            lds(vs1, at + p_at + 24 * L::kParams);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds(vb[i], at + vb_at + 4 * i * L::kParams);  // group g (mod kGroups) of this lane's four keys
+            if (odd) {
+                // a row takes nothing of a key that it does not see, whatever that stands for; one that sees NaN gets it
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool nan = !finite_group(vb[i][0]);
+                    if (nan) vb[i][0] = 0;
+                    if ((w_ & kNoPage) || !(j0 + 4 * i + t < keys.sink || (j0 + 4 * i + t >= keys.lo && j0 + 4 * i + t < keys.hi))) vb[i][0] = 0;
+                }
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t &v = e ? vs1[j] : vs0[j];
+                        const int key = j0 + k0 + 8 * e;
+                        const bool none = (w_ & kNoPage) || !(key < keys.sink || (key >= keys.lo && key < keys.hi)), nan = !finite_group(v) && !none;
+                        if (none || nan) v = 0;
+#pragma unroll
+                        for (int a = 0; a < NT; ++a)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                // (each row of the product of the bases is a group: the lanes with g = j take it up)
+                                const bool hit = __reduce_or_sync(kAll, nan && z[a][2 * e + i] != 0.f ? 1u << t : 0u) >> t & 1;
+                                if (hit && (g & (kGroups - 1)) == j) ob[a][i] = __uint_as_float(0x7FC00000u);
+                            }
+                    }
+            }
+            const uint32_t va0 = __byte_perm(vb[0][0], vb[1][0], 0x5410), va1 = __byte_perm(vb[2][0], vb[3][0], 0x5410);
 #pragma unroll
             for (int a = 0; a < NT; ++a)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) zp[a][i] = z[a][i] * prob;
+                mma_next(ob[a], va0, 0, va1, 0, transpose8x8(pack_bf16x2(z[a][0], z[a][1])), transpose8x8(pack_bf16x2(z[a][2], z[a][3])));
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 const uint32_t sel = j % 2 ? 0x7632 : 0x5410;
                 const uint32_t x0 = __byte_perm(w[0][j / 2], w[1][j / 2], sel), x1 = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
                 const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-                const float st0 = q4_step(vs0[j]), st1 = q4_step(vs1[j]), ba0 = q4_base(vs0[j]), ba1 = q4_base(vs1[j]);
+                const float st0 = q4_step(vs0[j]), st1 = q4_step(vs1[j]);
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    const uint32_t b0 = transpose8x8(pack_bf16x2(zp[a][0] * st0, zp[a][1] * st0));
-                    const uint32_t b1 = transpose8x8(pack_bf16x2(zp[a][2] * st1, zp[a][3] * st1));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) ob[a][j][i] = fmaf(z[a][i + 2], ba1, fmaf(z[a][i], ba0, ob[a][j][i]));
+                    const uint32_t b0 = transpose8x8(pack_bf16x2(z[a][0] * st0, z[a][1] * st0));
+                    const uint32_t b1 = transpose8x8(pack_bf16x2(z[a][2] * st1, z[a][3] * st1));
                     mma_next(o[a][2 * j], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
                     mma_next(o[a][2 * j + 1], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
                     mma_next(o[a][2 * j], code(x0), code16(x0), code(x1), code16(x1), b0, b1);
@@ -496,6 +539,8 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 for (int a = 0; a < NT; ++a) mma_next(o[a][s2], f[0], f[1], f[2], f[3], b0[a], b1[a]);
             }
         }
+        at += L::kStage;
+        if (at == ring_end) at = my_ring;
     }
 
     // -------------------------------------------------------------- the warps' parts
@@ -507,11 +552,14 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 l[a][i] += __shfl_xor_sync(kAll, l[a][i], w);
-                if constexpr (Q4) {
-#pragma unroll
-                    for (int j = 0; j < kGroups; ++j) ob[a][j][i] += __shfl_xor_sync(kAll, ob[a][j][i], w);
-                }
             }
+    float obs[NT][kGroups][2];  // every group's
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) obs[a][j][i] = Q4 ? __shfl_sync(kAll, ob[a][i], 4 * j + t) : 0.f;
     __syncthreads();  // the rings have been used
     constexpr int kPad = D + 4;
     float *const so = reinterpret_cast<float *>(ring), *const sm = so + kWarps * R * kPad, *const sl = sm + kWarps * R;
@@ -525,7 +573,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 // 4 bits: tile 2 j + h has channels 32 j + 4 g + 2 h, and the next one
                 if constexpr (Q4)
                     row[32 * (s2 / 2) + 4 * g + 2 * (s2 % 2) + i / 2] =
-                        fmaf(o[a][s2][i] * exponent_of((i < 2 ? 0 : -4) - kProbE - kCodeE), exponent_of(step_e), ob[a][s2 / 2][i & 1]);
+                        fmaf(o[a][s2][i] * exponent_of(i < 2 ? 66 : 62), exponent_of(-kCodeE - 66), obs[a][s2 / 2][i & 1]);
                 else row[16 * s2 + g + 8 * (i / 2)] = o[a][s2][i];
             }
             if (g == 0 && i < 2) {
