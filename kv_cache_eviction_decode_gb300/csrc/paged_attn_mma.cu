@@ -42,8 +42,10 @@ constexpr float kSlack = 8.f;  // powers of two that a logit may exceed the maxi
 template <int D, bool Q4> struct Ring {
     static constexpr int kRow = Q4 ? D / 2 : D * 2;                            // bytes of a key, codes only
     static constexpr int kParams = Q4 ? D / 8 : 0;                             // and its groups
-    static constexpr int kStage = 2 * kPagedTile * (kRow + kParams);           // K codes, V codes, K groups, V groups
-    static constexpr int kStages = Q4 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
+    static constexpr int kTile = 2 * kPagedTile * (kRow + kParams);            // K codes, V codes, K groups, V groups
+    static constexpr int kTiles = Q4 ? 2 : 1;                                  // of a stage
+    static constexpr int kStage = kTiles * kTile;
+    static constexpr int kStages = Q4 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : 6);
     static constexpr int kWarpBytes = kStage * kStages;
 };
 
@@ -63,22 +65,22 @@ template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("c
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
-// D = A B + C with C = 0.
+// D = A B, and D += A B. (Not volatile: what they need is in their operands, and the compiler may move them.)
 __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_next(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    const uint32_t a[4] = {a0, a1, a2, a3};
-    mma_bf16_16816(d, a, b0, b1);
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 2^x, off by two steps at most; 0 below 2^-126.
@@ -110,36 +112,17 @@ __device__ __forceinline__ float bf16_part(float x, int i)
     return i == 0 ? hi : i == 1 ? mid : i == 2 ? r - mid : 0.f;
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-
 // W words of shared memory.
-template <int W> __device__ __forceinline__ void lds(uint32_t (&v)[W], uint32_t a)
+template <int W> __device__ __forceinline__ void lds(uint32_t (&v)[W], const char *a)
 {
     if constexpr (W == 4) {
-        const uint4 x = lds128(a);
+        const uint4 x = *reinterpret_cast<const uint4 *>(a);
         v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
     } else if constexpr (W == 2) {
-        const uint2 x = lds64(a);
+        const uint2 x = *reinterpret_cast<const uint2 *>(a);
         v[0] = x.x; v[1] = x.y;
     } else {
-        v[0] = lds32(a);
+        v[0] = *reinterpret_cast<const uint32_t *>(a);
     }
 }
 
@@ -153,6 +136,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
 {
     using L = Ring<D, Q4>;
     constexpr int R = 8 * NT, kGroups = D / 32, kSteps = D / 16;  // rows; groups; 16-channel steps, or tiles of O^T
+    constexpr int kTiles = L::kTiles;
     extern __shared__ __align__(16) char ring[];
     grid_dependency_wait();
     const PagedCache &c = p.c;
@@ -170,13 +154,17 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
     const AttnKeys keys = attn_keys(p.mask, sq.m, pa, pb, kPagedTile);
     const int i_lo = static_cast<int>(static_cast<long long>(keys.count) * part / p.splits);
     const int i_hi = static_cast<int>(static_cast<long long>(keys.count) * (part + 1) / p.splits);
-    const int n_mine = max(0, (i_hi - i_lo - warp + kWarps - 1) / kWarps);  // tiles i_lo + warp + kWarps k
+    // this warp's tiles come kTiles at a time: number k is i_lo + kTiles (kWarps (k / kTiles) + warp) + k % kTiles, and an
+    // odd last one is followed by one without a page
+    const int n_all = i_hi - i_lo, n_rounds = n_all / (kTiles * kWarps), n_rest = n_all - n_rounds * (kTiles * kWarps) - kTiles * warp;
+    const int n_mine = n_rounds * kTiles + min(max(n_rest, 0), kTiles);
+    const int n_stages = (n_mine + kTiles - 1) / kTiles;
     const int low_b = p.mask.window > 0 && pb >= p.mask.window ? pb - p.mask.window + 1 : 0;
 
     // Of 32 of this warp's tiles, one a lane: where their pages' blocks are, the first key, and whether every row sees
     // every key (kWhole) or there is no page (kNoPage). The next 32 tiles' pages are on their way.
     constexpr int kWhole = 1, kNoPage = 2;
-    auto first_key = [&](int k) { return attn_tile_at(keys, i_lo + warp + kWarps * k) * kPagedTile; };
+    auto first_key = [&](int k) { return attn_tile_at(keys, i_lo + kTiles * (k / kTiles * kWarps + warp) + k % kTiles) * kPagedTile; };
     auto page_at = [&](int k) { return k < n_mine ? paged_page(c, b, first_key(k)) : 0; };
     const char *block[2] = {};
     int what = 0, page_next = page_at(lane);
@@ -184,8 +172,9 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
         const int page = page_next;
         page_next = page_at(k + 32 + lane);
         const int j0 = first_key(k + lane);
-        const bool whole = page >= 0 && j0 + kPagedTile - 1 <= min(pa, sq.m - 1) && (j0 + kPagedTile <= p.mask.n_sink || j0 >= low_b);
-        what = j0 | (whole ? kWhole : 0) | (page < 0 ? kNoPage : 0);
+        const bool none = page < 0 || k + lane >= n_mine;
+        const bool whole = !none && j0 + kPagedTile - 1 <= min(pa, sq.m - 1) && (j0 + kPagedTile <= p.mask.n_sink || j0 >= low_b);
+        what = j0 | (whole ? kWhole : 0) | (none ? kNoPage : 0);
         if (page < 0) atomicOr(c.err, KVEVICT_DEV_BAD_PAGE);
 #pragma unroll
         for (int i = 0; i < 2; ++i) block[i] = c.pages[i] + max(page, 0) * c.page_bytes[i] + kvh * c.head_bytes[i];
@@ -200,18 +189,21 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
     const int k_from = ((cr & 8) + key_of(cr & 7)) * L::kRow + cch * 16, v_from = cr * L::kRow + (D == 128 ? cch ^ (cr & 2) : cch) * 16;
     const int p_from = Q4 ? c.S * L::kRow + lane % max(kPc, 1) * 16 : 0;
     uint32_t to = my_ring;  // the stage that the next copies go to
-    auto issue = [&](int k) {
-        if (k < n_mine) {
-            if ((k & 31) == 0) next_tiles(k);
-            const int w = __shfl_sync(kAll, what, k & 31);
-            const char *kb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[0]), k & 31));
-            const char *vb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[1]), k & 31));
+    auto issue = [&](int k) {  // stage k
+        if (k < n_stages) {
+            if ((k * kTiles & 31) == 0) next_tiles(k * kTiles);
+#pragma unroll
+            for (int h = 0; h < kTiles; ++h) {
+            const int from = (k * kTiles + h) & 31;
+            const int w = __shfl_sync(kAll, what, from);
+            const char *kb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[0]), from));
+            const char *vb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[1]), from));
             const int slot0 = w & (c.S - kPagedTile);
             if constexpr (Q4) {
                 if (!(w & kNoPage)) {
                     const char *kc = kb + (slot0 * L::kRow + k_from), *vc = vb + (slot0 * L::kRow + v_from);
                     const char *pc = (lane < kPc ? kb : vb) + (slot0 * L::kParams + p_from);
-                    const uint32_t dst = to + lane * 16;
+                    const uint32_t dst = to + h * L::kTile + lane * 16;
 #pragma unroll
                     for (int e0 = 0; e0 < kPagedTile * L::kRow; e0 += 512) {
                         copy16(dst + e0, kc + e0, true);
@@ -231,6 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                     copy16(to + at, kb + (slot0 + r) * c.token_bytes[0] + ch * 16, real);
                     copy16(to + kPagedTile * L::kRow + at, vb + (slot0 + r) * c.token_bytes[1] + ch * 16, real);
                 }
+            }
             }
         }
         to += L::kStage;
@@ -339,50 +332,65 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
     int whats = 0;  // of the 32 tiles that the present one is among
 
 #pragma unroll 1
-    for (int k = 0; k < n_mine; ++k) {
-        if ((k & 31) == 0) whats = what;
+    for (int k = 0; k < n_stages; ++k) {
+        if ((k * kTiles & 31) == 0) whats = what;
         copies_wait<L::kStages - 2>();
         __syncwarp();
         issue(k + L::kStages - 1);
-        const int w_ = __shfl_sync(kAll, whats, k & 31), j0 = w_ & ~(kPagedTile - 1);
-        const bool whole = w_ & kWhole;
+        const char *const sp = ring + (at - smem_u32(ring));
+        int tile_is[kTiles];
+        bool whole = true;
+#pragma unroll
+        for (int h = 0; h < kTiles; ++h) {
+            tile_is[h] = __shfl_sync(kAll, whats, (k * kTiles + h) & 31);
+            whole = whole && (tile_is[h] & kWhole);
+        }
+        // whether no row of this item sees key `key` of tile h
+        auto unseen = [&](int h, int key) {
+            const int j = (tile_is[h] & ~(kPagedTile - 1)) + key;
+            return (tile_is[h] & kNoPage) || !(j < keys.sink || (j >= keys.lo && j < keys.hi));
+        };
 
         // ---------------------------------------------------------- logits
-        float z[NT][4];
+        float z[kTiles][NT][4];
         if constexpr (Q4) {
             constexpr int W = D / 32;  // words of codes: an eighth of a row twice
-            uint32_t w0[W], w1[W], ps0[kGroups], ps1[kGroups];
-            lds(w0, at + kw_at);
-            lds(w1, at + kw_at + 8 * L::kRow);
-            lds(ps0, at + p_at);
-            lds(ps1, at + p_at + 8 * L::kParams);
-            uint32_t p0[2], p1[2];  // this lane's pair of groups
-            lds(p0, at + pair_at);
-            lds(p1, at + pair_at + 8 * L::kParams);
-            // base (sum q) - 8 step (sum q), all groups
-            const uint32_t ba0 = __byte_perm(p0[0], p0[1], 0x5410), ba1 = __byte_perm(p1[0], p1[1], 0x5410);
-            const uint32_t sp0 = __byte_perm(p0[0], p0[1], 0x7632), sp1 = __byte_perm(p1[0], p1[1], 0x7632);
+            uint32_t w0[kTiles][W], w1[kTiles][W], ps0[kTiles][kGroups], ps1[kTiles][kGroups], p0[kTiles][2], p1[kTiles][2];
 #pragma unroll
-            for (int a = 0; a < NT; ++a) {
-                mma_first(z[a], ba0, ba1, ba0, ba1, qs[a][0][0], qs[a][0][1]);
-                mma_next(z[a], sp0, sp1, sp0, sp1, qs[a][1][0], qs[a][1][1]);
-            }
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                // half word j of both eighths: channels 8 t + i below, 8 t + 4 + i above
-                const uint32_t sel = j % 2 ? 0x7632 : 0x5410;
-                const uint32_t x0 = __byte_perm(w0[j / 2], w0[W / 2 + j / 2], sel), x1 = __byte_perm(w1[j / 2], w1[W / 2 + j / 2], sel);
-                const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-                const float st0 = q4_step(ps0[j]), st1 = q4_step(ps1[j]);
+            for (int h = 0; h < kTiles; ++h) {
+                lds(w0[h], sp + h * L::kTile + kw_at);
+                lds(w1[h], sp + h * L::kTile + kw_at + 8 * L::kRow);
+                lds(ps0[h], sp + h * L::kTile + p_at);
+                lds(ps1[h], sp + h * L::kTile + p_at + 8 * L::kParams);
+                lds(p0[h], sp + h * L::kTile + pair_at);  // this lane's pair of groups
+                lds(p1[h], sp + h * L::kTile + pair_at + 8 * L::kParams);
+                // base (sum q) - 8 step (sum q), all groups
+                const uint32_t ba0 = __byte_perm(p0[h][0], p0[h][1], 0x5410), ba1 = __byte_perm(p1[h][0], p1[h][1], 0x5410);
+                const uint32_t sp0 = __byte_perm(p0[h][0], p0[h][1], 0x7632), sp1 = __byte_perm(p1[h][0], p1[h][1], 0x7632);
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    float d[4];
-                    mma_first(d, code(x0), code(x1), code16(x0), code16(x1), qf[a][2 * j][0], qf[a][2 * j][1]);
-                    mma_next(d, code(y0), code(y1), code16(y0), code16(y1), qf[a][2 * j + 1][0], qf[a][2 * j + 1][1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) z[a][i] = fmaf(i < 2 ? st0 : st1, d[i], z[a][i]);
+                    mma_first(z[h][a], ba0, ba1, ba0, ba1, qs[a][0][0], qs[a][0][1]);
+                    mma_next(z[h][a], sp0, sp1, sp0, sp1, qs[a][1][0], qs[a][1][1]);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                for (int h = 0; h < kTiles; ++h) {
+                    // half word j of both eighths: channels 8 t + i below, 8 t + 4 + i above
+                    const uint32_t sel = j % 2 ? 0x7632 : 0x5410;
+                    const uint32_t x0 = __byte_perm(w0[h][j / 2], w0[h][W / 2 + j / 2], sel), x1 = __byte_perm(w1[h][j / 2], w1[h][W / 2 + j / 2], sel);
+                    const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+                    const float st0 = q4_step(ps0[h][j]), st1 = q4_step(ps1[h][j]);
+#pragma unroll
+                    for (int a = 0; a < NT; ++a) {
+                        float d[4];
+                        mma_first(d, code(x0), code(x1), code16(x0), code16(x1), qf[a][2 * j][0], qf[a][2 * j][1]);
+                        mma_next(d, code(y0), code(y1), code16(y0), code16(y1), qf[a][2 * j + 1][0], qf[a][2 * j + 1][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[h][a][i] = fmaf(i < 2 ? st0 : st1, d[i], z[h][a][i]);
+                    }
+                }
         } else {
             uint32_t f[4];
 #pragma unroll
@@ -392,8 +400,8 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 ldsm_x4(at + r * L::kRow + ((ch & ~7) | ((ch ^ r) & 7)) * 16, f[0], f[1], f[2], f[3]);
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    if (s2 == 0) mma_first(z[a], f[0], f[1], f[2], f[3], qf[a][s2][0], qf[a][s2][1]);
-                    else mma_next(z[a], f[0], f[1], f[2], f[3], qf[a][s2][0], qf[a][s2][1]);
+                    if (s2 == 0) mma_first(z[0][a], f[0], f[1], f[2], f[3], qf[a][s2][0], qf[a][s2][1]);
+                    else mma_next(z[0][a], f[0], f[1], f[2], f[3], qf[a][s2][0], qf[a][s2][1]);
                 }
             }
         }
@@ -401,34 +409,41 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
         // --------------------------------------------------------- softmax
         if (!whole) {
 #pragma unroll
-            for (int a = 0; a < NT; ++a)
+            for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = j0 + k0 + (i < 2 ? 0 : 8), r = min(8 * a + 2 * t + (i & 1), nr - 1), pos = sq.p0 + (r0 + r) / p.G;
-                    const bool see = j <= pos && j < sq.m && (p.mask.window <= 0 || j < p.mask.n_sink || j > pos - p.mask.window);
-                    if (!see || (w_ & kNoPage)) z[a][i] = -INFINITY;
-                }
+                for (int a = 0; a < NT; ++a)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = (tile_is[h] & ~(kPagedTile - 1)) + k0 + (i < 2 ? 0 : 8);
+                        const int r = min(8 * a + 2 * t + (i & 1), nr - 1), pos = sq.p0 + (r0 + r) / p.G;
+                        const bool see = j <= pos && j < sq.m && (p.mask.window <= 0 || j < p.mask.n_sink || j > pos - p.mask.window);
+                        if (!see || (tile_is[h] & kNoPage)) z[h][a][i] = -INFINITY;
+                    }
         }
-        const uint32_t av = at + kPagedTile * L::kRow;
         uint32_t largest = 0;
-        bool move = false, odd = false;  // odd (4 bits): V's groups need a look, one by one
+        bool move = false;
         if constexpr (Q4) {
-            // two words a lane (D = 64: one) are all of V's groups
-            uint32_t v[kGroups / 2];
-            lds(v, at + kParamsAt + kPagedTile * L::kParams + lane * (2 * kGroups));
+            // two words a lane (D = 64: one) are all of V's groups of a tile
 #pragma unroll
-            for (int i = 0; i < kGroups / 2; ++i) largest = max(largest, v[i]);
-            move = largest >= step_over;
-            odd = !whole;
-            if (odd) {
-                const int j = j0 + (lane >> 1);  // the words' key; one that no row sees does not count
-                if ((w_ & kNoPage) || !(j < keys.sink || (j >= keys.lo && j < keys.hi))) move = false, largest = 0;
+            for (int h = 0; h < kTiles; ++h) {
+                uint32_t v[kGroups / 2];
+                lds(v, sp + h * L::kTile + kParamsAt + kPagedTile * L::kParams + lane * (2 * kGroups));
+                if (!whole && unseen(h, lane >> 1)) v[0] = v[kGroups / 2 - 1] = 0;  // (a key that no row sees does not count)
+#pragma unroll
+                for (int i = 0; i < kGroups / 2; ++i) largest = max(largest, v[i]);
             }
+            move = largest >= step_over;
         }
+        float top[NT][2];
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) move = move || fmaxf(z[a][i], z[a][i + 2]) > over[a][i];
+            for (int i = 0; i < 2; ++i) {
+                top[a][i] = fmaxf(z[0][a][i], z[0][a][i + 2]);
+#pragma unroll
+                for (int h = 1; h < kTiles; ++h) top[a][i] = fmaxf(top[a][i], fmaxf(z[h][a][i], z[h][a][i + 2]));
+                move = move || top[a][i] > over[a][i];
+            }
         if (__any_sync(kAll, move)) {
             float lower = 0.f, rise = 0.f;
             if constexpr (Q4) {
@@ -443,7 +458,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             for (int a = 0; a < NT; ++a)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float mx = fmaxf(z[a][i], z[a][i + 2]) * sl2[a][i];
+                    float mx = top[a][i] * sl2[a][i];
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, w));
                     const float mn = fmaxf(rise - nm[a][i], mx - lower), f = pow2(-nm[a][i] - mn);
@@ -460,81 +475,86 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 }
         }
 #pragma unroll
-        for (int a = 0; a < NT; ++a)
+        for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                z[a][i] = pow2(fmaf(z[a][i], sl2[a][i & 1], nm[a][i & 1]));
-                l[a][i & 1] += z[a][i];
-            }
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    z[h][a][i] = pow2(fmaf(z[h][a][i], sl2[a][i & 1], nm[a][i & 1]));
+                    l[a][i & 1] += z[h][a][i];
+                }
 
         // --------------------------------------------------------- outputs
         if constexpr (Q4) {
             constexpr int W = D / 64;  // words of an eighth of a row
-            uint32_t w[4][W], vs0[kGroups], vs1[kGroups], vb[4][1];
+            uint32_t w[kTiles][4][W], vs0[kTiles][kGroups], vs1[kTiles][kGroups], vb[kTiles][4][1];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lds(w[i], at + vw_at + 4 * i * L::kRow);
-            lds(vs0, at + p_at + 16 * L::kParams);
-            lds(vs1, at + p_at + 24 * L::kParams);
+            for (int h = 0; h < kTiles; ++h) {
+                const char *const tp = sp + h * L::kTile;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lds(vb[i], at + vb_at + 4 * i * L::kParams);  // group g (mod kGroups) of this lane's four keys
-            if (odd) {
-                // a row takes nothing of a key that it does not see, whatever that stands for; one that sees NaN gets it
+                for (int i = 0; i < 4; ++i) lds(w[h][i], tp + vw_at + 4 * i * L::kRow);
+                lds(vs0[h], tp + p_at + 16 * L::kParams);
+                lds(vs1[h], tp + p_at + 24 * L::kParams);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool nan = !finite_group(vb[i][0]);
-                    if (nan) vb[i][0] = 0;
-                    if ((w_ & kNoPage) || !(j0 + 4 * i + t < keys.sink || (j0 + 4 * i + t >= keys.lo && j0 + 4 * i + t < keys.hi))) vb[i][0] = 0;
+                for (int i = 0; i < 4; ++i) lds(vb[h][i], tp + vb_at + 4 * i * L::kParams);  // group g (mod kGroups) of this lane's four keys
+                if (!whole) {
+                    // a row takes nothing of a key that it does not see, whatever that stands for; one that sees NaN gets it
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!finite_group(vb[h][i][0]) || unseen(h, 4 * i + t)) vb[h][i][0] = 0;
+#pragma unroll
+                    for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t &v = e ? vs1[h][j] : vs0[h][j];
+                            const bool none = unseen(h, k0 + 8 * e), nan = !finite_group(v) && !none;
+                            if (none || nan) v = 0;
+#pragma unroll
+                            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    // (each row of the product of the bases is a group: the lanes with g = j take it up)
+                                    const bool hit = __reduce_or_sync(kAll, nan && z[h][a][2 * e + i] != 0.f ? 1u << t : 0u) >> t & 1;
+                                    if (hit && (g & (kGroups - 1)) == j) ob[a][i] = __uint_as_float(0x7FC00000u);
+                                }
+                        }
                 }
+                const uint32_t va0 = __byte_perm(vb[h][0][0], vb[h][1][0], 0x5410), va1 = __byte_perm(vb[h][2][0], vb[h][3][0], 0x5410);
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j)
+                for (int a = 0; a < NT; ++a)
+                    mma_next(ob[a], va0, 0, va1, 0, transpose8x8(pack_bf16x2(z[h][a][0], z[h][a][1])),
+                             transpose8x8(pack_bf16x2(z[h][a][2], z[h][a][3])));
+            }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t &v = e ? vs1[j] : vs0[j];
-                        const int key = j0 + k0 + 8 * e;
-                        const bool none = (w_ & kNoPage) || !(key < keys.sink || (key >= keys.lo && key < keys.hi)), nan = !finite_group(v) && !none;
-                        if (none || nan) v = 0;
+            for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-                        for (int a = 0; a < NT; ++a)
+                for (int h = 0; h < kTiles; ++h) {
+                    const uint32_t sel = j % 2 ? 0x7632 : 0x5410;
+                    const uint32_t x0 = __byte_perm(w[h][0][j / 2], w[h][1][j / 2], sel), x1 = __byte_perm(w[h][2][j / 2], w[h][3][j / 2], sel);
+                    const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+                    const float st0 = q4_step(vs0[h][j]), st1 = q4_step(vs1[h][j]);
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                // (each row of the product of the bases is a group: the lanes with g = j take it up)
-                                const bool hit = __reduce_or_sync(kAll, nan && z[a][2 * e + i] != 0.f ? 1u << t : 0u) >> t & 1;
-                                if (hit && (g & (kGroups - 1)) == j) ob[a][i] = __uint_as_float(0x7FC00000u);
-                            }
+                    for (int a = 0; a < NT; ++a) {
+                        const uint32_t b0 = transpose8x8(pack_bf16x2(z[h][a][0] * st0, z[h][a][1] * st0));
+                        const uint32_t b1 = transpose8x8(pack_bf16x2(z[h][a][2] * st1, z[h][a][3] * st1));
+                        mma_next(o[a][2 * j], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
+                        mma_next(o[a][2 * j + 1], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
+                        mma_next(o[a][2 * j], code(x0), code16(x0), code(x1), code16(x1), b0, b1);
+                        mma_next(o[a][2 * j + 1], code(y0), code16(y0), code(y1), code16(y1), b0, b1);
                     }
-            }
-            const uint32_t va0 = __byte_perm(vb[0][0], vb[1][0], 0x5410), va1 = __byte_perm(vb[2][0], vb[3][0], 0x5410);
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-                mma_next(ob[a], va0, 0, va1, 0, transpose8x8(pack_bf16x2(z[a][0], z[a][1])), transpose8x8(pack_bf16x2(z[a][2], z[a][3])));
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                const uint32_t sel = j % 2 ? 0x7632 : 0x5410;
-                const uint32_t x0 = __byte_perm(w[0][j / 2], w[1][j / 2], sel), x1 = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
-                const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
-                const float st0 = q4_step(vs0[j]), st1 = q4_step(vs1[j]);
-#pragma unroll
-                for (int a = 0; a < NT; ++a) {
-                    const uint32_t b0 = transpose8x8(pack_bf16x2(z[a][0] * st0, z[a][1] * st0));
-                    const uint32_t b1 = transpose8x8(pack_bf16x2(z[a][2] * st1, z[a][3] * st1));
-                    mma_next(o[a][2 * j], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
-                    mma_next(o[a][2 * j + 1], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
-                    mma_next(o[a][2 * j], code(x0), code16(x0), code(x1), code16(x1), b0, b1);
-                    mma_next(o[a][2 * j + 1], code(y0), code16(y0), code(y1), code16(y1), b0, b1);
                 }
-            }
         } else {
             uint32_t b0[NT], b1[NT], f[4];
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
-                b0[a] = transpose8x8(pack_bf16x2(z[a][0], z[a][1]));
-                b1[a] = transpose8x8(pack_bf16x2(z[a][2], z[a][3]));
+                b0[a] = transpose8x8(pack_bf16x2(z[0][a][0], z[0][a][1]));
+                b1[a] = transpose8x8(pack_bf16x2(z[0][a][2], z[0][a][3]));
             }
 #pragma unroll
             for (int s2 = 0; s2 < kSteps; ++s2) {
                 // matrices, transposed: channels 16 s / 16 s + 8, keys 0-7 / 8-15
                 const int r = (lane & 7) + (lane >> 4) * 8, ch = 2 * s2 + (lane >> 3 & 1);
-                ldsm_x4_trans(av + r * L::kRow + ((ch & ~7) | ((ch ^ r) & 7)) * 16, f[0], f[1], f[2], f[3]);
+                ldsm_x4_trans(at + kPagedTile * L::kRow + r * L::kRow + ((ch & ~7) | ((ch ^ r) & 7)) * 16, f[0], f[1], f[2], f[3]);
 #pragma unroll
                 for (int a = 0; a < NT; ++a) mma_next(o[a][s2], f[0], f[1], f[2], f[3], b0[a], b1[a]);
             }
