@@ -113,19 +113,25 @@ int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens)
     return std::min(all, (static_cast<int64_t>(n_sink) + kPagedTile - 1) / kPagedTile + (window + tokens - 1 + kPagedTile - 1) / kPagedTile + 1);
 }
 
-// Parts that the keys of a unit are split into: items run in waves of `slots` CTAs,
-// and one takes the tiles of a warp and kItemCost tiles more for its start and end;
-// joining the parts costs kJoinCost.
-constexpr double kItemCost = 4, kJoinCost = 5;
+// Parts that the keys of a unit are split into. An item takes the tiles of a warp
+// and `item` tiles more for its start and end, joining the parts costs kJoinCost.
+// Items under a window are of one length and run in waves of `slots` CTAs. Without
+// one their lengths are on the device, and taken to spread around kShare of the
+// longest: the slots are then filled but for half an item at the end. (4 bits, 256
+// units of up to 2048 tiles: 316, 231, 221, 224 and 245 us with 1, 4, 7, 10 and 20
+// parts; bf16, 256 units of up to 640: 167, 149, 152 and 164 us with 1, 5, 10 and
+// 16; 4 bits, 128 units of 130 under a window: 41, 31, 41 us with 1, 2 and 3.)
+constexpr double kJoinCost = 4, kShare = 0.75;
 
-int parts(int64_t units, int64_t tiles, int64_t slots)
+int parts(int64_t units, int64_t tiles, int64_t slots, double item, bool window)
 {
     int best = 1;
     double least = 0;
     for (int64_t s = 1; s <= kMaxParts && (s == 1 || s * kPagedMmaWarps <= tiles); ++s) {
-        const double waves = std::ceil(static_cast<double>(units * s) / static_cast<double>(slots));
-        const double cost = waves * (std::ceil(static_cast<double>(tiles) / static_cast<double>(s * kPagedMmaWarps)) + kItemCost) + (s > 1 ? kJoinCost : 0);
-        if (s == 1 || cost < least * 0.97) {
+        const double load = static_cast<double>(units * s) / static_cast<double>(slots);
+        const double len = std::ceil(static_cast<double>(tiles) / static_cast<double>(s * kPagedMmaWarps)), longest = len + item;
+        const double cost = (window ? std::ceil(load) * longest : std::max(longest, load * (len * kShare + item) + longest / 2)) + (s > 1 ? kJoinCost : 0);
+        if (s == 1 || cost < least * 0.99) {
             least = cost;
             best = static_cast<int>(s);
         }
@@ -153,7 +159,10 @@ int plan_attention(const kvevict_paged_attention_args *a, Plan &w)
     p.q_tiles = static_cast<int>((rows + w.rows - 1) / w.rows);
     const int64_t units = static_cast<int64_t>(a->c.batch) * a->c.n_kv_heads * p.q_tiles;
     const int64_t tiles = key_tiles(max_k, p.mask.n_sink, p.mask.window, std::min<int64_t>(p.max_q, (w.rows + p.G - 1) / p.G + 1));
-    p.splits = parts(units, tiles, kSMs * (!tensor || (q4 && w.rows == 8) ? 3 : 2));
+    // (with starts only the mean of the new tokens is known here)
+    const int64_t mean = a->c.batch ? (a->tokens + a->c.batch - 1) / a->c.batch * p.G : 0;
+    const int64_t busy = static_cast<int64_t>(a->c.batch) * a->c.n_kv_heads * std::min<int64_t>(p.q_tiles, (mean + w.rows - 1) / w.rows);
+    p.splits = parts(busy, tiles, kSMs * (!tensor || (q4 && w.rows == 8) ? 3 : 2), q4 ? 6 : 3, p.mask.window > 0);
     w.items = units * p.splits;
     if (w.items >= (int64_t{1} << 31)) return KVEVICT_ERR_INVALID_ARG;
     const size_t slots = static_cast<size_t>(p.splits) * a->tokens * p.Hq;

@@ -11,15 +11,15 @@
 //
 // 4 bits: a code needs a mask and nothing else to be a matrix operand. bf16's bit
 // patterns 0 .. 255 are the values 0 .. 255 times 2^-133 (its subnormals and, with
-// the same spacing, the first normal numbers), so c and 16 c are read off as they
-// lie in a half word, two bits of work a channel. Queries are scaled by a power of
+// the same spacing, the first normal numbers), so c, 16 c and a byte of
+// two codes are read off as they lie in a half word. Queries are scaled by a power of
 // two to at most 2^101, a sixteenth of it for every second channel, and
 //   S_ij = sum_groups step (sum_c c q) + (base - 8 step) (sum q),
 // the sums over a group in fp32. In the second product the step goes into the
 // probabilities, which are then rounded to bf16, once, and scaled by a power of two
 // that follows the largest step seen:
 //   O_i = sum_j (p_ij step_j) (c_j - 8) + sum_j p_ij base_j,
-// the 8 taken off by an instruction with constant codes, the base's part in fp32.
+// the 8 taken off the codes, exactly, the base's part in an instruction of its own.
 //
 // The running maximum is moved only where a logit exceeds it by 2^8 or more: then,
 // and only then, sums and outputs are rescaled. Probabilities below 2^8 instead of
@@ -39,19 +39,19 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kSlack = 8.f;  // powers of two that a logit may exceed the maximum by
 
-template <int D, bool Q4> struct Ring {
+template <int D, bool Q4, int NT> struct Ring {
     static constexpr int kRow = Q4 ? D / 2 : D * 2;                            // bytes of a key, codes only
     static constexpr int kParams = Q4 ? D / 8 : 0;                             // and its groups
     static constexpr int kTile = 2 * kPagedTile * (kRow + kParams);            // K codes, V codes, K groups, V groups
-    static constexpr int kTiles = Q4 ? 2 : 1;                                  // of a stage
+    static constexpr int kTiles = Q4 && NT == 1 ? 2 : 1;                                  // of a stage
     static constexpr int kStage = kTiles * kTile;
-    static constexpr int kStages = Q4 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : 6);
+    static constexpr int kStages = Q4 ? (D == 128 ? 6 : 8) / kTiles : (D == 128 ? 3 : 6);
     static constexpr int kWarpBytes = kStage * kStages;
 };
 
 template <int D, bool Q4, int NT> constexpr int smem_bytes()
 {
-    constexpr int ring = Ring<D, Q4>::kWarpBytes * kWarps, join = kWarps * 8 * NT * (D + 4 + 2) * 4;
+    constexpr int ring = Ring<D, Q4, NT>::kWarpBytes * kWarps, join = kWarps * 8 * NT * (D + 4 + 2) * 4;
     return ring > join ? ring : join;
 }
 
@@ -92,11 +92,19 @@ __device__ __forceinline__ float pow2(float x)
 }
 
 // Codes of two keys or channels, one in each half word, as bf16: c 2^-133, and
-// from the next nibble 16 c 2^-133.
+// from the next nibble 16 c 2^-133. Or a byte of each, c + 16 c' of two nibbles.
 __device__ __forceinline__ uint32_t code(uint32_t x) { return x & 0x000F000Fu; }
 __device__ __forceinline__ uint32_t code16(uint32_t x) { return x & 0x00F000F0u; }
+// Such a code less 8, such a byte less 136 (8 of either nibble): exact.
+template <int N> __device__ __forceinline__ uint32_t less(uint32_t x)
+{
+    uint32_t y;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(N * 0x00010001u));
+    return y;
+}
+__device__ __forceinline__ uint32_t low_bytes(uint32_t x) { return x & 0x00FF00FFu; }
+__device__ __forceinline__ uint32_t high_bytes(uint32_t x) { return __byte_perm(x, 0u, 0x4341); }
 __device__ __forceinline__ bool finite_group(uint32_t v) { return (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u; }
-constexpr uint32_t kMinus8 = 0x80088008u, kMinus8x16 = 0x80808080u;  // -8 as such a code
 
 __device__ __forceinline__ float exponent_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // 2^e
 
@@ -134,7 +142,7 @@ __device__ __forceinline__ int key_of(int r) { return (r & 1) * 4 + (r >> 1); }
 template <int D, bool Q4, int NT>
 __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kernel(const __grid_constant__ PagedAttnParams p)
 {
-    using L = Ring<D, Q4>;
+    using L = Ring<D, Q4, NT>;
     constexpr int R = 8 * NT, kGroups = D / 32, kSteps = D / 16;  // rows; groups; 16-channel steps, or tiles of O^T
     constexpr int kTiles = L::kTiles;
     extern __shared__ __align__(16) char ring[];
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
 
     // ---------------------------------------------------------------- queries, row n = 8 a + g
     uint32_t qf[NT][kSteps][2];
-    uint32_t qs[NT][2][2];       // 4 bits: of each group the sum of row g, and -8 of it, in three bf16 parts (see below)
+    uint32_t qs[NT][2][2];       // 4 bits: of each group the sum of row g, and -8 of it, in bf16 parts (see below)
     float sl2[NT][2];            // what turns those rows' products into logits to base 2
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
@@ -531,16 +539,16 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                 for (int h = 0; h < kTiles; ++h) {
                     const uint32_t sel = j % 2 ? 0x7632 : 0x5410;
                     const uint32_t x0 = __byte_perm(w[h][0][j / 2], w[h][1][j / 2], sel), x1 = __byte_perm(w[h][2][j / 2], w[h][3][j / 2], sel);
-                    const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+                    const uint32_t y0 = high_bytes(x0), y1 = high_bytes(x1), v0 = low_bytes(x0), v1 = low_bytes(x1);
                     const float st0 = q4_step(vs0[h][j]), st1 = q4_step(vs1[h][j]);
 #pragma unroll
                     for (int a = 0; a < NT; ++a) {
                         const uint32_t b0 = transpose8x8(pack_bf16x2(z[h][a][0] * st0, z[h][a][1] * st0));
                         const uint32_t b1 = transpose8x8(pack_bf16x2(z[h][a][2] * st1, z[h][a][3] * st1));
-                        mma_next(o[a][2 * j], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
-                        mma_next(o[a][2 * j + 1], kMinus8, kMinus8x16, kMinus8, kMinus8x16, b0, b1);
-                        mma_next(o[a][2 * j], code(x0), code16(x0), code(x1), code16(x1), b0, b1);
-                        mma_next(o[a][2 * j + 1], code(y0), code16(y0), code(y1), code16(y1), b0, b1);
+                        
+                        
+                        mma_next(o[a][2 * j], less<8>(code(v0)), less<136>(v0), less<8>(code(v1)), less<136>(v1), b0, b1);
+                        mma_next(o[a][2 * j + 1], less<8>(code(y0)), less<136>(y0), less<8>(code(y1)), less<136>(y1), b0, b1);
                     }
                 }
         } else {
@@ -590,10 +598,11 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             float *row = so + (warp * R + 8 * a + 2 * t + (i & 1)) * kPad;
 #pragma unroll
             for (int s2 = 0; s2 < kSteps; ++s2) {
-                // 4 bits: tile 2 j + h has channels 32 j + 4 g + 2 h, and the next one
+                // 4 bits: tile 2 j + h has channel 32 j + 4 g + 2 h, and it with 16 times the next one
                 if constexpr (Q4)
                     row[32 * (s2 / 2) + 4 * g + 2 * (s2 % 2) + i / 2] =
-                        fmaf(o[a][s2][i] * exponent_of(i < 2 ? 66 : 62), exponent_of(-kCodeE - 66), obs[a][s2 / 2][i & 1]);
+                        fmaf((i < 2 ? o[a][s2][i] : (o[a][s2][i] - o[a][s2][i & 1]) * 0.0625f) * exponent_of(66), exponent_of(-kCodeE - 66),
+                             obs[a][s2 / 2][i & 1]);
                 else row[16 * s2 + g + 8 * (i / 2)] = o[a][s2][i];
             }
             if (g == 0 && i < 2) {
