@@ -1,13 +1,16 @@
 // norm_rotary.cu -- kvevict_norm_rotary: the root-mean-square norm of every head
 // of queries and keys and its rotary positions, in one launch.
 //
-// y = x r w, r = 1 / sqrt(mean x^2 + eps), then every pair of y turns. Bound by
-// bytes: a head is read once and written once, so its lanes keep it in registers
-// while its squares are summed. A head's lanes are a power of two of neighbours in
-// a warp (its units of 16-byte chunks, as in rotary.cu: a pair of chunks
-// rotary_dim / 2 apart, a chunk of neighbouring pairs, or one that does not turn);
-// the sum takes log2 of them shuffles, and nothing else is exchanged. All in fp32,
-// rounded once.
+// y = x w r, r = 1 / sqrt(mean x^2 + eps), then every pair of y turns. A head is read
+// once and written once; beside these bytes the instructions count (121 us for 16384
+// tokens of 64 + 8 heads of 128 with an address worked out for each head, 110 now,
+// 103 for the rotation alone in rotary.cu). So a head's lanes, a
+// power of two of neighbours in a warp, take two 16-byte chunks each (a pair
+// rotary_dim / 2 apart, or two of neighbouring pairs or of elements that do not
+// turn), walk from head to head by adding strides, keep the weights as fp32, and
+// fold r into cosine and sine. What a thread reads comes through places of its own
+// in shared memory, three heads ahead, without registers and (since it reads only
+// its own copies) without a barrier. All in fp32, rounded once.
 #include <algorithm>
 #include <cmath>
 
@@ -22,109 +25,201 @@ struct NormParams {
     RotParams r;
     const void *w[2];  // q's, k's weights
     float eps;
-    uint32_t lanes;    // of a head: a power of two, at least its units
+    uint32_t lanes;    // of a head: a power of two, at least half its chunks
 };
 
-// Units of one thread, as in rotary_kernel. A thread's unit within the head stays;
-// it walks the CTA's heads, kBatch of them in flight.
+// 16 bytes global -> shared without a register between.
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A thread's way through the (token, head) rows of a CTA, `step` rows at a time: a
+// pointer that follows the strides.
+struct Walk {
+    char *p;
+    int h, t, ts;  // head, token of the CTA, token of its sequence
+    int nh, tokens, heads_on, tokens_on;           // a step: so many heads and whole tokens on
+    long long by_step, by_token, by_seq;           // bytes: a step; from behind the last head to the next token; over a sequence's end
+
+    __device__ __forceinline__ void start(char *base, const long long (&s)[3], int elem, long long b, int token, int heads, int step, int first, int per)
+    {
+        nh = heads;
+        tokens = per;
+        heads_on = step % nh;
+        tokens_on = step / nh;
+        by_token = (s[2] - nh * s[1]) * elem;
+        by_step = (heads_on * s[1] + tokens_on * s[2]) * elem;
+        by_seq = (s[0] - tokens * s[2]) * elem;
+        h = first % nh;
+        t = first / nh;
+        ts = token + t;
+        p = base + (b * s[0] + ts * s[2] + h * s[1]) * elem;
+        ends();
+    }
+    __device__ __forceinline__ void ends()
+    {
+        if (ts >= tokens) {
+            const int n = ts / tokens;
+            ts -= n * tokens;
+            p += n * by_seq;
+        }
+    }
+    __device__ __forceinline__ void on()
+    {
+        int dt = tokens_on;
+        h += heads_on;
+        p += by_step;
+        if (h >= nh) {
+            h -= nh;
+            p += by_token;
+            ++dt;
+        }
+        t += dt;
+        ts += dt;
+        ends();
+    }
+};
+
+constexpr int kNormStages = 4;
+
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, 4) norm_rotary_kernel(const __grid_constant__ NormParams np)
 {
-    constexpr int N = Vec<T>::N, kBatch = INTER ? 4 : 2;
+    constexpr int N = Vec<T>::N, kLines = INTER ? N / 4 : N / 2;  // 16-byte lines of cosines and sines of a chunk (pair)
     const RotParams &p = np.r;
-    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    extern __shared__ __align__(16) char sh[];
+    uint4 *const own = reinterpret_cast<uint4 *>(sh) + threadIdx.x;                                     // [stages][2][threads]
+    float4 *const cs = reinterpret_cast<float4 *>(sh + kNormStages * 2 * kRotThreads * 16);  // [tokens_per][lines][R / N, or half of it]
     grid_dependency_wait();
-    const uint32_t half = p.R / 2;
-    const uint32_t pairs = INTER ? 0 : half / N;
-    const uint32_t units = INTER ? p.D / N : pairs + (p.D - p.R) / N;
-    const uint32_t tok0 = blockIdx.x / p.head_blocks * p.tokens_per;
-    const uint32_t nt = min(p.tokens_per, static_cast<uint32_t>(p.total) - tok0);
-    const uint32_t h0 = blockIdx.x % p.head_blocks * p.heads_per;
-    const uint32_t nh = min(p.heads_per, static_cast<uint32_t>(p.heads[0] + p.heads[1]) - h0);
-    const uint32_t step = kRotThreads / np.lanes, u = threadIdx.x & (np.lanes - 1);
-    const bool mine = u < units;
-    const bool two = !INTER && u < pairs;
-    const uint32_t c = !mine ? 0 : INTER || u < pairs ? u * N : p.R + (u - pairs) * N;
-    const uint32_t rows = nt * nh;
-    uint32_t row = threadIdx.x / np.lanes;
+    const int half = p.R / 2, chunks = p.D / N, turning = INTER ? p.R / N : half / N;  // (half layout: pairs of chunks)
+    const int tok0 = blockIdx.x / p.head_blocks * p.tokens_per;
+    const int nt = min(static_cast<int>(p.tokens_per), static_cast<int>(p.total - tok0));
+    const int h0 = blockIdx.x % p.head_blocks * p.heads_per;
+    const int nh_all = min(static_cast<int>(p.heads_per), p.heads[0] + p.heads[1] - h0);
+    const int step = kRotThreads / np.lanes, first = threadIdx.x / np.lanes, u = threadIdx.x & (np.lanes - 1);
+    const int tokens = static_cast<int>(p.tokens);
+    const long long b0 = tok0 / tokens;
+    const int t0 = tok0 - static_cast<int>(b0) * tokens;
+    // this lane's chunks, and which lines of the table they use
+    const bool mine = 2 * u < chunks, turn = INTER ? 2 * u < turning : u < turning, turn2 = INTER && 2 * u + 1 < turning;
+    const int ca = !mine ? 0 : INTER ? 2 * u * N : u < turning ? u * N : p.R + 2 * (u - turning) * N;
+    const int cb = !mine ? 0 : !INTER && u < turning ? ca + half : ca + N;
     const float over_d = 1.f / static_cast<float>(p.D);
+    const int per_token = kLines * turning;
     bool ready = false;
-    for (uint32_t row0 = 0; row0 < rows; row0 += step * kBatch) {
-        uint4 a[kBatch], b[kBatch];
-        T *y[kBatch];
-        uint32_t tk[kBatch];
-        bool key[kBatch];
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {  // queries, keys
+        const int ha = w ? max(h0 - p.heads[0], 0) : h0, hz = w ? h0 + nh_all - p.heads[0] : min(h0 + nh_all, p.heads[0]);
+        const int nh = hz - ha;
+        if (nh <= 0) continue;
+        Walk in, out;
+        in.start(const_cast<char *>(static_cast<const char *>(p.x[w])) + (ha * p.xs[w][1] + ca) * static_cast<int>(sizeof(T)), p.xs[w], sizeof(T), b0, t0, nh, step,
+                 first, tokens);
+        out.start(static_cast<char *>(p.y[w]) + (ha * p.ys[w][1] + ca) * static_cast<int>(sizeof(T)), p.ys[w], sizeof(T), b0, t0, nh, step, first, tokens);
+        const int apart = (cb - ca) * static_cast<int>(sizeof(T));
+        int to = 0;
+        auto load = [&]() {
+            if (in.t < nt && mine) {
+                copy16(own + to, in.p);
+                copy16(own + to + kRotThreads, in.p + apart);
+            }
+            copies_close();
+            to = to == (kNormStages - 1) * 2 * kRotThreads ? 0 : to + 2 * kRotThreads;
+            in.on();
+        };
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i, row += step) {
-            y[i] = nullptr;
-            key[i] = false;
-            a[i] = b[i] = make_uint4(0, 0, 0, 0);
-            tk[i] = row / nh;
-            if (row >= rows || !mine) continue;
-            const uint32_t hh = h0 + row - tk[i] * nh;
-            const bool k = hh >= static_cast<uint32_t>(p.heads[0]);
-            const uint32_t hl = k ? hh - p.heads[0] : hh;
-            const uint32_t bt = tok0 + tk[i], bb = bt / static_cast<uint32_t>(p.tokens), t = bt - bb * static_cast<uint32_t>(p.tokens);
-            const T *x = static_cast<const T *>(p.x[k]) + bb * p.xs[k][0] + t * p.xs[k][2] + hl * p.xs[k][1] + c;
-            y[i] = static_cast<T *>(p.y[k]) + bb * p.ys[k][0] + t * p.ys[k][2] + hl * p.ys[k][1] + c;
-            key[i] = k;
-            a[i] = *reinterpret_cast<const uint4 *>(x);
-            if (two) b[i] = *reinterpret_cast<const uint4 *>(x + half);
-        }
+        for (int i = 0; i < kNormStages - 1; ++i) load();
+        float wa[N], wb[N];
+        unpack16(*reinterpret_cast<const uint4 *>(static_cast<const T *>(np.w[w]) + ca), wa);
+        unpack16(*reinterpret_cast<const uint4 *>(static_cast<const T *>(np.w[w]) + cb), wb);
         if (!ready) {
-            for (uint32_t i = threadIdx.x; i < nt * half; i += kRotThreads) {
-                const uint32_t t0 = i / half, bt = tok0 + t0, bb = bt / static_cast<uint32_t>(p.tokens);
-                const long long t = bt - bb * static_cast<uint32_t>(p.tokens);
-                cs[i] = rot_cos_sin(p.freq[i - t0 * half], rot_position(p, bb, t), p.scale, false);
+            // pair f: (INTER) chunk 2 f / N, else pair of chunks f / N; lines of two pairs lie beside those of the other chunks
+            for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
+                const int lt = i / half, f = i - lt * half, in_chunk = INTER ? N / 2 : N;
+                const int q = f / in_chunk, e = f - q * in_chunk;
+                const int bt = tok0 + lt, b = bt / tokens;
+                reinterpret_cast<float2 *>(cs)[((lt * kLines + e / 2) * turning + q) * 2 + (e & 1)] =
+                    rot_cos_sin(p.freq[f], rot_position(p, b, bt - static_cast<long long>(b) * tokens), p.scale, false);
             }
             __syncthreads();
             ready = true;
         }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
+        const int trips = (nt * nh + step - 1) / step;
+        int at = 0;
+#pragma unroll 1
+        for (int trip = 0; trip < trips; ++trip) {
+            copies_wait<kNormStages - 2>();
             float v[N], z[N], sum = 0.f;
-            unpack16(a[i], v);
-            unpack16(b[i], z);
+            const bool real = out.t < nt && mine;
+            unpack16(real ? own[at] : make_uint4(0, 0, 0, 0), v);
+            unpack16(real ? own[at + kRotThreads] : make_uint4(0, 0, 0, 0), z);
+            at = at == (kNormStages - 1) * 2 * kRotThreads ? 0 : at + 2 * kRotThreads;
+            load();
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 sum = fmaf(v[j], v[j], sum);
-                if (!INTER) sum = fmaf(z[j], z[j], sum);
+                sum = fmaf(z[j], z[j], sum);
             }
             for (uint32_t o = np.lanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (!y[i]) continue;
             const float r = rsqrtf(fmaf(sum, over_d, np.eps));
-            const T *wp = static_cast<const T *>(np.w[key[i]]) + c;
-            const float2 *k = cs + tk[i] * half + (INTER ? c / 2 : c);
-            float w[N];
-            unpack16(*reinterpret_cast<const uint4 *>(wp), w);
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] *= r * w[j];
-            if (INTER) {
-                if (c < static_cast<uint32_t>(p.R)) {
-#pragma unroll
-                    for (int j = 0; j < N; j += 2) {
-                        const float x = v[j], e = v[j + 1];
-                        v[j] = x * k[j / 2].x - e * k[j / 2].y;
-                        v[j + 1] = x * k[j / 2].y + e * k[j / 2].x;
-                    }
-                }
-            } else if (two) {
-                unpack16(*reinterpret_cast<const uint4 *>(wp + half), w);
+            if (real) {
+                const float4 *k = cs + out.t * per_token;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float x = v[j], e = z[j] * (r * w[j]);
-                    v[j] = x * k[j].x - e * k[j].y;
-                    z[j] = x * k[j].y + e * k[j].x;
+                    v[j] *= wa[j];
+                    z[j] *= wb[j];
                 }
-                *reinterpret_cast<uint4 *>(y[i] + half) = pack16(z);
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int l = 0; l < 2; ++l) {
+                        float(&x)[N] = l ? z : v;
+                        if (l ? turn2 : turn) {
+#pragma unroll
+                            for (int j = 0; j < N; j += 4) {
+                                const float4 c = k[j / 4 * turning + 2 * u + l];
+                                const float a0 = x[j] * r, b0_ = x[j + 1] * r, a1 = x[j + 2] * r, b1 = x[j + 3] * r;
+                                x[j] = a0 * c.x - b0_ * c.y;
+                                x[j + 1] = a0 * c.y + b0_ * c.x;
+                                x[j + 2] = a1 * c.z - b1 * c.w;
+                                x[j + 3] = a1 * c.w + b1 * c.z;
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < N; ++j) x[j] *= r;
+                        }
+                    }
+                } else if (turn) {
+#pragma unroll
+                    for (int j = 0; j < N; j += 2) {
+                        const float4 c = k[j / 2 * turning + u];
+                        const float c0 = c.x * r, s0 = c.y * r, c1 = c.z * r, s1 = c.w * r;
+                        const float a0 = v[j], a1 = v[j + 1], e0 = z[j], e1 = z[j + 1];
+                        v[j] = a0 * c0 - e0 * s0;
+                        z[j] = a0 * s0 + e0 * c0;
+                        v[j + 1] = a1 * c1 - e1 * s1;
+                        z[j + 1] = a1 * s1 + e1 * c1;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        v[j] *= r;
+                        z[j] *= r;
+                    }
+                }
+                *reinterpret_cast<uint4 *>(out.p) = pack16(v);
+                *reinterpret_cast<uint4 *>(out.p + apart) = pack16(z);
             }
-            *reinterpret_cast<uint4 *>(y[i]) = pack16(v);
+            out.on();
         }
+        copies_wait<0>();
     }
 }
 
-// Heads of more than 32 units, and rotary parts whose pairs do not fall into
-// 16-byte chunks. One CTA per token, a warp per head, which passes through shared
+// Heads of more than 64 or an odd number of chunks, and rotary parts whose pairs do
+// not fall into 16-byte chunks. One CTA per token, a warp per head, which passes through shared
 // memory as fp32; it is read whole before any of it is written, so that in place
 // needs no care.
 template <typename T>
@@ -181,19 +276,56 @@ __global__ void __launch_bounds__(kRotThreads) norm_rotary_any_kernel(const __gr
     }
 }
 
+// A CTA's share of tokens (all heads), or of one token's heads where there are few
+// tokens: what lets whole waves of four CTAs an SM end soonest, a CTA taking what
+// its rows take and as much as kStart times its 256 threads' rows to find its way
+// and its cosines. (16384 tokens, 64 + 8 heads of 128: 110 us, 81% of the copy
+// bandwidth, 111 with 4 tokens a CTA; 3 x 2049 tokens, 12 + 4 heads, 48 of 128 in
+// fp32: 26 us, 30 with ten tokens a CTA.)
+constexpr int kStart = 5;
+
+long long norm_shares(NormParams &np)
+{
+    RotParams &p = np.r;
+    const long long heads = p.heads[0] + p.heads[1], step = kRotThreads / np.lanes, slots = 4 * 152;
+    p.heads_per = static_cast<uint32_t>(heads);
+    p.head_blocks = 1;
+    p.tokens_per = 1;
+    if (p.total < slots / 2) {
+        // few tokens: two trips of a CTA's threads at most
+        const long long want = std::max(step, p.total * heads / (slots / 2));
+        p.heads_per = static_cast<uint32_t>(std::min(heads, want));
+        p.head_blocks = static_cast<uint32_t>((heads + p.heads_per - 1) / p.heads_per);
+        return p.total * p.head_blocks;
+    }
+    double least = 0;
+    for (long long t = 1; t <= std::min<long long>(64, 8192 / std::max(p.R, 2)); ++t) {
+        const long long waves = ((p.total + t - 1) / t + slots - 1) / slots;
+        const double cost = static_cast<double>(waves) * (static_cast<double>(t * heads) / static_cast<double>(step) + kStart);
+        if (t == 1 || cost < least * 0.995) {
+            least = cost;
+            p.tokens_per = static_cast<uint32_t>(t);
+        }
+    }
+    return (p.total + p.tokens_per - 1) / p.tokens_per;
+}
+
 template <typename T> cudaError_t launch_norm(NormParams &np, bool chunks, uint32_t units, cudaStream_t st, int &rc)
 {
     RotParams &p = np.r;
     if (chunks) {
         np.lanes = 1;
         while (np.lanes < units) np.lanes *= 2;
-        const long long blocks = rot_shares(p, units);
+        const long long blocks = norm_shares(np);
         if (blocks >= (1LL << 31)) {
             rc = KVEVICT_ERR_INVALID_ARG;
             return cudaSuccess;
         }
-        const size_t smem = static_cast<size_t>(p.tokens_per) * (p.R / 2) * sizeof(float2);
+        constexpr int kOwn = kNormStages * 2 * kRotThreads * 16;
+        const size_t smem = static_cast<size_t>(p.tokens_per) * (p.R / 2) * sizeof(float2) + kOwn;
         auto kern = p.interleaved ? norm_rotary_kernel<T, true> : norm_rotary_kernel<T, false>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwn + 8192 * static_cast<int>(sizeof(float2)) / 2);
+        if (e != cudaSuccess) return e;
         return launch_dependent(kern, static_cast<unsigned>(blocks), kRotThreads, smem, st, np);
     }
     const size_t smem = static_cast<size_t>(p.R / 2) * sizeof(float2) + static_cast<size_t>(kRotThreads / 32) * p.D * 4;
@@ -223,8 +355,8 @@ extern "C" int kvevict_norm_rotary(const kvevict_norm_rotary_args *a, void *cuda
     for (int i = 0; i < 2; ++i)
         if (p.heads[i] && (!np.w[i] || (reinterpret_cast<uintptr_t>(np.w[i]) & 15))) return KVEVICT_ERR_INVALID_ARG;
     const int n = a->r.dtype == KVEVICT_F32 ? 4 : 8;  // elements of a chunk
-    const uint32_t units = static_cast<uint32_t>(p.interleaved ? p.D / n : p.R / 2 / n + (p.D - p.R) / n);
-    const bool chunks = (p.interleaved ? p.R % n == 0 : p.R / 2 % n == 0) && p.D % n == 0 && units <= 32;
+    const uint32_t units = static_cast<uint32_t>(p.D / n / 2);  // pairs of chunks a head
+    const bool chunks = p.D % (2 * n) == 0 && (p.interleaved ? p.R % n == 0 : p.R / 2 % n == 0) && units <= 32;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const cudaError_t e = n == 4 ? launch_norm<float>(np, chunks, units, st, rc) : launch_norm<__nv_bfloat16>(np, chunks, units, st, rc);
     return rc != KVEVICT_OK ? rc : e == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
