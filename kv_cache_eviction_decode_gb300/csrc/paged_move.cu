@@ -24,31 +24,21 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4])
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-// Four neighbouring channels a lane: channels 32 j + 4 g + i are lane 8 j + g of a
-// head's D / 4 lanes, so that a group of 32 is eight lanes, whose minimum and
-// maximum take three shuffles, and a lane's four codes are two bytes side by side.
-// A channel's mate in the rotation is in the lane itself (interleaved) or a whole
-// number of lanes away (rotary_dim a multiple of 8); only other rotary dims read
-// it from memory. A CTA takes `tokens_per` tokens x `heads_per` of the heads of k
-// and v; its places in the pages and its cosines are found once. kBatch heads a warp
-// (D = 64: two at a time) are in flight.
-template <typename T, bool Q4, int D>
-__global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_constant__ AppendParams p)
+// The places of the tokens tok0 .. tok0 + nt - 1 and their positions, by a whole
+// block; ends with a barrier.
+struct Places {
+    int seq[kAppendTokens], page[kAppendTokens], slot[kAppendTokens], fall;
+    long long pos[kAppendTokens];
+};
+
+__device__ __forceinline__ void find_places(const AppendParams &p, int tok0, int nt, Places &s)
 {
-    constexpr int kLanes = D / 4, kAtOnce = kPagedThreads / kLanes, kBatch = 4;
-    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
-    __shared__ int s_seq[kAppendTokens], s_page[kAppendTokens], s_slot[kAppendTokens], s_fall;
-    __shared__ long long s_pos[kAppendTokens];
-    grid_dependency_wait();
     const PagedCache &c = p.c;
     const int tid = threadIdx.x;
-    const int tok0 = static_cast<int>(blockIdx.x / p.head_blocks) * p.tokens_per;
-    const int nt = min(p.tokens_per, p.tokens - tok0);
-    const int h0 = static_cast<int>(blockIdx.x % p.head_blocks) * p.heads_per, nh = min(p.heads_per, 2 * c.Hkv - h0);
     uint32_t bits = 0;
-    if (p.starts) paged_owners<kPagedThreads>(p.starts, c.batch, p.tokens, tok0, nt, s_seq, &s_fall, bits);
+    if (p.starts) paged_owners<kPagedThreads>(p.starts, c.batch, p.tokens, tok0, nt, s.seq, &s.fall, bits);
     if (tid < nt) {
-        const int t = tok0 + tid, b = p.starts ? s_seq[tid] : t / p.per;
+        const int t = tok0 + tid, b = p.starts ? s.seq[tid] : t / p.per;
         int page = -1, slot = 0;
         long long pos = 0;
         if (b >= 0) {
@@ -63,17 +53,128 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_cons
             }
             pos = !p.pos ? i : p.pos64 ? static_cast<const long long *>(p.pos)[t * p.ps] : static_cast<const int *>(p.pos)[t * p.ps];
         }
-        s_page[tid] = page;
-        s_slot[tid] = slot;
-        s_pos[tid] = pos;
+        s.page[tid] = page;
+        s.slot[tid] = slot;
+        s.pos[tid] = pos;
     }
     if (bits) atomicOr(c.err, bits);
     __syncthreads();
+}
+
+// Pages of the keys' own type, rotary parts in whole 16-byte chunks. A unit of one
+// thread is two chunks of a head (a pair rotary_dim / 2 apart, or neighbours), and a
+// thread's units, kBatch of them, are all on their way while the CTA looks up its
+// tokens' places and forms its cosines: three dependent reads, which took longer
+// than the copying.
+template <typename T, int D>
+__global__ void __launch_bounds__(kPagedThreads) append_own_kernel(const __grid_constant__ AppendParams p)
+{
+    constexpr int N = Vec<T>::N, kLanes = D / N / 2, kAtOnce = kPagedThreads / kLanes, kBatch = kAppendOwnBatch;
+    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    __shared__ Places s;
+    grid_dependency_wait();
+    const PagedCache &c = p.c;
+    const int tid = threadIdx.x, u = tid % kLanes;
+    const int tok0 = static_cast<int>(blockIdx.x / p.head_blocks) * p.tokens_per;
+    const int nt = min(p.tokens_per, p.tokens - tok0);
+    const int h0 = static_cast<int>(blockIdx.x % p.head_blocks) * p.heads_per, nh = min(p.heads_per, 2 * c.Hkv - h0);
+    const int half = p.R / 2, rows = nt * nh, pairs = p.inter ? 0 : half / N;
+    // this lane's chunks of a key; a value's are the two halves of a row
+    const int ka = p.inter ? 2 * u * N : u < pairs ? u * N : p.R + 2 * (u - pairs) * N, kb = !p.inter && u < pairs ? ka + half : ka + N;
+    bool ready = false;
+    for (int row0 = 0; row0 < rows; row0 += kAtOnce * kBatch) {
+        uint4 a[kBatch], b[kBatch];
+        int lt[kBatch], hh[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int row = row0 + i * kAtOnce + tid / kLanes;
+            lt[i] = row / nh;
+            hh[i] = row < rows ? h0 + row - lt[i] * nh : -1;
+            if (hh[i] < 0) continue;
+            const int v = hh[i] >= c.Hkv, h = v ? hh[i] - c.Hkv : hh[i];
+            const T *x = static_cast<const T *>(p.x[v]) + h * p.xs[v][0] + (tok0 + lt[i]) * p.xs[v][1];
+            a[i] = *reinterpret_cast<const uint4 *>(x + (v ? u * N : ka));
+            b[i] = *reinterpret_cast<const uint4 *>(x + (v ? u * N + D / 2 : kb));
+        }
+        if (!ready) {
+            find_places(p, tok0, nt, s);
+            if (half && h0 < c.Hkv) {
+                for (int i = tid; i < nt * half; i += kPagedThreads) {
+                    const int t = i / half;
+                    cs[i] = rot_cos_sin(p.freq[i - t * half], s.pos[t], p.scale, false);
+                }
+                __syncthreads();
+            }
+            ready = true;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (hh[i] < 0 || s.page[lt[i]] < 0) continue;
+            const int v = hh[i] >= c.Hkv, h = v ? hh[i] - c.Hkv : hh[i];
+            T *y = reinterpret_cast<T *>(c.pages[v] + s.page[lt[i]] * c.page_bytes[v] + h * c.head_bytes[v] + s.slot[lt[i]] * c.token_bytes[v]);
+            if (!v && ka < p.R) {
+                const float2 *k = cs + lt[i] * half;
+                float x[N], z[N];
+                unpack16(a[i], x);
+                unpack16(b[i], z);
+                if (p.inter) {
+#pragma unroll
+                    for (int l = 0; l < 2; ++l) {
+                        float(&w)[N] = l ? z : x;
+                        const int ch = l ? kb : ka;
+                        if (ch >= p.R) continue;
+#pragma unroll
+                        for (int j = 0; j < N; j += 2) {
+                            const float2 f = k[ch / 2 + j / 2];
+                            const float e = w[j], o = w[j + 1];
+                            w[j] = e * f.x - o * f.y;
+                            w[j + 1] = e * f.y + o * f.x;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const float2 f = k[ka + j];
+                        const float e = x[j], o = z[j];
+                        x[j] = e * f.x - o * f.y;
+                        z[j] = e * f.y + o * f.x;
+                    }
+                }
+                a[i] = pack16(x);
+                b[i] = pack16(z);
+            }
+            *reinterpret_cast<uint4 *>(y + (v ? u * N : ka)) = a[i];
+            *reinterpret_cast<uint4 *>(y + (v ? u * N + D / 2 : kb)) = b[i];
+        }
+    }
+}
+
+// Four neighbouring channels a lane: channels 32 j + 4 g + i are lane 8 j + g of a
+// head's D / 4 lanes, so that a group of 32 is eight lanes, whose minimum and
+// maximum take three shuffles, and a lane's four codes are two bytes side by side.
+// A channel's mate in the rotation is in the lane itself (interleaved) or a whole
+// number of lanes away (rotary_dim a multiple of 8); only other rotary dims read
+// it from memory. For 4 bits, and for rotary parts that no whole chunks make up. A CTA takes `tokens_per` tokens x `heads_per` of the heads of k
+// and v; its places in the pages and its cosines are found once. kBatch heads a warp
+// (D = 64: two at a time) are in flight.
+template <typename T, bool Q4, int D>
+__global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_constant__ AppendParams p)
+{
+    constexpr int kLanes = D / 4, kAtOnce = kPagedThreads / kLanes, kBatch = 4;
+    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    __shared__ Places s;
+    grid_dependency_wait();
+    const PagedCache &c = p.c;
+    const int tid = threadIdx.x;
+    const int tok0 = static_cast<int>(blockIdx.x / p.head_blocks) * p.tokens_per;
+    const int nt = min(p.tokens_per, p.tokens - tok0);
+    const int h0 = static_cast<int>(blockIdx.x % p.head_blocks) * p.heads_per, nh = min(p.heads_per, 2 * c.Hkv - h0);
+    find_places(p, tok0, nt, s);
     const int half = p.R / 2;
     if (half && h0 < c.Hkv) {
         for (int i = tid; i < nt * half; i += kPagedThreads) {
             const int lt = i / half;
-            cs[i] = rot_cos_sin(p.freq[i - lt * half], s_pos[lt], p.scale, false);
+            cs[i] = rot_cos_sin(p.freq[i - lt * half], s.pos[lt], p.scale, false);
         }
         __syncthreads();
     }
@@ -137,7 +238,7 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_cons
                     }
                 }
             }
-            const int page = real ? s_page[lt[u]] : -1, slot = real ? s_slot[lt[u]] : 0;
+            const int page = real ? s.page[lt[u]] : -1, slot = real ? s.slot[lt[u]] : 0;
             const int which = real && !key, h = which ? hh[u] - c.Hkv : hh[u];
             char *block = c.pages[which] + page * c.page_bytes[which] + h * c.head_bytes[which];
             if constexpr (Q4) {
@@ -278,6 +379,7 @@ template <int D> cudaError_t append_for(const AppendParams &p, int elem, bool q4
     const size_t smem = static_cast<size_t>(p.tokens_per) * (p.R / 2) * sizeof(float2);
     auto kern = elem == 4 ? (q4 ? append_kernel<float, true, D> : append_kernel<float, false, D>)
                           : (q4 ? append_kernel<__nv_bfloat16, true, D> : append_kernel<__nv_bfloat16, false, D>);
+    if (append_own(p, elem, q4)) kern = elem == 4 ? append_own_kernel<float, D> : append_own_kernel<__nv_bfloat16, D>;
     return launch_dependent(kern, grid, kPagedThreads, smem, st, p);
 }
 

@@ -8,6 +8,7 @@ namespace kvevict {
 
 constexpr int kPagedThreads = 256;
 constexpr int kAppendTokens = 32;  // of a CTA, at most
+constexpr int kAppendOwnBatch = 4; // units of a thread at once, own type
 constexpr int kGatherRows = 64;    // of a CTA
 
 struct AppendParams {
@@ -32,7 +33,10 @@ struct GatherParams {
     int rows, tiles;     // rows of a sequence (padded) or in all (packed); row tiles
 };
 
-// elem: bytes of dtype, 2 or 4.
+// Whether the kernel for pages of the keys' own type takes a call: the rotary part is
+// whole 16-byte chunks (pairs of them). elem: bytes of dtype, 2 or 4.
+inline bool append_own(const AppendParams &p, int elem, bool q4) { return !q4 && (p.inter ? p.R * elem % 16 == 0 : p.R / 2 * elem % 16 == 0); }
+
 cudaError_t launch_append(const AppendParams &p, int head_dim, int elem, bool q4, cudaStream_t st);
 cudaError_t launch_gather(const GatherParams &p, int head_dim, int elem, bool q4, cudaStream_t st);
 
