@@ -213,7 +213,7 @@ extern "C" int kvevict_paged_append(const kvevict_paged_append_args *a, void *cu
     // A CTA's heads: a thread's whole batch of loads (4 bits: four of them), or, where that would leave SMs idle, what
     // gives every SM two CTAs, but what its threads take at once at least.
     const bool own = append_own(p, elem, a->c.page_dtype == KVEVICT_Q4);
-    const int64_t heads = 2 * a->c.n_kv_heads, once = own ? 2 * kPagedThreads * 16 / (a->c.head_dim * elem) : 4 * kPagedThreads / a->c.head_dim;
+    const int64_t heads = 2 * a->c.n_kv_heads, once = own ? 2 * kPagedThreads * 16 / (a->c.head_dim * elem) : 8 * kPagedThreads / a->c.head_dim;
     const int64_t want = std::min((own ? kAppendOwnBatch : 16) * once, std::max(once, a->tokens * heads / (2 * kSMs)));
     p.heads_per = static_cast<int>(std::min(heads, want));
     p.head_blocks = static_cast<int>((heads + p.heads_per - 1) / p.heads_per);

@@ -3,7 +3,7 @@
 //
 // y = x w r, r = 1 / sqrt(mean x^2 + eps), then every pair of y turns. A head is read
 // once and written once; beside these bytes the instructions count (121 us for 16384
-// tokens of 64 + 8 heads of 128 with an address worked out for each head, 110 now,
+// tokens of 64 + 8 heads of 128 with an address worked out for each head, 108 now,
 // 103 for the rotation alone in rotary.cu). So a head's lanes, a
 // power of two of neighbours in a warp, take two 16-byte chunks each (a pair
 // rotary_dim / 2 apart, or two of neighbouring pairs or of elements that do not
@@ -36,54 +36,9 @@ __device__ __forceinline__ void copy16(uint4 *dst, const void *src)
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A thread's way through the (token, head) rows of a CTA, `step` rows at a time: a
-// pointer that follows the strides.
-struct Walk {
-    char *p;
-    int h, t, ts;  // head, token of the CTA, token of its sequence
-    int nh, tokens, heads_on, tokens_on;           // a step: so many heads and whole tokens on
-    long long by_step, by_token, by_seq;           // bytes: a step; from behind the last head to the next token; over a sequence's end
-
-    __device__ __forceinline__ void start(char *base, const long long (&s)[3], int elem, long long b, int token, int heads, int step, int first, int per)
-    {
-        nh = heads;
-        tokens = per;
-        heads_on = step % nh;
-        tokens_on = step / nh;
-        by_token = (s[2] - nh * s[1]) * elem;
-        by_step = (heads_on * s[1] + tokens_on * s[2]) * elem;
-        by_seq = (s[0] - tokens * s[2]) * elem;
-        h = first % nh;
-        t = first / nh;
-        ts = token + t;
-        p = base + (b * s[0] + ts * s[2] + h * s[1]) * elem;
-        ends();
-    }
-    __device__ __forceinline__ void ends()
-    {
-        if (ts >= tokens) {
-            const int n = ts / tokens;
-            ts -= n * tokens;
-            p += n * by_seq;
-        }
-    }
-    __device__ __forceinline__ void on()
-    {
-        int dt = tokens_on;
-        h += heads_on;
-        p += by_step;
-        if (h >= nh) {
-            h -= nh;
-            p += by_token;
-            ++dt;
-        }
-        t += dt;
-        ts += dt;
-        ends();
-    }
-};
-
 constexpr int kNormStages = 4;
+constexpr int kNormPairs = 256;  // of a head of 64 chunks at most
+
 
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, 4) norm_rotary_kernel(const __grid_constant__ NormParams np)
@@ -93,6 +48,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) norm_rotary_kernel(const __gri
     extern __shared__ __align__(16) char sh[];
     uint4 *const own = reinterpret_cast<uint4 *>(sh) + threadIdx.x;                                     // [stages][2][threads]
     float4 *const cs = reinterpret_cast<float4 *>(sh + kNormStages * 2 * kRotThreads * 16);  // [tokens_per][lines][R / N, or half of it]
+    __shared__ long long turns[kNormPairs];
     grid_dependency_wait();
     const int half = p.R / 2, chunks = p.D / N, turning = INTER ? p.R / N : half / N;  // (half layout: pairs of chunks)
     const int tok0 = blockIdx.x / p.head_blocks * p.tokens_per;
@@ -136,13 +92,15 @@ __global__ void __launch_bounds__(kRotThreads, 4) norm_rotary_kernel(const __gri
         unpack16(*reinterpret_cast<const uint4 *>(static_cast<const T *>(np.w[w]) + ca), wa);
         unpack16(*reinterpret_cast<const uint4 *>(static_cast<const T *>(np.w[w]) + cb), wb);
         if (!ready) {
+            for (int i = threadIdx.x; i < half; i += kRotThreads) turns[i] = rot_turns(p.freq[i]);
+            __syncthreads();
             // pair f: (INTER) chunk 2 f / N, else pair of chunks f / N; lines of two pairs lie beside those of the other chunks
             for (int i = threadIdx.x; i < nt * half; i += kRotThreads) {
                 const int lt = i / half, f = i - lt * half, in_chunk = INTER ? N / 2 : N;
                 const int q = f / in_chunk, e = f - q * in_chunk;
                 const int bt = tok0 + lt, b = bt / tokens;
                 reinterpret_cast<float2 *>(cs)[((lt * kLines + e / 2) * turning + q) * 2 + (e & 1)] =
-                    rot_cos_sin(p.freq[f], rot_position(p, b, bt - static_cast<long long>(b) * tokens), p.scale, false);
+                    rot_cos_sin(turns[f], rot_position(p, b, bt - static_cast<long long>(b) * tokens), p.scale);
             }
             __syncthreads();
             ready = true;
@@ -279,7 +237,7 @@ __global__ void __launch_bounds__(kRotThreads) norm_rotary_any_kernel(const __gr
 // A CTA's share of tokens (all heads), or of one token's heads where there are few
 // tokens: what lets whole waves of four CTAs an SM end soonest, a CTA taking what
 // its rows take and as much as kStart times its 256 threads' rows to find its way
-// and its cosines. (16384 tokens, 64 + 8 heads of 128: 110 us, 81% of the copy
+// and its cosines. (16384 tokens, 64 + 8 heads of 128: 108 us, 82% of the copy
 // bandwidth, 111 with 4 tokens a CTA; 3 x 2049 tokens, 12 + 4 heads, 48 of 128 in
 // fp32: 26 us, 30 with ten tokens a CTA.)
 constexpr int kStart = 5;

@@ -86,12 +86,13 @@ __device__ __forceinline__ void paged_owners(const int32_t *starts, int batch, i
 }
 
 // ------------------------------------------------------------- 4-bit groups
-// A group's base and step for values between lo and hi, and the code of a value.
-// In fp32, each operation rounded by itself.
+// A group's base and step for values between lo and hi, and the code of a value:
+// round((x - base) / step) + 8, by the step's reciprocal (what that is off by, 2^-23
+// of the quotient, moves a code only where the value is that near to the border).
 __device__ __forceinline__ void q4_group(float lo, float hi, bool finite, uint32_t &base_step, float &base, float &step)
 {
-    base = __bfloat162float(__float2bfloat16_rn(__fadd_rn(__fmul_rn(hi, 8.f / 15.f), __fmul_rn(lo, 7.f / 15.f))));
-    step = fmaxf(__fdiv_rn(__fsub_rn(hi, base), 7.f), __fmul_rn(__fsub_rn(base, lo), 0.125f));
+    base = __bfloat162float(__float2bfloat16_rn(fmaf(hi, 8.f / 15.f, lo * (7.f / 15.f))));
+    step = fmaxf((hi - base) * (1.f / 7.f), (base - lo) * 0.125f);
     step = __uint_as_float((__float_as_uint(step) + 0xFFFFu) & 0xFFFF0000u);  // (>= 0: up)
     if (!finite) {
         base = __uint_as_float(0x7FC00000u);
@@ -100,11 +101,20 @@ __device__ __forceinline__ void q4_group(float lo, float hi, bool finite, uint32
     base_step = (__float_as_uint(base) >> 16) | (__float_as_uint(step) & 0xFFFF0000u);
 }
 
-__device__ __forceinline__ uint32_t q4_code(float x, float base, float step)
+// 1 / step, 0 for none. (Of steps below 2^-126, 2^126: their codes end at 0 or 15.)
+__device__ __forceinline__ float q4_inverse(float step) { return step > 0.f ? fminf(__fdividef(1.f, step), 8.507059173e37f) : 0.f; }
+
+// A code in the low bits of 2^23 + 2^22 + code, where fp32's step is 1: the sum rounds.
+__device__ __forceinline__ uint32_t q4_code(float x, float base, float inverse)
 {
-    if (!(step > 0.f)) return 8u;
-    const float c = rintf(__fdiv_rn(__fsub_rn(x, base), step)) + 8.f;
-    return static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
+    const float least = 12582912.f;
+    return __float_as_uint(fminf(fmaxf(fmaf(x - base, inverse, least + 8.f), least), least + 15.f));
+}
+// Four of them side by side, in the low 16 bits.
+__device__ __forceinline__ uint16_t q4_codes(const float *v, float base, float inverse)
+{
+    return static_cast<uint16_t>(q4_code(v[0], base, inverse) + q4_code(v[1], base, inverse) * 16u + q4_code(v[2], base, inverse) * 256u +
+                                 q4_code(v[3], base, inverse) * 4096u);
 }
 
 __device__ __forceinline__ float q4_base(uint32_t base_step) { return __uint_as_float(base_step << 16); }

@@ -27,6 +27,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4])
 // The places of the tokens tok0 .. tok0 + nt - 1 and their positions, by a whole
 // block; ends with a barrier.
 struct Places {
+    long long turns[64];  // of a pair, see rot_turns
     int seq[kAppendTokens], page[kAppendTokens], slot[kAppendTokens], fall;
     long long pos[kAppendTokens];
 };
@@ -36,6 +37,7 @@ __device__ __forceinline__ void find_places(const AppendParams &p, int tok0, int
     const PagedCache &c = p.c;
     const int tid = threadIdx.x;
     uint32_t bits = 0;
+    if (tid >= kPagedThreads - p.R / 2) s.turns[kPagedThreads - 1 - tid] = rot_turns(p.freq[kPagedThreads - 1 - tid]);
     if (p.starts) paged_owners<kPagedThreads>(p.starts, c.batch, p.tokens, tok0, nt, s.seq, &s.fall, bits);
     if (tid < nt) {
         const int t = tok0 + tid, b = p.starts ? s.seq[tid] : t / p.per;
@@ -58,6 +60,18 @@ __device__ __forceinline__ void find_places(const AppendParams &p, int tok0, int
         s.pos[tid] = pos;
     }
     if (bits) atomicOr(c.err, bits);
+    __syncthreads();
+}
+
+// [tokens][R / 2] cosines and sines of the tokens' positions, by a whole block; ends
+// with a barrier (and begins with one behind find_places).
+__device__ __forceinline__ void form_cosines(const AppendParams &p, int nt, Places &s, float2 *cs)
+{
+    const int half = p.R / 2;
+    for (int i = threadIdx.x; i < nt * half; i += kPagedThreads) {
+        const int t = i / half;
+        cs[i] = rot_cos_sin(s.turns[i - t * half], s.pos[t], p.scale);
+    }
     __syncthreads();
 }
 
@@ -98,13 +112,7 @@ __global__ void __launch_bounds__(kPagedThreads) append_own_kernel(const __grid_
         }
         if (!ready) {
             find_places(p, tok0, nt, s);
-            if (half && h0 < c.Hkv) {
-                for (int i = tid; i < nt * half; i += kPagedThreads) {
-                    const int t = i / half;
-                    cs[i] = rot_cos_sin(p.freq[i - t * half], s.pos[t], p.scale, false);
-                }
-                __syncthreads();
-            }
+            if (half && h0 < c.Hkv) form_cosines(p, nt, s, cs);
             ready = true;
         }
 #pragma unroll
@@ -149,14 +157,165 @@ __global__ void __launch_bounds__(kPagedThreads) append_own_kernel(const __grid_
     }
 }
 
-// Four neighbouring channels a lane: channels 32 j + 4 g + i are lane 8 j + g of a
-// head's D / 4 lanes, so that a group of 32 is eight lanes, whose minimum and
-// maximum take three shuffles, and a lane's four codes are two bytes side by side.
-// A channel's mate in the rotation is in the lane itself (interleaved) or a whole
-// number of lanes away (rotary_dim a multiple of 8); only other rotary dims read
-// it from memory. For 4 bits, and for rotary parts that no whole chunks make up. A CTA takes `tokens_per` tokens x `heads_per` of the heads of k
-// and v; its places in the pages and its cosines are found once. kBatch heads a warp
-// (D = 64: two at a time) are in flight.
+// Eight neighbouring elements as they are in memory.
+template <typename T> struct Eight {
+    static constexpr int kWords = 2 * sizeof(T);
+    uint32_t w[kWords];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const char *p)
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 2) bf16x2_to_f32(w[i], v[2 * i], v[2 * i + 1]);
+            else v[i] = __uint_as_float(w[i]);
+        }
+    }
+    // Another lane's.
+    __device__ __forceinline__ void from(int lane, float (&v)[8]) const
+    {
+        Eight o;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) o.w[i] = __shfl_sync(0xffffffffu, w[i], lane);
+        o.get(v);
+    }
+};
+
+// 4 bits. Eight neighbouring channels a lane: 32 j + 8 t .. of lane 4 j + t, so that a
+// group of 32 is four lanes, whose minimum and maximum take two shuffles each, and
+// goes out as two bytes for each of two neighbouring g. A channel's mate in the
+// rotation is in the lane itself (interleaved) or a whole number of lanes away.
+// Instructions bound it, not bytes, so that rows are walked by strides, keys first
+// and then values, which need no rotation; kBatch rows of a thread are on their way
+// at once, the first ones while the CTA looks up its tokens' places. (15,505 tokens
+// of 8 heads of 128: 38 us, with four channels a lane 52.)
+template <typename T, int D>
+__global__ void __launch_bounds__(kPagedThreads) append_q4_kernel(const __grid_constant__ AppendParams p)
+{
+    constexpr int kLanes = D / 8, kAtOnce = kPagedThreads / kLanes, kBatch = 4;
+    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    __shared__ Places s;
+    __shared__ char *s_codes[2][kAppendTokens], *s_groups[2][kAppendTokens];
+    grid_dependency_wait();
+    const PagedCache &c = p.c;
+    const int tid = threadIdx.x, lane = tid % kLanes, ch = lane * 8;
+    const int tok0 = static_cast<int>(blockIdx.x / p.head_blocks) * p.tokens_per;
+    const int nt = min(p.tokens_per, p.tokens - tok0);
+    const int h0 = static_cast<int>(blockIdx.x % p.head_blocks) * p.heads_per, nh_all = min(p.heads_per, 2 * c.Hkv - h0);
+    const int half = p.R / 2;
+    const bool turns = ch < p.R, first = ch < half;
+    const int mate = (tid & 31) + (p.inter || !turns ? 0 : first ? half / 8 : -(half / 8)), ang = p.inter ? ch / 2 : first ? ch : ch - half;
+    const int byte = (D / 16) * 2 * (lane & 3) + 2 * (lane >> 2);
+    bool ready = false;
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+        const int ha = w ? max(h0 - c.Hkv, 0) : h0, hz = w ? h0 + nh_all - c.Hkv : min(h0 + nh_all, c.Hkv), nh = hz - ha;
+        if (nh <= 0) continue;
+        const long long strides[3] = {0, p.xs[w][0], p.xs[w][1]};
+        Walk in;
+        const T *x0 = static_cast<const T *>(p.x[w]) + ha * p.xs[w][0] + ch;
+        in.start(const_cast<char *>(reinterpret_cast<const char *>(x0)), strides, sizeof(T), 0, tok0, nh, kAtOnce, tid / kLanes, INT_MAX);
+        const long long head_bytes = c.head_bytes[w];
+        const int trips = (nt * nh + kAtOnce - 1) / kAtOnce;
+#pragma unroll 1
+        for (int trip = 0; trip < trips; trip += kBatch) {
+            Eight<T> x[kBatch];
+            int tk[kBatch], hd[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                x[u].zero();
+                tk[u] = in.t;
+                hd[u] = in.h;
+                if (in.t < nt) x[u].load(in.p);
+                in.on();
+            }
+            if (!ready) {
+                find_places(p, tok0, nt, s);
+                for (int i = tid; i < 2 * nt; i += kPagedThreads) {
+                    const int v = i / nt, t = i - v * nt;
+                    char *block = s.page[t] < 0 ? nullptr : c.pages[v] + s.page[t] * c.page_bytes[v];
+                    s_codes[v][t] = block ? block + s.slot[t] * (D / 2) : nullptr;
+                    s_groups[v][t] = block ? block + c.S * (D / 2) + s.slot[t] * (D / 8) : nullptr;
+                }
+                if (half && h0 < c.Hkv) form_cosines(p, nt, s, cs);
+                else __syncthreads();
+                ready = true;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (trip + u >= trips) break;
+                float v[8];
+                x[u].get(v);
+                const int t = min(tk[u], nt - 1);
+                if (!w && half) {  // (the same for every thread)
+                    if (p.inter) {
+                        if (turns) {
+#pragma unroll
+                            for (int i = 0; i < 8; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(cs + t * half + ang + i / 2);
+                                const float a0 = v[i], b0 = v[i + 1], a1 = v[i + 2], b1 = v[i + 3];
+                                v[i] = a0 * f.x - b0 * f.y;
+                                v[i + 1] = a0 * f.y + b0 * f.x;
+                                v[i + 2] = a1 * f.z - b1 * f.w;
+                                v[i + 3] = a1 * f.w + b1 * f.z;
+                            }
+                        }
+                    } else {
+                        float o[8];
+                        x[u].from(mate, o);
+                        if (turns) {
+                            const float sg = first ? -1.f : 1.f;
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const float4 f = *reinterpret_cast<const float4 *>(cs + t * half + ang + i);
+                                v[i] = v[i] * f.x + sg * o[i] * f.y;
+                                v[i + 1] = v[i + 1] * f.z + sg * o[i + 1] * f.w;
+                            }
+                        }
+                    }
+                }
+                float lo = v[0], hi = v[0], none = v[0] * 0.f;  // (none: NaN where one is not finite)
+#pragma unroll
+                for (int i = 1; i < 8; ++i) {
+                    lo = fminf(lo, v[i]);
+                    hi = fmaxf(hi, v[i]);
+                    none = fmaf(v[i], 0.f, none);
+                }
+#pragma unroll
+                for (int o = 2; o; o >>= 1) {
+                    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+                    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+                }
+                const uint32_t fine = __ballot_sync(0xffffffffu, none == 0.f) >> (tid & 28) & 0xfu;
+                uint32_t params;
+                float base, step;
+                q4_group(lo, hi, fine == 0xfu, params, base, step);
+                char *const to = s_codes[w][t];
+                if (tk[u] < nt && to) {
+                    const long long head = (ha + hd[u]) * head_bytes;
+                    const float inverse = q4_inverse(step);
+                    *reinterpret_cast<uint16_t *>(to + head + byte) = q4_codes(v, base, inverse);
+                    *reinterpret_cast<uint16_t *>(to + head + byte + D / 16) = q4_codes(v + 4, base, inverse);
+                    if ((lane & 3) == 0) *reinterpret_cast<uint32_t *>(s_groups[w][t] + head + 4 * (lane >> 2)) = params;
+                }
+            }
+        }
+    }
+}
+
+// Rotary parts that the two kernels above do not take, own type and 4 bits, with the
+// latter's layout; a channel's mate in the rotation is read from memory.
 template <typename T, bool Q4, int D>
 __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_constant__ AppendParams p)
 {
@@ -169,21 +328,11 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_cons
     const int tok0 = static_cast<int>(blockIdx.x / p.head_blocks) * p.tokens_per;
     const int nt = min(p.tokens_per, p.tokens - tok0);
     const int h0 = static_cast<int>(blockIdx.x % p.head_blocks) * p.heads_per, nh = min(p.heads_per, 2 * c.Hkv - h0);
-    find_places(p, tok0, nt, s);
     const int half = p.R / 2;
-    if (half && h0 < c.Hkv) {
-        for (int i = tid; i < nt * half; i += kPagedThreads) {
-            const int lt = i / half;
-            cs[i] = rot_cos_sin(p.freq[i - lt * half], s.pos[lt], p.scale, false);
-        }
-        __syncthreads();
-    }
+    bool ready = false;
 
     const int lane = tid % kLanes, ch = lane * 4;
-    // where a lane's mates are: in itself, `far` lanes off, or (found one by one) anywhere
-    const bool by_lane = !p.inter && half % 4 == 0, turns = ch < p.R;
-    const bool first = ch < half;
-    const int far = first ? half / 4 : -(half / 4);
+    const bool turns = ch < p.R;
     const int rows = nt * nh;
     for (int row0 = 0; row0 < rows; row0 += kAtOnce * kBatch) {
         float4 x[kBatch];
@@ -201,20 +350,16 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_cons
             const int v = hh[u] >= c.Hkv, h = v ? hh[u] - c.Hkv : hh[u];
             x[u] = load4(static_cast<const T *>(p.x[v]) + h * p.xs[v][0] + (tok0 + lt[u]) * p.xs[v][1] + ch);
         }
+        if (!ready) {  // (the first loads are under way)
+            find_places(p, tok0, nt, s);
+            if (half && h0 < c.Hkv) form_cosines(p, nt, s, cs);
+            ready = true;
+        }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const bool real = hh[u] >= 0, key = real && hh[u] < c.Hkv;
             float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            if (by_lane && half) {  // (the same for every thread)
-                const int mate = (tid & 31) + (turns ? far : 0);
-                const float o[4] = {__shfl_sync(0xffffffffu, v[0], mate), __shfl_sync(0xffffffffu, v[1], mate),
-                                    __shfl_sync(0xffffffffu, v[2], mate), __shfl_sync(0xffffffffu, v[3], mate)};
-                if (key && turns) {
-                    const float2 *k = cs + lt[u] * half + (first ? ch : ch - half);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = first ? v[i] * k[i].x - o[i] * k[i].y : o[i] * k[i].y + v[i] * k[i].x;
-                }
-            } else if (key && turns) {
+            if (key && turns) {
                 const float2 *k = cs + lt[u] * half;
                 if (p.inter) {
 #pragma unroll
@@ -253,13 +398,11 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_cons
                 }
                 const uint32_t all = __ballot_sync(0xffffffffu, fine) >> (tid & 24) & 0xffu;
                 if (page < 0) continue;
-                uint32_t params, codes = 0;
+                uint32_t params;
                 float base, step;
                 q4_group(lo, hi, all == 0xffu, params, base, step);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) codes |= q4_code(v[i], base, step) << (4 * i);
                 const int g = lane & 7, j = lane >> 3;
-                *reinterpret_cast<uint16_t *>(block + slot * (D / 2) + (D / 16) * g + 2 * j) = static_cast<uint16_t>(codes);
+                *reinterpret_cast<uint16_t *>(block + slot * (D / 2) + (D / 16) * g + 2 * j) = q4_codes(v, base, q4_inverse(step));
                 if (g == 0) *reinterpret_cast<uint32_t *>(block + c.S * (D / 2) + slot * (D / 8) + 4 * j) = params;
             } else {
                 if (page < 0) continue;
@@ -379,6 +522,7 @@ template <int D> cudaError_t append_for(const AppendParams &p, int elem, bool q4
     const size_t smem = static_cast<size_t>(p.tokens_per) * (p.R / 2) * sizeof(float2);
     auto kern = elem == 4 ? (q4 ? append_kernel<float, true, D> : append_kernel<float, false, D>)
                           : (q4 ? append_kernel<__nv_bfloat16, true, D> : append_kernel<__nv_bfloat16, false, D>);
+    if (append_q4(p, q4)) kern = elem == 4 ? append_q4_kernel<float, D> : append_q4_kernel<__nv_bfloat16, D>;
     if (append_own(p, elem, q4)) kern = elem == 4 ? append_own_kernel<float, D> : append_own_kernel<__nv_bfloat16, D>;
     return launch_dependent(kern, grid, kPagedThreads, smem, st, p);
 }

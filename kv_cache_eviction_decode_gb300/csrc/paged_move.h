@@ -33,10 +33,11 @@ struct GatherParams {
     int rows, tiles;     // rows of a sequence (padded) or in all (packed); row tiles
 };
 
-// Whether the kernel for pages of the keys' own type takes a call: the rotary part is
-// whole 16-byte chunks (pairs of them). elem: bytes of dtype, 2 or 4.
+// Which kernel takes a call. Pages of the keys' own type: the rotary part is whole
+// 16-byte chunks (pairs of them). 4 bits: whole eights of
+// channels turn (pairs of them). (All else: the general one.) elem: bytes of dtype, 2 or 4.
 inline bool append_own(const AppendParams &p, int elem, bool q4) { return !q4 && (p.inter ? p.R * elem % 16 == 0 : p.R / 2 * elem % 16 == 0); }
-
+inline bool append_q4(const AppendParams &p, bool q4) { return q4 && (p.inter ? p.R % 8 == 0 : p.R / 2 % 8 == 0); }
 cudaError_t launch_append(const AppendParams &p, int head_dim, int elem, bool q4, cudaStream_t st);
 cudaError_t launch_gather(const GatherParams &p, int head_dim, int elem, bool q4, cudaStream_t st);
 

@@ -63,6 +63,22 @@ __device__ __forceinline__ float2 rot_cos_sin(double freq, long long pos, float 
     return make_float2(c * scale, inverse ? -s * scale : s * scale);
 }
 
+// The same in two parts: a frequency's turns a position as a fraction, once for many
+// tokens (fp64 instructions are scarce: 16 cycles of an SM for a warp's), and a
+// position's cosine and sine from it.
+__device__ __forceinline__ long long rot_turns(double freq)
+{
+    const double turns = freq * 0.15915494309189535;
+    return __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
+}
+__device__ __forceinline__ float2 rot_cos_sin(long long turns, long long pos, float scale)
+{
+    const long long frac = static_cast<long long>(static_cast<unsigned long long>(pos) * static_cast<unsigned long long>(turns));
+    float s, c;
+    sincospif(static_cast<float>(frac) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
+    return make_float2(c * scale, s * scale);
+}
+
 // Position of token t of sequence b.
 __device__ __forceinline__ long long rot_position(const RotParams &p, long long b, long long t)
 {
@@ -71,6 +87,53 @@ __device__ __forceinline__ long long rot_position(const RotParams &p, long long 
                   : (p.pos64 ? static_cast<const long long *>(p.pos)[at]
                              : static_cast<long long>(static_cast<const int *>(p.pos)[at]));
 }
+
+// A thread's way through the (token, head) rows of a CTA, `step` rows at a time: a
+// pointer that follows the strides.
+struct Walk {
+    char *p;
+    int h, t, ts;  // head, token of the CTA, token of its sequence
+    int nh, tokens, heads_on, tokens_on;           // a step: so many heads and whole tokens on
+    long long by_step, by_token, by_seq;           // bytes: a step; from behind the last head to the next token; over a sequence's end
+
+    __device__ __forceinline__ void start(char *base, const long long (&s)[3], int elem, long long b, int token, int heads, int step, int first, int per)
+    {
+        nh = heads;
+        tokens = per;
+        heads_on = step % nh;
+        tokens_on = step / nh;
+        by_token = (s[2] - nh * s[1]) * elem;
+        by_step = (heads_on * s[1] + tokens_on * s[2]) * elem;
+        by_seq = static_cast<long long>(static_cast<unsigned long long>(s[0]) - static_cast<unsigned long long>(tokens) * s[2]) * elem;
+        h = first % nh;
+        t = first / nh;
+        ts = token + t;
+        p = base + (b * s[0] + ts * s[2] + h * s[1]) * elem;
+        ends();
+    }
+    __device__ __forceinline__ void ends()
+    {
+        if (ts >= tokens) {
+            const int n = ts / tokens;
+            ts -= n * tokens;
+            p += n * by_seq;
+        }
+    }
+    __device__ __forceinline__ void on()
+    {
+        int dt = tokens_on;
+        h += heads_on;
+        p += by_step;
+        if (h >= nh) {
+            h -= nh;
+            p += by_token;
+            ++dt;
+        }
+        t += dt;
+        ts += dt;
+        ends();
+    }
+};
 
 constexpr int kRotThreads = 256;
 
