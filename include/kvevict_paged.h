@@ -27,7 +27,7 @@ extern "C" {
  * (a group with an infinity or NaN in it stands for NaN).
  *   base = bf16(8/15 hi + 7/15 lo), hi and lo the group's largest and smallest;
  *   step = max((hi - base) / 7, (base - lo) / 8), rounded up to bf16;
- *   code = round((x - base) / step) + 8, in 0 .. 15 (8 where step is 0).
+ *   code = round((x - base) / step) + 8, ties to even, in 0 .. 15 (8 where step is 0).
  * A page's block for one head, [page_size * 5 head_dim / 8] bytes, contiguous:
  * first the codes [page_size][head_dim / 2], then [page_size][head_dim / 32]
  * groups of (base, step). Channel 32 j + 4 g + i of a row (j the group, g 0 .. 7,

@@ -86,13 +86,21 @@ __device__ __forceinline__ void paged_owners(const int32_t *starts, int batch, i
 }
 
 // ------------------------------------------------------------- 4-bit groups
-// A group's base and step for values between lo and hi, and the code of a value:
-// round((x - base) / step) + 8, by the step's reciprocal (what that is off by, 2^-23
-// of the quotient, moves a code only where the value is that near to the border).
+// d / by from the reciprocal, put right once: exact wherever the quotient is an fp32
+// value. Channels of bf16 keys and steps in bf16 make codes that lie just between two
+// (k + 1/2) and steps that need no rounding common, so that those have to be.
+__device__ __forceinline__ float q4_divide(float d, float by, float inverse)
+{
+    const float q = d * inverse;
+    return fmaf(fmaf(-q, by, d), inverse, q);
+}
+
+// A group's base and step for values between lo and hi.
 __device__ __forceinline__ void q4_group(float lo, float hi, bool finite, uint32_t &base_step, float &base, float &step)
 {
-    base = __bfloat162float(__float2bfloat16_rn(fmaf(hi, 8.f / 15.f, lo * (7.f / 15.f))));
-    step = fmaxf((hi - base) * (1.f / 7.f), (base - lo) * 0.125f);
+    // (8 hi + 7 lo) / 15, by sixteenths so that it cannot overflow
+    base = __bfloat162float(__float2bfloat16_rn(q4_divide(fmaf(hi, 0.5f, lo * 0.4375f), 0.9375f, 1.f / 0.9375f)));
+    step = fmaxf(q4_divide(hi - base, 7.f, 1.f / 7.f), (base - lo) * 0.125f);
     step = __uint_as_float((__float_as_uint(step) + 0xFFFFu) & 0xFFFF0000u);  // (>= 0: up)
     if (!finite) {
         base = __uint_as_float(0x7FC00000u);
@@ -104,17 +112,18 @@ __device__ __forceinline__ void q4_group(float lo, float hi, bool finite, uint32
 // 1 / step, 0 for none. (Of steps below 2^-126, 2^126: their codes end at 0 or 15.)
 __device__ __forceinline__ float q4_inverse(float step) { return step > 0.f ? fminf(__fdividef(1.f, step), 8.507059173e37f) : 0.f; }
 
-// A code in the low bits of 2^23 + 2^22 + code, where fp32's step is 1: the sum rounds.
-__device__ __forceinline__ uint32_t q4_code(float x, float base, float inverse)
+// A code in the low bits of 2^23 + 2^22 + code, where fp32's step is 1: the sum rounds
+// (k + 1/2 to the even code).
+__device__ __forceinline__ uint32_t q4_code(float x, float base, float step, float inverse)
 {
     const float least = 12582912.f;
-    return __float_as_uint(fminf(fmaxf(fmaf(x - base, inverse, least + 8.f), least), least + 15.f));
+    return __float_as_uint(fminf(fmaxf(q4_divide(x - base, step, inverse) + (least + 8.f), least), least + 15.f));
 }
 // Four of them side by side, in the low 16 bits.
-__device__ __forceinline__ uint16_t q4_codes(const float *v, float base, float inverse)
+__device__ __forceinline__ uint16_t q4_codes(const float *v, float base, float step, float inverse)
 {
-    return static_cast<uint16_t>(q4_code(v[0], base, inverse) + q4_code(v[1], base, inverse) * 16u + q4_code(v[2], base, inverse) * 256u +
-                                 q4_code(v[3], base, inverse) * 4096u);
+    return static_cast<uint16_t>(q4_code(v[0], base, step, inverse) + q4_code(v[1], base, step, inverse) * 16u +
+                                 q4_code(v[2], base, step, inverse) * 256u + q4_code(v[3], base, step, inverse) * 4096u);
 }
 
 __device__ __forceinline__ float q4_base(uint32_t base_step) { return __uint_as_float(base_step << 16); }

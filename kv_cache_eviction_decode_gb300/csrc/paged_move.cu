@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(kPagedThreads) append_q4_kernel(const __grid_c
                 if (tk[u] < nt && to) {
                     const long long head = (ha + hd[u]) * head_bytes;
                     const float inverse = q4_inverse(step);
-                    *reinterpret_cast<uint16_t *>(to + head + byte) = q4_codes(v, base, inverse);
-                    *reinterpret_cast<uint16_t *>(to + head + byte + D / 16) = q4_codes(v + 4, base, inverse);
+                    *reinterpret_cast<uint16_t *>(to + head + byte) = q4_codes(v, base, step, inverse);
+                    *reinterpret_cast<uint16_t *>(to + head + byte + D / 16) = q4_codes(v + 4, base, step, inverse);
                     if ((lane & 3) == 0) *reinterpret_cast<uint32_t *>(s_groups[w][t] + head + 4 * (lane >> 2)) = params;
                 }
             }
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_cons
                 float base, step;
                 q4_group(lo, hi, all == 0xffu, params, base, step);
                 const int g = lane & 7, j = lane >> 3;
-                *reinterpret_cast<uint16_t *>(block + slot * (D / 2) + (D / 16) * g + 2 * j) = q4_codes(v, base, q4_inverse(step));
+                *reinterpret_cast<uint16_t *>(block + slot * (D / 2) + (D / 16) * g + 2 * j) = q4_codes(v, base, step, q4_inverse(step));
                 if (g == 0) *reinterpret_cast<uint32_t *>(block + c.S * (D / 2) + slot * (D / 8) + 4 * j) = params;
             } else {
                 if (page < 0) continue;

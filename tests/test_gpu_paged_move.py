@@ -107,6 +107,39 @@ def test_append_what_four_bits_cannot_hold(cuda_device):
         assert ((got[5, 0] - 1).abs() <= 2.0 ** -12 * (1 + 2.0 ** -7)).all() and ((got[6, 0] - k[6, 0].double()).abs() <= 1e-31).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_rounds_ties_to_even(cuda_device, d):
+    """bf16 channels over steps in bf16 often lie just between two codes, and steps often need no rounding. Every code that
+    64 bits put at k + 1/2 is the even one, all others the nearest but within 2^-18 of a border; the step is the least that
+    bf16 has, wherever 64 bits are not within 2^-18 of the one below it; and the base is the nearest (8 hi + 7 lo is exact in
+    fp32 here, and its fifteenth put right once)."""
+    T, H = 512, 4
+    pool = Pool([T], H, 16, d, torch.bfloat16, True, garbage=False)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn(T, H, d, device="cuda", generator=g)
+    x = torch.stack([x, torch.round(x * 8) / 8])[torch.arange(T, device="cuda") % 2, torch.arange(T, device="cuda")].bfloat16()  # half of them on a grid
+    kv.paged_append(x, x, pool.k, pool.v, pool.table, pool.kv_lens)
+    ties = 0
+    for pages in (pool.k, pool.v):
+        codes, params = parts(pages, d)
+        page, slot = pool.table[0, torch.arange(T, device="cuda") // 16].long(), torch.arange(T, device="cuda") % 16
+        c = unpack(codes[page, :, slot]).double().unflatten(-1, (-1, 32))
+        base, step = (params[page, :, slot][..., i].double()[..., None] for i in (0, 1))
+        z = x.double().unflatten(-1, (-1, 32))
+        q = (z - base) / step
+        near = torch.round(q).clamp(-8, 7)
+        tie = (q - q.floor() == 0.5) & (q > -8) & (q < 7)
+        ties += int(tie.sum())
+        assert torch.equal(c[tie] - 8, near[tie])
+        assert ((c - 8 == near) | ((q - q.floor() - 0.5).abs() < 2.0 ** -18)).all()
+        exact = ((8 * z.amax(-1, keepdim=True) + 7 * z.amin(-1, keepdim=True)) / 15).bfloat16().double()
+        assert torch.equal(base, exact)
+        need = torch.maximum((z.amax(-1, keepdim=True) - base) / 7, (base - z.amin(-1, keepdim=True)) / 8)
+        below = (params[page, :, slot][..., 1].contiguous().view(torch.int16) - 1).view(torch.bfloat16).double()[..., None]
+        assert (below < need * (1 + 2.0 ** -18)).all() and (step >= need * (1 - 2.0 ** -18)).all()
+    assert ties > 1000
+
+
 @pytest.mark.parametrize("dtype,four", KINDS)
 @pytest.mark.parametrize("d,S,H", [(128, 16, 8), (64, 32, 3), (128, 256, 1)])
 @pytest.mark.parametrize("lens", [[1], [0, 17, 64, 200, 1], [129, 0, 0, 65]])
