@@ -85,7 +85,7 @@ typedef struct {
  *              none of them is looked at.
  * Tokens before the first place or behind the table (BAD_LENGTH) and in no page
  * (BAD_PAGE) are dropped, and so is every sequence of starts that go back from the
- * first such on. Two tokens that the tables put in one place, or a call that reads
+ * first such on. k and v must not overlap the pages. Two tokens that the tables put in one place, or a call that reads
  * the pages at the same time, give undefined contents there. Other rows of the
  * pages are left as they were.
  */
@@ -131,7 +131,11 @@ int kvevict_paged_gather(const kvevict_paged_gather_args *a, void *cuda_stream);
  * the query's own place), which also says what a row without keys gives.
  *   q, out:    [tokens][n_q_heads][head_dim], strides (head, token) positive
  *              multiples of 16 bytes; n_q_heads a multiple of n_kv_heads, at most
- *              64 times it. lse: dense fp32 [tokens][n_q_heads] or NULL.
+ *              64 times it. lse: dense fp32 [tokens][n_q_heads] or NULL. out and
+ *              lse must not overlap q or the pages.
+ *   Sums, softmax statistics and lse are fp32. bf16 queries take the tensor cores,
+ *              the probabilities (4 bits: times the step) rounded to bf16 for the
+ *              product with V; fp32 ones the CUDA cores, in fp32.
  *   max_q:     with starts: no sequence has more new tokens. max_k: the most keys
  *              of a sequence, or 0: as many as the table holds; it only steers the
  *              launch.

@@ -28,6 +28,8 @@ _NORM = struct.Struct("@8i2q4P12qP3qPf4x2Pf4x")
 _HEAD, _PTRS, _Q9, _Q3, _TAIL = (struct.Struct("@" + f) for f in ("9if2q", "5P", "9q", "3q", "4PPNP"))
 _ROT_HEAD, _Q12, _ROT_TAIL, _P2, _P4, _NORM_TAIL = (struct.Struct("@" + f) for f in ("8i2q", "12q", "P3qPf4x", "2P", "4P", "2Pf4x"))
 
+_DENSE = torch.contiguous_format  # empty_like(t, ...) costs a fifth of empty(shape, dtype, device)
+
 # The handle of a device's current stream as a number (torch.cuda.current_stream
 # builds a Stream object first, ten times the cost), where torch has it.
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -88,13 +90,13 @@ def _scale(scale) -> float:
 
 def _outputs(q, out, lse, return_lse, lse_shape):
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=_DENSE)
     else:
         _like(out, q, q.dim(), "out", q.shape)
         _strides(out, "out")
     if lse is None:
         if return_lse:
-            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+            lse = q.new_empty(lse_shape, dtype=torch.float32)
     elif lse.dtype != torch.float32 or lse.device != q.device or lse.shape != lse_shape or not lse.is_contiguous():
         raise ValueError(f"lse: need a contiguous float32 tensor of {tuple(lse_shape)} on {q.device}")
     return out, lse
@@ -104,7 +106,7 @@ def _workspace(workspace, need: int, q: torch.Tensor):
     if need == 0:
         return None, 0, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     size = workspace.numel() * workspace.element_size()
     if workspace.device != q.device or not workspace.is_contiguous() or size < need:
         raise ValueError(f"workspace: need {need} contiguous bytes on {q.device}")
@@ -404,14 +406,18 @@ def norm_rotary(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor,
     if inv_freq is None:
         positions = 0
     q_out, k_out, args = _rotary_args(q, k, positions, inv_freq, interleaved, scale, False, q_out, k_out)
-    wp = [0, 0]
-    for i, (w, name) in enumerate(((q_weight, "q_weight"), (k_weight, "k_weight"))):
-        if w is not None:
-            _like(w, q, 1, name, q.shape[-1:])
-            wp[i] = w.data_ptr()
-            if wp[i] % 16:
-                raise ValueError(f"{name}: need an address that is a multiple of 16 bytes")
-    _call("kvevict_norm_rotary", q.get_device(), args + _NORM_TAIL.pack(*wp, eps))
+    qw, kw = q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr()
+    key = (q.dtype, q.get_device(), q.shape[-1], q_weight.dtype, q_weight.get_device(), q_weight.shape, q_weight.stride(),
+           None if k_weight is None else (k_weight.dtype, k_weight.get_device(), k_weight.shape, k_weight.stride()))
+    if key not in _layouts:
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _like(w, q, 1, name, q.shape[-1:])
+        _remember(key, _Layout())
+    for w, name in ((qw, "q_weight"), (kw, "k_weight")):
+        if w % 16:
+            raise ValueError(f"{name}: need an address that is a multiple of 16 bytes")
+    _call("kvevict_norm_rotary", q.get_device(), args + _NORM_TAIL.pack(qw, kw, eps))
     return q_out if k is None else (q_out, k_out)
 
 
@@ -422,18 +428,18 @@ def _rotary_args(q, k, positions, inv_freq, interleaved, scale, inverse, q_out, 
            None if inv_freq is None else inv_freq.shape, interleaved, inverse)
     lay = _layouts.get(key) or _remember(key, _rotary_layout(q, k, positions, inv_freq, interleaved, inverse))
     if q_out is None and k_out is None:
-        q_out, strides = torch.empty(q.shape, dtype=q.dtype, device=q.device), lay.strides
+        q_out, strides = torch.empty_like(q, memory_format=_DENSE), lay.strides
         if k is not None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            k_out = torch.empty_like(k, memory_format=_DENSE)
     else:
         dims = q.dim()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=_DENSE)
         _like(q_out, q, dims, "q_out", q.shape)
         _strides(q_out, "q_out")
         if k is not None:
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+                k_out = torch.empty_like(k, memory_format=_DENSE)
             _like(k_out, q, dims, "k_out", k.shape)
             _strides(k_out, "k_out")
         strides = _Q12.pack(*_heads(q), *_heads(q_out), *((0,) * 6 if k is None else (*_heads(k), *_heads(k_out))))

@@ -169,7 +169,7 @@ def paged_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
             raise ValueError(f"paged_gather: need pages of 4 axes and float32 or bfloat16, got {tuple(k_pages.shape)} and {t}")
         d = k_pages.shape[-1] * 8 // 5 if k_pages.dtype is torch.uint8 else k_pages.shape[-1]
         shape = (block_table.shape[0], k_pages.shape[1], most, d) if k_starts is None else (most, k_pages.shape[1], d)
-        k_out, v_out = (torch.empty(shape, dtype=t, device=k_pages.device) for _ in range(2))
+        k_out, v_out = k_pages.new_empty(shape, dtype=t), k_pages.new_empty(shape, dtype=t)
     key = ("gather", k_out.dtype, v_out.dtype, k_out.get_device(), v_out.get_device(), k_out.shape, v_out.shape, k_out.stride(), v_out.stride(),
            *_pages_key(k_pages, v_pages, block_table, kv_lens), k_starts is None)
     lay = ops._layouts.get(key) or _remember(key, _gather_layout(k_pages, v_pages, block_table, k_starts, k_out, v_out))
