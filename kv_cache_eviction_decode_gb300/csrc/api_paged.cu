@@ -155,7 +155,7 @@ int plan_attention(const kvevict_paged_attention_args *a, Plan &w)
     p.mask.q_starts = a->q_starts;
     const bool tensor = a->c.dtype == KVEVICT_BF16, q4 = a->c.page_dtype == KVEVICT_Q4;
     const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
-    w.rows = !tensor ? kPagedSimtRows : rows <= 8 ? 8 : 16;
+    w.rows = tensor ? (rows <= 8 ? 8 : 16) : rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
     p.q_tiles = static_cast<int>((rows + w.rows - 1) / w.rows);
     const int64_t units = static_cast<int64_t>(a->c.batch) * a->c.n_kv_heads * p.q_tiles;
     const int64_t tiles = key_tiles(max_k, p.mask.n_sink, p.mask.window, std::min<int64_t>(p.max_q, (w.rows + p.G - 1) / p.G + 1));
@@ -296,7 +296,7 @@ extern "C" int kvevict_paged_attention(const kvevict_paged_attention_args *a, vo
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const bool bf16 = a->c.dtype == KVEVICT_BF16, q4 = a->c.page_dtype == KVEVICT_Q4;
-    cudaError_t e = bf16 ? launch_paged_mma(p, a->c.head_dim, q4, w.rows, st) : launch_paged_simt(p, a->c.head_dim, bf16, q4, st);
+    cudaError_t e = bf16 ? launch_paged_mma(p, a->c.head_dim, q4, w.rows, st) : launch_paged_simt(p, a->c.head_dim, q4, w.rows, st);
     if (e == cudaSuccess && p.splits > 1) e = launch_paged_join(p, a->c.head_dim, bf16, st);
     return e == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
 }

@@ -1,11 +1,13 @@
-// paged_attn.cu -- attention over a paged cache on the CUDA cores, and the join of
-// an attention's parts.
+// paged_attn.cu -- attention of fp32 queries over a paged cache, fp32 or 4 bits, on
+// the CUDA cores, and the join of an attention's parts.
 //
 // out_i = sum_j 2^(z_ij - M_i) v_j / sum_j 2^(z_ij - M_i), z = q . k * scale *
 // log2(e), M the running maximum of one pass. A warp takes tiles of 16 keys; a lane
-// holds eight channels of eight query rows and of their outputs, D / 8 lanes a key.
+// holds eight channels of up to eight query rows and of their outputs, D / 8 lanes a key.
 // The partial products of a key are added up so that each lane ends with one row's
-// logit (three halving exchanges), which is also how softmax is spread.
+// logit (halving exchanges), which is also how softmax is spread. 8 sequences to 8000
+// tokens, 8 heads of 128, one token each: 78 us (4.9 TB/s), 233 with items of eight
+// rows whatever there are and nothing read ahead; 32 heads over 8: 95 (237).
 #include <cmath>
 
 #include "launch.h"
@@ -25,43 +27,62 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8])
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
+__device__ __forceinline__ void store8(float *p, const float (&v)[8])
 {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    bf16x2_to_f32(w.x, v[0], v[1]);
-    bf16x2_to_f32(w.y, v[2], v[3]);
-    bf16x2_to_f32(w.z, v[4], v[5]);
-    bf16x2_to_f32(w.w, v[6], v[7]);
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&v)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = Elem<T>::from_f32(v[i]);
-}
+// Eight channels as they lie in a page: fp32, or the codes and the group's base and
+// step.
+template <bool Q4> struct Raw {
+    static constexpr int kWords = Q4 ? 2 : 8;
+    uint32_t w[kWords];
 
-// Channels 8 s .. 8 s + 7 of row `slot` of a head's block in a page.
-template <typename T, bool Q4, int D>
-__device__ __forceinline__ void page_row8(const char *block, int slot, long long token_bytes, int S, int s, float (&v)[8])
-{
-    if constexpr (Q4) {
-        const int j = s / 4, g = s % 4 * 2;
-        const char *codes = block + slot * (D / 2) + 2 * j;
-        const uint32_t w = *reinterpret_cast<const uint16_t *>(codes + (D / 16) * g) |
-                           static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(codes + (D / 16) * (g + 1))) << 16;
-        const uint32_t bs = *reinterpret_cast<const uint32_t *>(block + S * (D / 2) + slot * (D / 8) + 4 * j);
+    __device__ __forceinline__ void zero()
+    {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(static_cast<float>(static_cast<int>(w >> (4 * i) & 15u) - 8), q4_step(bs), q4_base(bs));
-    } else {
-        load8(reinterpret_cast<const T *>(block + slot * token_bytes) + 8 * s, v);
+        for (int i = 0; i < kWords; ++i) w[i] = 0;  // (4 bits: base and step 0)
     }
-}
+    // Channels 8 s .. 8 s + 7 of row `slot` of a head's block in a page.
+    template <int D> __device__ __forceinline__ void load(const char *block, int slot, long long token_bytes, int S, int s)
+    {
+        if constexpr (Q4) {
+            const int j = s / 4, g = s % 4 * 2;
+            const char *codes = block + slot * (D / 2) + 2 * j;
+            w[0] = *reinterpret_cast<const uint16_t *>(codes + (D / 16) * g) |
+                   static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(codes + (D / 16) * (g + 1))) << 16;
+            w[1] = *reinterpret_cast<const uint32_t *>(block + S * (D / 2) + slot * (D / 8) + 4 * j);
+        } else {
+            const char *p = block + slot * token_bytes + 32 * s;
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
+                w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        if constexpr (Q4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(static_cast<float>(static_cast<int>(w[0] >> (4 * i) & 15u) - 8), q4_step(w[1]), q4_base(w[1]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+        }
+    }
+};
 
-template <typename T, bool Q4, int D>
+// R rows of an item: the arithmetic is per row, so an item of few is not computed as
+// one of eight. With up to four, V's rows and the next tile's K are on their way
+// while a tile's logits and products are made.
+template <bool Q4, int D, int R>
 __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __grid_constant__ PagedAttnParams p)
 {
-    constexpr int R = kPagedSimtRows, kLanes = D / 8, kKeys = 32 / kLanes, U = kPagedTile / kKeys;  // keys at once, steps a tile
-    constexpr int kRowShift = D == 128 ? 1 : 0;  // D = 128: two lanes hold the same row's logit
+    constexpr int kLanes = D / 8, kKeys = 32 / kLanes, U = kPagedTile / kKeys;  // lanes a key, keys at once, steps a tile
+    constexpr int kShift = R == 8 ? (D == 128 ? 1 : 0) : R == 4 ? (D == 128 ? 2 : 1) : R == 2 ? (D == 128 ? 3 : 2) : (D == 128 ? 4 : 3);
+    constexpr bool kAhead = R <= 4;
     __shared__ float s_o[kSimtWarps][R][D], s_m[kSimtWarps][R], s_l[kSimtWarps][R];
     grid_dependency_wait();
     const PagedCache &c = p.c;
@@ -87,46 +108,73 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
         for (int i = 0; i < 8; ++i) q[r][i] = o[r][i] = 0.f;
         if (r < nr) {
             const int t = (r0 + r) / p.G, g = r0 + r - t * p.G;
-            load8(static_cast<const T *>(p.q) + (kvh * p.G + g) * p.qs[0] + (sq.q0 + t) * p.qs[1] + 8 * s, q[r]);
+            load8(static_cast<const float *>(p.q) + (kvh * p.G + g) * p.qs[0] + (sq.q0 + t) * p.qs[1] + 8 * s, q[r]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[r][i] *= p.scale_log2;
         }
     }
     // the row whose softmax this lane keeps, and the keys it sees: j <= top, and j < n_sink or j >= low
-    const int mine = s >> kRowShift;
+    const int mine = s >> kShift;
     const int pos = sq.p0 + (r0 + mine) / p.G;
     const int top = mine < nr ? pos : -1, low = p.mask.window > 0 && pos >= p.mask.window ? pos - p.mask.window + 1 : 0;
     float m = -INFINITY, l = 0.f;
 
+    auto seen = [&](int j) { return j < keys.sink || (j >= keys.lo && j < keys.hi); };
+    // tile i's first key and page; the next one's page is looked up one tile ahead
+    auto first_key = [&](int i) { return attn_tile_at(keys, i) * kPagedTile; };
+    auto page_at = [&](int i) { return i < i_hi ? paged_page(c, b, first_key(i)) : -1; };
+    auto load_tile = [&](Raw<Q4>(&x)[U], int which, int j0, int page) {
+        const char *block = c.pages[which] + max(page, 0) * c.page_bytes[which] + kvh * c.head_bytes[which];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int key = u * kKeys + kk;
+            x[u].zero();
+            if (page >= 0 && seen(j0 + key)) x[u].template load<D>(block, (j0 & (c.S - 1)) + key, c.token_bytes[which], c.S, s);
+        }
+    };
+    Raw<Q4> ks[kAhead ? U : 1], vs[kAhead ? U : 1];
+    int page = page_at(i_lo + warp), page_next = page_at(i_lo + warp + kSimtWarps);
+    if constexpr (kAhead) {
+        if (i_lo + warp < i_hi) load_tile(ks, 0, first_key(i_lo + warp), page);
+    }
     for (int i = i_lo + warp; i < i_hi; i += kSimtWarps) {
-        const int j0 = attn_tile_at(keys, i) * kPagedTile;
-        const int page = paged_page(c, b, j0);
+        const int j0 = first_key(i), page_after = page_at(i + 2 * kSimtWarps);
         if (page < 0) {
             if (lane == 0) atomicOr(c.err, KVEVICT_DEV_BAD_PAGE);
+            if constexpr (kAhead) {
+                if (i + kSimtWarps < i_hi) load_tile(ks, 0, first_key(i + kSimtWarps), page_next);
+            }
+            page = page_next;
+            page_next = page_after;
             continue;
         }
         const char *kb = c.pages[0] + page * c.page_bytes[0] + kvh * c.head_bytes[0];
         const char *vb = c.pages[1] + page * c.page_bytes[1] + kvh * c.head_bytes[1];
         const int slot0 = j0 & (c.S - 1);
+        if constexpr (kAhead) load_tile(vs, 1, j0, page);
         float z[U], mx = -INFINITY;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int key = u * kKeys + kk, j = j0 + key;
-            const bool seen = j < keys.sink || (j >= keys.lo && j < keys.hi);
             float k[8], d[R];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) k[e] = 0.f;
-            if (seen) page_row8<T, Q4, D>(kb, slot0 + key, c.token_bytes[0], c.S, s, k);
+            if constexpr (kAhead) {
+                ks[u].get(k);
+            } else {
+                Raw<Q4> x;
+                x.zero();
+                if (seen(j)) x.template load<D>(kb, slot0 + key, c.token_bytes[0], c.S, s);
+                x.get(k);
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 d[r] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[r] = fmaf(q[r][e], k[e], d[r]);
             }
-            // a lane keeps the rows whose bits are its own, and sends the others
+            // a lane keeps the rows whose bits are its own, and sends the others; then the lanes of one row add up
 #pragma unroll
-            for (int w = 4; w; w >>= 1) {
-                const int o_ = w << kRowShift;
+            for (int w = R / 2; w; w >>= 1) {
+                const int o_ = w << kShift;
                 const bool high = s & o_;
 #pragma unroll
                 for (int r = 0; r < w; ++r) {
@@ -134,9 +182,13 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
                     d[r] = keep + __shfl_xor_sync(kAll, send, o_);
                 }
             }
-            if (kRowShift) d[0] += __shfl_xor_sync(kAll, d[0], 1);
-            z[u] = seen && j <= top && (j < p.mask.n_sink || j >= low) ? d[0] : -INFINITY;
+#pragma unroll
+            for (int o_ = (1 << kShift) / 2; o_; o_ >>= 1) d[0] += __shfl_xor_sync(kAll, d[0], o_);
+            z[u] = seen(j) && j <= top && (j < p.mask.n_sink || j >= low) ? d[0] : -INFINITY;
             mx = fmaxf(mx, z[u]);
+        }
+        if constexpr (kAhead) {
+            if (i + kSimtWarps < i_hi) load_tile(ks, 0, first_key(i + kSimtWarps), page_next);
         }
 #pragma unroll
         for (int o_ = kLanes; o_ < 32; o_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o_));
@@ -150,27 +202,33 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float fr = __shfl_sync(kAll, f, r << kRowShift);
+            const float fr = __shfl_sync(kAll, f, r << kShift);
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[r][e] *= fr;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int key = u * kKeys + kk, j = j0 + key;
-            const bool seen = j < keys.sink || (j >= keys.lo && j < keys.hi);
+            const int key = u * kKeys + kk;
             float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-            if (seen) page_row8<T, Q4, D>(vb, slot0 + key, c.token_bytes[1], c.S, s, v);
+            if constexpr (kAhead) {
+                vs[u].get(v);
+            } else {
+                Raw<Q4> x;
+                x.zero();
+                if (seen(j0 + key)) x.template load<D>(vb, slot0 + key, c.token_bytes[1], c.S, s);
+                x.get(v);
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float w = __shfl_sync(kAll, z[u], (lane & ~(kLanes - 1)) | r << kRowShift);
+                const float w = __shfl_sync(kAll, z[u], (lane & ~(kLanes - 1)) | r << kShift);
                 // (4 bits: a row that does not see the key takes nothing of it, whatever it stands for)
                 if (Q4 && w == 0.f) continue;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[r][e] = fmaf(w, v[e], o[r][e]);
             }
         }
+        page = page_next;
+        page_next = page_after;
     }
 
     // the keys of a step, then the warps
@@ -187,7 +245,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int e = 0; e < 8; ++e) s_o[warp][r][8 * s + e] = o[r][e];
-        if ((s & ((1 << kRowShift) - 1)) == 0) {
+        if ((s & ((1 << kShift) - 1)) == 0) {
             s_m[warp][mine] = m;
             s_l[warp][mine] = l;
         }
@@ -219,7 +277,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
             store8(p.part_o + at * D + ch, v);
             if (ch == 0) p.part_l[at] = lse2;
         } else {
-            store8(static_cast<T *>(p.out) + h * p.os[0] + t * p.os[1] + ch, v);
+            store8(static_cast<float *>(p.out) + h * p.os[0] + t * p.os[1] + ch, v);
             if (ch == 0 && p.lse) p.lse[row] = lse2 * kLn2;
         }
     }
@@ -267,10 +325,15 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     }
 }
 
-template <typename T, int D> cudaError_t simt_for(const PagedAttnParams &p, bool q4, cudaStream_t st)
+template <int D, int R> cudaError_t simt_rows(const PagedAttnParams &p, bool q4, cudaStream_t st)
 {
     const unsigned grid = static_cast<unsigned>(p.c.batch) * p.c.Hkv * p.q_tiles * p.splits;
-    return launch_dependent(q4 ? paged_simt_kernel<T, true, D> : paged_simt_kernel<T, false, D>, grid, kSimtWarps * 32, 0, st, p);
+    return launch_dependent(q4 ? paged_simt_kernel<true, D, R> : paged_simt_kernel<false, D, R>, grid, kSimtWarps * 32, 0, st, p);
+}
+
+template <int D> cudaError_t simt_for(const PagedAttnParams &p, bool q4, int rows, cudaStream_t st)
+{
+    return rows == 1 ? simt_rows<D, 1>(p, q4, st) : rows == 2 ? simt_rows<D, 2>(p, q4, st) : rows == 4 ? simt_rows<D, 4>(p, q4, st) : simt_rows<D, 8>(p, q4, st);
 }
 
 template <typename T, int D> cudaError_t join_for(const PagedAttnParams &p, cudaStream_t st)
@@ -281,10 +344,9 @@ template <typename T, int D> cudaError_t join_for(const PagedAttnParams &p, cuda
 
 }  // namespace
 
-cudaError_t launch_paged_simt(const PagedAttnParams &p, int head_dim, bool bf16, bool q4, cudaStream_t st)
+cudaError_t launch_paged_simt(const PagedAttnParams &p, int head_dim, bool q4, int rows, cudaStream_t st)
 {
-    if (bf16) return head_dim == 64 ? simt_for<__nv_bfloat16, 64>(p, q4, st) : simt_for<__nv_bfloat16, 128>(p, q4, st);
-    return head_dim == 64 ? simt_for<float, 64>(p, q4, st) : simt_for<float, 128>(p, q4, st);
+    return head_dim == 64 ? simt_for<64>(p, q4, rows, st) : simt_for<128>(p, q4, rows, st);
 }
 
 cudaError_t launch_paged_join(const PagedAttnParams &p, int head_dim, bool bf16, cudaStream_t st)

@@ -54,9 +54,8 @@ __device__ __forceinline__ PagedSeq paged_sequence(const PagedAttnParams &p, int
     return s;
 }
 
-// fp32 arithmetic on the CUDA cores, for every type.
-constexpr int kPagedSimtRows = 8;
-cudaError_t launch_paged_simt(const PagedAttnParams &p, int head_dim, bool bf16, bool q4, cudaStream_t st);
+// fp32 queries on the CUDA cores; rows: 1, 2, 4 or 8 of an item.
+cudaError_t launch_paged_simt(const PagedAttnParams &p, int head_dim, bool q4, int rows, cudaStream_t st);
 // bf16 queries on the tensor cores; rows: 8 or 16 of an item.
 constexpr int kPagedMmaWarps = 4;
 cudaError_t launch_paged_mma(const PagedAttnParams &p, int head_dim, bool q4, int rows, cudaStream_t st);
