@@ -113,27 +113,39 @@ int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens)
     return std::min(all, (static_cast<int64_t>(n_sink) + kPagedTile - 1) / kPagedTile + (window + tokens - 1 + kPagedTile - 1) / kPagedTile + 1);
 }
 
-// Parts that the keys of a unit are split into. An item takes the tiles of a warp
-// and `item` tiles more for its start and end, joining the parts costs kJoinCost.
-// Items under a window are of one length and run in waves of `slots` CTAs. Without
-// one their lengths are on the device, and taken to spread around kShare of the
-// longest: the slots are then filled but for half an item at the end. (4 bits, 256
-// units of up to 2048 tiles: 316, 231, 221, 224 and 245 us with 1, 4, 7, 10 and 20
-// parts; bf16, 256 units of up to 640: 167, 149, 152 and 164 us with 1, 5, 10 and
-// 16; 4 bits, 128 units of 130 under a window: 41, 31, 41 us with 1, 2 and 3.)
-constexpr double kJoinCost = 4, kShare = 0.75;
+// Parts that the keys of a unit are split into, by a cost in a warp's tiles. An item
+// takes kItemCost more for its start and end, joining takes what is below, both times
+// `light`: 1 where a tile is 4 bits, less where it is more bytes (bf16 a half, fp32 a
+// quarter). Items under a window are of one length
+// and run in waves of `slots` CTAs. Without one their lengths are on the device, and
+// taken to spread around kShare of the longest: the slots are then filled but for half
+// an item at the end. (4 bits, 256 units of up to 2048 tiles: 316, 231, 221, 224 and
+// 245 us with 1, 4, 7, 10 and 20 parts; bf16, 256 units of up to 640: 167, 149, 152
+// and 164 us with 1, 5, 10 and 16; 4 bits, 128 units of 130 under a window: 41, 31, 41
+// us with 1, 2 and 3.)
+// Up to eight parts are joined in clusters where all of them run at once, with some
+// room, as clusters do not fill every slot (4 bits, 32 units of 63 tiles: 9.5 us with
+// eight parts, 11.4 through the workspace, 12.8 with one; 64 units of 250: 16.4 with
+// six, 17.7 with four through the workspace; but 256 units of 2048 in seven: 242,
+// through the workspace 213).
+constexpr int kMaxCluster = 8;
+constexpr double kItemCost = 6, kClusterCost = 3, kJoinCost = 8, kJoinPart = 0.1, kShare = 0.75, kClusterFill = 0.9;
 
-int parts(int64_t units, int64_t tiles, int64_t slots, double item, bool window)
+int parts(int64_t units, int64_t tiles, int64_t slots, double light, bool window, int &clusters)
 {
     int best = 1;
     double least = 0;
+    clusters = 0;
     for (int64_t s = 1; s <= kMaxParts && (s == 1 || s * kPagedMmaWarps <= tiles); ++s) {
         const double load = static_cast<double>(units * s) / static_cast<double>(slots);
-        const double len = std::ceil(static_cast<double>(tiles) / static_cast<double>(s * kPagedMmaWarps)), longest = len + item;
-        const double cost = (window ? std::ceil(load) * longest : std::max(longest, load * (len * kShare + item) + longest / 2)) + (s > 1 ? kJoinCost : 0);
+        const double item = kItemCost * light, len = std::ceil(static_cast<double>(tiles) / static_cast<double>(s * kPagedMmaWarps)), longest = len + item;
+        const bool cluster = s > 1 && s <= kMaxCluster && load <= kClusterFill;
+        const double cost = (window ? std::ceil(load) * longest : std::max(longest, load * (len * kShare + item) + longest / 2)) +
+                            (s == 1 ? 0 : cluster ? kClusterCost : kJoinCost + kJoinPart * static_cast<double>(s)) * light;
         if (s == 1 || cost < least * 0.99) {
             least = cost;
             best = static_cast<int>(s);
+            clusters = cluster;
         }
     }
     return best;
@@ -162,11 +174,12 @@ int plan_attention(const kvevict_paged_attention_args *a, Plan &w)
     // (with starts only the mean of the new tokens is known here)
     const int64_t mean = a->c.batch ? (a->tokens + a->c.batch - 1) / a->c.batch * p.G : 0;
     const int64_t busy = static_cast<int64_t>(a->c.batch) * a->c.n_kv_heads * std::min<int64_t>(p.q_tiles, (mean + w.rows - 1) / w.rows);
-    p.splits = parts(busy, tiles, kSMs * (!tensor || (q4 && w.rows == 8) ? 3 : 2), q4 ? 6 : 3, p.mask.window > 0);
+    p.splits = parts(busy, tiles, kSMs * (!tensor || (q4 && w.rows == 8) ? 3 : 2), q4 && tensor ? 1 : tensor || q4 ? 0.5 : 0.25, p.mask.window > 0,
+                     p.clusters);
     w.items = units * p.splits;
     if (w.items >= (int64_t{1} << 31)) return KVEVICT_ERR_INVALID_ARG;
     const size_t slots = static_cast<size_t>(p.splits) * a->tokens * p.Hq;
-    w.bytes = p.splits > 1 ? up256(slots * a->c.head_dim * 4) + up256(slots * 4) : 0;
+    w.bytes = p.splits > 1 && !p.clusters ? up256(slots * a->c.head_dim * 4) + up256(slots * 4) : 0;
     return KVEVICT_OK;
 }
 
@@ -297,6 +310,6 @@ extern "C" int kvevict_paged_attention(const kvevict_paged_attention_args *a, vo
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const bool bf16 = a->c.dtype == KVEVICT_BF16, q4 = a->c.page_dtype == KVEVICT_Q4;
     cudaError_t e = bf16 ? launch_paged_mma(p, a->c.head_dim, q4, w.rows, st) : launch_paged_simt(p, a->c.head_dim, q4, w.rows, st);
-    if (e == cudaSuccess && p.splits > 1) e = launch_paged_join(p, a->c.head_dim, bf16, st);
+    if (e == cudaSuccess && p.splits > 1 && !p.clusters) e = launch_paged_join(p, a->c.head_dim, bf16, st);
     return e == cudaSuccess ? KVEVICT_OK : KVEVICT_ERR_CUDA;
 }

@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
     constexpr int kLanes = D / 8, kKeys = 32 / kLanes, U = kPagedTile / kKeys;  // lanes a key, keys at once, steps a tile
     constexpr int kShift = R == 8 ? (D == 128 ? 1 : 0) : R == 4 ? (D == 128 ? 2 : 1) : R == 2 ? (D == 128 ? 3 : 2) : (D == 128 ? 4 : 3);
     constexpr bool kAhead = R <= 4;
-    __shared__ float s_o[kSimtWarps][R][D], s_m[kSimtWarps][R], s_l[kSimtWarps][R];
+    __shared__ __align__(16) float s_o[kSimtWarps][R][D];
+    __shared__ float s_m[kSimtWarps][R], s_l[kSimtWarps][R], s_cm[R], s_cl[R];  // a warp's, the CTA's
     grid_dependency_wait();
     const PagedCache &c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -251,9 +252,9 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < nr * kLanes; e += kSimtWarps * 32) {
-        const int r = e / kLanes, ch = e % kLanes * 8;
-        float big = -INFINITY, total = 0.f, v[8];
+    auto join_warps = [&](int r, int ch, float(&v)[8], float &big) {
+        float total = 0.f;
+        big = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
 #pragma unroll
@@ -266,13 +267,34 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = fmaf(f, s_o[w][r][ch + i], v[i]);
         }
+        return total;
+    };
+    if (p.clusters) {
+        // into the place of the first warp's part, where only this thread reads; then each CTA of the cluster joins a share
+        for (int e = threadIdx.x; e < nr * kLanes; e += kSimtWarps * 32) {
+            const int r = e / kLanes, ch = e % kLanes * 8;
+            float v[8], big;
+            const float total = join_warps(r, ch, v, big);
+            store8(&s_o[0][r][ch], v);
+            if (ch == 0) {
+                s_cm[r] = big;
+                s_cl[r] = total;
+            }
+        }
+        cluster_sync();
+    }
+    const int share = p.clusters ? p.splits : 1, from = p.clusters ? part : 0;
+    for (int e = threadIdx.x * share + from; e < nr * kLanes; e += kSimtWarps * 32 * share) {
+        const int r = e / kLanes, ch = e % kLanes * 8;
+        float v[8], big;
+        const float total = p.clusters ? paged_join_peers(&s_o[0][r][ch], &s_cm[r], &s_cl[r], p.splits, v, big) : join_warps(r, ch, v, big);
         const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= inv;
         const float lse2 = total == 0.f ? -INFINITY : big + log2f(total);
         const int t = sq.q0 + (r0 + r) / p.G, h = kvh * p.G + (r0 + r) % p.G;
         const long long row = static_cast<long long>(t) * p.Hq + h;
-        if (p.splits > 1) {
+        if (p.splits > 1 && !p.clusters) {
             const long long at = static_cast<long long>(part) * p.tokens * p.Hq + row;
             store8(p.part_o + at * D + ch, v);
             if (ch == 0) p.part_l[at] = lse2;
@@ -281,6 +303,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __gri
             if (ch == 0 && p.lse) p.lse[row] = lse2 * kLn2;
         }
     }
+    if (p.clusters) cluster_sync();  // no CTA's shared memory goes while another reads it
 }
 
 // One warp per query row: the parts' weights from their log2 normalisers, then
@@ -328,7 +351,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 template <int D, int R> cudaError_t simt_rows(const PagedAttnParams &p, bool q4, cudaStream_t st)
 {
     const unsigned grid = static_cast<unsigned>(p.c.batch) * p.c.Hkv * p.q_tiles * p.splits;
-    return launch_dependent(q4 ? paged_simt_kernel<true, D, R> : paged_simt_kernel<false, D, R>, grid, kSimtWarps * 32, 0, st, p);
+    return launch_dependent(q4 ? paged_simt_kernel<true, D, R> : paged_simt_kernel<false, D, R>, grid, kSimtWarps * 32, 0, st, p,
+                            p.clusters ? static_cast<unsigned>(p.splits) : 1u);
 }
 
 template <int D> cudaError_t simt_for(const PagedAttnParams &p, bool q4, int rows, cudaStream_t st)

@@ -4,9 +4,10 @@
 // A unit is a (sequence, KV head); its query rows are (token, group head) pairs,
 // row = token * G + g, so that the G query heads of a KV head share every key. An
 // item of work is a tile of rows of one unit against one of `splits` parts of the
-// 16-key tiles that those rows see (a tile lies in one page); with more than one
-// part each writes its own normalised output and log2 normaliser to the workspace,
-// and launch_paged_join joins them.
+// 16-key tiles that those rows see (a tile lies in one page). Up to eight parts are
+// the CTAs of a cluster, which join them through distributed shared memory; of more,
+// each writes its own normalised output and log2 normaliser to the workspace, and
+// launch_paged_join joins them.
 #pragma once
 
 #include "paged_common.cuh"
@@ -27,8 +28,9 @@ struct PagedAttnParams {
     int G, Hq;
     float scale_log2;
     int splits, q_tiles;
+    int clusters;      // the parts are joined in their cluster
     float *part_o;     // [splits][tokens * Hq][d], and
-    float *part_l;     // [splits][tokens * Hq] log2 normalisers, where splits > 1
+    float *part_l;     // [splits][tokens * Hq] log2 normalisers, where splits > 1 and not clusters
 };
 
 // A sequence's new tokens and keys: rows q0 .. q0 + n - 1, the first of them at
@@ -52,6 +54,36 @@ __device__ __forceinline__ PagedSeq paged_sequence(const PagedAttnParams &p, int
     s.bad = r.bad || !sound || s.n != r.n || s.m != len;
     s.p0 = paged_max(s.m - r.given, -(1 << 30));
     return s;
+}
+
+// Four values of a CTA of the cluster (an address from peer_addr).
+__device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Eight channels of a row, joined over the cluster's parts: each has its maximum (to
+// base 2), its sum and its unnormalised output at the same places of its shared
+// memory. Returns the sum, and the maximum in `big`.
+__device__ __forceinline__ float paged_join_peers(const float *o, const float *m, const float *l, int parts, float (&v)[8], float &big)
+{
+    big = -INFINITY;
+    for (int s = 0; s < parts; ++s) big = fmaxf(big, ld_peer_f32(peer_addr(m, s)));
+    const float base = big == -INFINITY ? 0.f : big;
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    for (int s = 0; s < parts; ++s) {
+        const float f = exp2f(ld_peer_f32(peer_addr(m, s)) - base);
+        total = fmaf(f, ld_peer_f32(peer_addr(l, s)), total);
+        const uint32_t at = peer_addr(o, s);
+        const float4 a = ld_peer_f32x4(at), b = ld_peer_f32x4(at + 16);
+        v[0] = fmaf(f, a.x, v[0]); v[1] = fmaf(f, a.y, v[1]); v[2] = fmaf(f, a.z, v[2]); v[3] = fmaf(f, a.w, v[3]);
+        v[4] = fmaf(f, b.x, v[4]); v[5] = fmaf(f, b.y, v[5]); v[6] = fmaf(f, b.z, v[6]); v[7] = fmaf(f, b.w, v[7]);
+    }
+    return total;
 }
 
 // fp32 queries on the CUDA cores; rows: 1, 2, 4 or 8 of an item.

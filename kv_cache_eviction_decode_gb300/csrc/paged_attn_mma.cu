@@ -51,7 +51,7 @@ template <int D, bool Q4, int NT> struct Ring {
 
 template <int D, bool Q4, int NT> constexpr int smem_bytes()
 {
-    constexpr int ring = Ring<D, Q4, NT>::kWarpBytes * kWarps, join = kWarps * 8 * NT * (D + 4 + 2) * 4;
+    constexpr int ring = Ring<D, Q4, NT>::kWarpBytes * kWarps, join = (kWarps * (D + 4 + 2) + 2) * 8 * NT * 4;
     return ring > join ? ring : join;
 }
 
@@ -150,9 +150,9 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
     const PagedCache &c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int item = blockIdx.x;
-    const int tile = item % p.q_tiles;
-    item /= p.q_tiles;
-    const int part = item % p.splits, unit = item / p.splits;
+    const int part = item % p.splits;
+    item /= p.splits;
+    const int tile = item % p.q_tiles, unit = item / p.q_tiles;
     const int b = unit / c.Hkv, kvh = unit - b * c.Hkv;
     const PagedSeq sq = paged_sequence(p, b, !p.mask.q_starts || attn_first_fall(p.mask, b, lane) == INT_MAX);
     if (sq.bad && threadIdx.x == 0) atomicOr(c.err, KVEVICT_DEV_BAD_LENGTH);
@@ -611,9 +611,11 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             }
         }
     __syncthreads();
-    for (int e = threadIdx.x; e < nr * (D / 8); e += kWarps * 32) {
-        const int r = e / (D / 8), ch = e % (D / 8) * 8;
-        float big = -FLT_MAX, total = 0.f, v[8];
+    float *const cm = sl + kWarps * R, *const cl = cm + R;  // the CTA's maximum and sum of a row
+    // the warps' parts of eight channels of a row (e: which), and the CTA's maximum and sum
+    auto join_warps = [&](int r, int ch, float(&v)[8], float &big) {
+        float total = 0.f;
+        big = -FLT_MAX;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
 #pragma unroll
@@ -625,13 +627,35 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = fmaf(f, so[(w * R + r) * kPad + ch + i], v[i]);
         }
+        return total;
+    };
+    if (p.clusters) {
+        // into the place of the first warp's part, where only this thread reads; then each CTA of the cluster joins a share
+        for (int e = threadIdx.x; e < nr * (D / 8); e += kWarps * 32) {
+            const int r = e / (D / 8), ch = e % (D / 8) * 8;
+            float v[8], big;
+            const float total = join_warps(r, ch, v, big);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) so[r * kPad + ch + i] = v[i];
+            if (ch == 0) {
+                cm[r] = big;
+                cl[r] = total;
+            }
+        }
+        cluster_sync();
+    }
+    const int share = p.clusters ? p.splits : 1, from = p.clusters ? part : 0;
+    for (int e = threadIdx.x * share + from; e < nr * (D / 8); e += kWarps * 32 * share) {
+        const int r = e / (D / 8), ch = e % (D / 8) * 8;
+        float v[8], big;
+        const float total = p.clusters ? paged_join_peers(so + r * kPad + ch, cm + r, cl + r, p.splits, v, big) : join_warps(r, ch, v, big);
         const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= inv;
         const float lse2 = total == 0.f ? -INFINITY : big + log2f(total);
         const int tk = (r0 + r) / p.G, h = kvh * p.G + r0 + r - tk * p.G;
         const long long row = static_cast<long long>(sq.q0 + tk) * p.Hq + h;
-        if (p.splits > 1) {
+        if (p.splits > 1 && !p.clusters) {
             const long long slot = static_cast<long long>(part) * p.tokens * p.Hq + row;
             float4 *po = reinterpret_cast<float4 *>(p.part_o + slot * D + ch);
             po[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -643,6 +667,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             if (ch == 0 && p.lse) p.lse[row] = lse2 * kLn2;
         }
     }
+    if (p.clusters) cluster_sync();  // no CTA's shared memory goes while another reads it
 }
 
 template <int D, bool Q4, int NT> cudaError_t mma_for(const PagedAttnParams &p, cudaStream_t st)
@@ -651,7 +676,8 @@ template <int D, bool Q4, int NT> cudaError_t mma_for(const PagedAttnParams &p, 
     auto kern = paged_mma_kernel<D, Q4, NT>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, static_cast<unsigned>(p.c.batch) * p.c.Hkv * p.q_tiles * p.splits, kWarps * 32, bytes, st, p);
+    return launch_dependent(kern, static_cast<unsigned>(p.c.batch) * p.c.Hkv * p.q_tiles * p.splits, kWarps * 32, bytes, st, p,
+                            p.clusters ? static_cast<unsigned>(p.splits) : 1u);
 }
 
 template <int D, bool Q4> cudaError_t mma_rows(const PagedAttnParams &p, int rows, cudaStream_t st)
