@@ -116,12 +116,13 @@ int64_t key_tiles(int64_t max_k, int n_sink, int window, int64_t tokens)
 // Parts that the keys of a unit are split into, by a cost in a warp's tiles. An item
 // takes kItemCost more for its start and end, joining takes what is below, both times
 // `light`: 1 where a tile is 4 bits, less where it is more bytes (bf16 a half, fp32 a
-// quarter). Items under a window are of one length
-// and run in waves of `slots` CTAs. Without one their lengths are on the device, and
-// taken to spread around kShare of the longest: the slots are then filled but for half
-// an item at the end. (4 bits, 256 units of up to 2048 tiles: 316, 231, 221, 224 and
-// 245 us with 1, 4, 7, 10 and 20 parts; bf16, 256 units of up to 640: 167, 149, 152
-// and 164 us with 1, 5, 10 and 16; 4 bits, 128 units of 130 under a window: 41, 31, 41
+// quarter). Items under a window are of one length and run in waves of `slots` CTAs.
+// Without one their lengths are on the device, and taken to be anything from all alike
+// to spread around kShare of the longest, where the slots are filled but for half an
+// item at the end: the mean of both. (4 bits, 256 units of up to 2048 tiles: 316, 231,
+// 221, 224 and 245 us with 1, 4, 7, 10 and 20 parts; bf16, 256 units of up to 640: 167,
+// 149, 152 and 164 us with 1, 5, 10 and 16; bf16, 8 units of 2048, all alike: 36, 33, 34
+// and 45 us with 16, 24, 38 and 40; 4 bits, 128 units of 130 under a window: 41, 31, 41
 // us with 1, 2 and 3.)
 // Up to eight parts are joined in clusters where all of them run at once, with some
 // room, as clusters do not fill every slot (4 bits, 32 units of 63 tiles: 9.5 us with
@@ -140,7 +141,8 @@ int parts(int64_t units, int64_t tiles, int64_t slots, double light, bool window
         const double load = static_cast<double>(units * s) / static_cast<double>(slots);
         const double item = kItemCost * light, len = std::ceil(static_cast<double>(tiles) / static_cast<double>(s * kPagedMmaWarps)), longest = len + item;
         const bool cluster = s > 1 && s <= kMaxCluster && load <= kClusterFill;
-        const double cost = (window ? std::ceil(load) * longest : std::max(longest, load * (len * kShare + item) + longest / 2)) +
+        const double waves = std::ceil(load) * longest, spread = std::max(longest, load * (len * kShare + item) + longest / 2);
+        const double cost = (window ? waves : (waves + spread) / 2) +
                             (s == 1 ? 0 : cluster ? kClusterCost : kJoinCost + kJoinPart * static_cast<double>(s)) * light;
         if (s == 1 || cost < least * 0.99) {
             least = cost;
