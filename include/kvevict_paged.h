@@ -135,7 +135,8 @@ int kvevict_paged_gather(const kvevict_paged_gather_args *a, void *cuda_stream);
  *              lse must not overlap q or the pages.
  *   Sums, softmax statistics and lse are fp32. bf16 queries take the tensor cores,
  *              the probabilities (4 bits: times the step) rounded to bf16 for the
- *              product with V; fp32 ones the CUDA cores, in fp32.
+ *              product with V (steps of V below 2^-50 lose precision, bases above
+ *              2^60 may overflow); fp32 ones the CUDA cores, in fp32.
  *   max_q:     with starts: no sequence has more new tokens. max_k: the most keys
  *              of a sequence, or 0: as many as the table holds; it only steers the
  *              launch.

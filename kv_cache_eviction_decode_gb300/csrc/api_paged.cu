@@ -300,6 +300,11 @@ extern "C" int kvevict_paged_attention(const kvevict_paged_attention_args *a, vo
     }
     rc = bind_cache(a->c, p.c);
     if (rc) return rc;
+    if (a->c.n_pages == 0)  // no key is read, but the copies of none of its bytes need an address: a row of q
+        for (int i = 0; i < 2; ++i) {
+            p.c.pages[i] = const_cast<char *>(static_cast<const char *>(a->q));
+            p.c.head_bytes[i] = p.c.token_bytes[i] = 0;
+        }
     p.q = a->q;
     p.out = a->out;
     p.lse = a->lse;

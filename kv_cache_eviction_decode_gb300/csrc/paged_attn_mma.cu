@@ -202,36 +202,37 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
             if ((k * kTiles & 31) == 0) next_tiles(k * kTiles);
 #pragma unroll
             for (int h = 0; h < kTiles; ++h) {
-            const int from = (k * kTiles + h) & 31;
-            const int w = __shfl_sync(kAll, what, from);
-            const char *kb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[0]), from));
-            const char *vb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[1]), from));
-            const int slot0 = w & (c.S - kPagedTile);
-            if constexpr (Q4) {
-                if (!(w & kNoPage)) {
-                    const char *kc = kb + (slot0 * L::kRow + k_from), *vc = vb + (slot0 * L::kRow + v_from);
-                    const char *pc = (lane < kPc ? kb : vb) + (slot0 * L::kParams + p_from);
-                    const uint32_t dst = to + h * L::kTile + lane * 16;
+                const int from = (k * kTiles + h) & 31;
+                const int w = __shfl_sync(kAll, what, from);
+                const char *kb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[0]), from));
+                const char *vb = reinterpret_cast<const char *>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(block[1]), from));
+                const int slot0 = w & (c.S - kPagedTile);
+                if constexpr (Q4) {
+                    if (!(w & kNoPage)) {
+                        const char *kc = kb + (slot0 * L::kRow + k_from), *vc = vb + (slot0 * L::kRow + v_from);
+                        const char *pc = (lane < kPc ? kb : vb) + (slot0 * L::kParams + p_from);
+                        const uint32_t dst = to + h * L::kTile + lane * 16;
 #pragma unroll
-                    for (int e0 = 0; e0 < kPagedTile * L::kRow; e0 += 512) {
-                        copy16(dst + e0, kc + e0, true);
-                        copy16(dst + kPagedTile * L::kRow + e0, vc + e0, true);
+                        for (int e0 = 0; e0 < kPagedTile * L::kRow; e0 += 512) {
+                            copy16(dst + e0, kc + e0, true);
+                            copy16(dst + kPagedTile * L::kRow + e0, vc + e0, true);
+                        }
+                        if (lane < 2 * kPc) copy16(dst + 2 * kPagedTile * L::kRow, pc, true);
                     }
-                    if (lane < 2 * kPc) copy16(dst + 2 * kPagedTile * L::kRow, pc, true);
-                }
-            } else {
-                // 16-byte chunks swapped by row, so that the eight rows of a matrix load lie in different banks
-                constexpr int kChunks = L::kRow / 16;
-                const int j0 = w & ~(kPagedTile - 1);
+                } else {
+                    // 16-byte chunks swapped by row, so that the eight rows of a matrix load lie in different banks
+                    constexpr int kChunks = L::kRow / 16;
+                    const int j0 = w & ~(kPagedTile - 1);
 #pragma unroll
-                for (int e0 = 0; e0 < kPagedTile * kChunks; e0 += 32) {
-                    const int e = e0 + lane, r = e / kChunks, ch = e % kChunks, j = j0 + r;
-                    const bool real = !(w & kNoPage) && (j < keys.sink || (j >= keys.lo && j < keys.hi));
-                    const uint32_t at = r * L::kRow + ((ch & ~7) | ((ch ^ r) & 7)) * 16;
-                    copy16(to + at, kb + (slot0 + r) * c.token_bytes[0] + ch * 16, real);
-                    copy16(to + kPagedTile * L::kRow + at, vb + (slot0 + r) * c.token_bytes[1] + ch * 16, real);
+                    for (int e0 = 0; e0 < kPagedTile * kChunks; e0 += 32) {
+                        const int e = e0 + lane, r = e / kChunks, ch = e % kChunks, j = j0 + r;
+                        const bool real = !(w & kNoPage) && (j < keys.sink || (j >= keys.lo && j < keys.hi));
+                        const uint32_t at = r * L::kRow + ((ch & ~7) | ((ch ^ r) & 7)) * 16;
+                        // (zeros where no row sees the key; the address of a tile without a page is the first page's)
+                        copy16(to + at, kb + (slot0 + r) * c.token_bytes[0] + ch * 16, real);
+                        copy16(to + kPagedTile * L::kRow + at, vb + (slot0 + r) * c.token_bytes[1] + ch * 16, real);
+                    }
                 }
-            }
             }
         }
         to += L::kStage;

@@ -5,7 +5,7 @@ import torch
 
 import kv_cache_eviction_decode_gb300 as kv
 from tests import attn_reference as ref
-from tests.paged_reference import Pool, attention_bounds
+from tests.paged_reference import Pool, attention_bounds, parts
 
 pytestmark = pytest.mark.gpu
 KINDS = [(torch.bfloat16, False), (torch.float32, False), (torch.bfloat16, True), (torch.float32, True)]
@@ -240,6 +240,31 @@ def test_capture_streams_and_workspaces(cuda_device, dtype, four):
     torch.cuda.synchronize()
     for b, m in enumerate((2990, 2)):
         check_sequence(pool, b, q[b:b + 1], out[b:b + 1], lse[b:b + 1], m, 0, None, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_any_size_in_four_bits(cuda_device, d):
+    """V's groups far from one: small, large, and growing or falling by 2^40 from tile to tile of one sequence."""
+    for scale in ([2.0 ** -40], [2.0 ** 50], [2.0 ** -20, 2.0 ** 20], [2.0 ** 30, 2.0 ** -10], [2.0 ** -15, 1.0, 2.0 ** 15, 0.0]):
+        pool = Pool([400, 60], 2, 16, d, torch.bfloat16, True, seed=5)
+        _, params = parts(pool.v, d)
+        for b in range(2):
+            for j in range(-(-pool.lens[b] // 16)):
+                params[int(pool.table[b, j])] *= scale[j % len(scale)]
+        q = torch.randn(2, 8, d, device="cuda", dtype=torch.bfloat16, generator=torch.Generator(device="cuda").manual_seed(6))
+        out, lse = kv.paged_attention(q, pool.k, pool.v, pool.table, pool.kv_lens, return_lse=True)
+        for b, m in enumerate(pool.lens):
+            check_sequence(pool, b, q[b:b + 1], out[b:b + 1], lse[b:b + 1], m, 0, None, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,four", KINDS)
+def test_no_pages_at_all(cuda_device, dtype, four):
+    """A cache without pages: every key is in none, and nothing is read."""
+    k, v = kv.paged_pool(0, 2, 16, 64, dtype=dtype, four_bit=four)
+    table, lens = torch.zeros(1, 3, dtype=torch.int32, device="cuda"), torch.tensor([40], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = kv.paged_attention(torch.ones(1, 4, 64, device="cuda", dtype=dtype), k, v, table, lens, return_lse=True, error_word=err)
+    assert (out == 0).all() and (lse == -float("inf")).all() and int(err) == 0x20
 
 
 def test_nothing_to_do(cuda_device):
