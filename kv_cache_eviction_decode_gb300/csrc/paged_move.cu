@@ -79,7 +79,8 @@ __device__ __forceinline__ void form_cosines(const AppendParams &p, int nt, Plac
 // thread is two chunks of a head (a pair rotary_dim / 2 apart, or neighbours), and a
 // thread's units, kBatch of them, are all on their way while the CTA looks up its
 // tokens' places and forms its cosines: three dependent reads, which took longer
-// than the copying.
+// than the copying (13 prompts to 4097 tokens, 8 heads of 128, bf16: 28 us, 74% of the
+// copy bandwidth; 73 with eight bytes a lane loaded behind the reads).
 template <typename T, int D>
 __global__ void __launch_bounds__(kPagedThreads) append_own_kernel(const __grid_constant__ AppendParams p)
 {
@@ -415,7 +416,9 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_cons
 // A CTA takes kGatherRows rows of one head, keys and values, which it finds in the
 // pages once. Own type: 16-byte chunks, eight of a thread in flight. 4 bits: a unit
 // of one thread is an eighth of a row's codes twice (neighbouring g: eight channels
-// side by side of every group), so that the results go out in 16-byte chunks.
+// side by side of every group), so that the results go out in 16-byte chunks. (16
+// sequences to 16384 tokens, 8 heads of 128, 4 bits to bf16: 168 us, 99% of the copy
+// bandwidth.)
 template <typename T, bool Q4, int D>
 __global__ void __launch_bounds__(kPagedThreads) gather_kernel(const __grid_constant__ GatherParams p)
 {
