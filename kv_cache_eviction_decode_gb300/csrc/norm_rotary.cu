@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kRotThreads) norm_rotary_any_kernel(const __gr
 {
     constexpr int N = Vec<T>::N;
     const RotParams &p = np.r;
-    extern __shared__ float2 cs[];  // [R / 2] cos, sin, then [8][D] floats
+    extern __shared__ __align__(16) float2 cs[];  // [R / 2] cos, sin, then [8][D] floats
     const int half = p.R / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float *line = reinterpret_cast<float *>(cs + half) + warp * p.D;
     grid_dependency_wait();

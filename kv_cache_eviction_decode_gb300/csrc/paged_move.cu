@@ -85,7 +85,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPagedThreads) append_own_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int N = Vec<T>::N, kLanes = D / N / 2, kAtOnce = kPagedThreads / kLanes, kBatch = kAppendOwnBatch;
-    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    extern __shared__ __align__(16) float2 cs[];  // [tokens_per][R / 2] cos, sin
     __shared__ Places s;
     grid_dependency_wait();
     const PagedCache &c = p.c;
@@ -205,7 +205,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPagedThreads) append_q4_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int kLanes = D / 8, kAtOnce = kPagedThreads / kLanes, kBatch = 4;
-    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    extern __shared__ __align__(16) float2 cs[];  // [tokens_per][R / 2] cos, sin
     __shared__ Places s;
     __shared__ char *s_codes[2][kAppendTokens], *s_groups[2][kAppendTokens];
     grid_dependency_wait();
@@ -321,7 +321,7 @@ template <typename T, bool Q4, int D>
 __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int kLanes = D / 4, kAtOnce = kPagedThreads / kLanes, kBatch = 4;
-    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    extern __shared__ __align__(16) float2 cs[];  // [tokens_per][R / 2] cos, sin
     __shared__ Places s;
     grid_dependency_wait();
     const PagedCache &c = p.c;

@@ -32,7 +32,7 @@ template <typename T>
 __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const __grid_constant__ RotParams p)
 {
     constexpr int N = Vec<T>::N;
-    extern __shared__ float2 cs[];  // [R / 2] cos, sin
+    extern __shared__ __align__(16) float2 cs[];  // [R / 2] cos, sin
     grid_dependency_wait();
     const long long bt = blockIdx.x;
     const long long b = bt / p.tokens, t = bt - b * p.tokens;
@@ -92,7 +92,7 @@ template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_constant__ RotParams p)
 {
     constexpr int N = Vec<T>::N, kBatch = INTER ? 4 : 2;
-    extern __shared__ float2 cs[];  // [tokens_per][R / 2] cos, sin
+    extern __shared__ __align__(16) float2 cs[];  // [tokens_per][R / 2] cos, sin
     grid_dependency_wait();
     const uint32_t half = p.R / 2;
     const uint32_t pairs = INTER ? 0 : half / N;                       // units of two chunks a head

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreadsF32, (F32Layout<D, R>::kCtas)) attn_f3
     constexpr int RM = R / 16;      // rows of a thread
     constexpr int KM = kBK / 16;    // keys of a thread
     constexpr int CV = D / 64;      // float4 columns of a thread's output
-    extern __shared__ float fsm[];
+    extern __shared__ __align__(16) float fsm[];
     float *sQ = fsm, *sK = sQ + R * L::kQ, *sV = sK + kBK * L::kQ, *sP = sV + kBK * L::kQ;
 
     grid_dependency_wait();
