@@ -100,13 +100,26 @@ __device__ __forceinline__ void q4_group(float lo, float hi, bool finite, uint32
 {
     // (8 hi + 7 lo) / 15, by sixteenths so that it cannot overflow
     base = __bfloat162float(__float2bfloat16_rn(q4_divide(fmaf(hi, 0.5f, lo * 0.4375f), 0.9375f, 1.f / 0.9375f)));
-    step = fmaxf(q4_divide(hi - base, 7.f, 1.f / 7.f), (base - lo) * 0.125f);
+    // (by eighths, as base - lo can pass the largest fp32 value)
+    step = fmaxf(q4_divide(hi - base, 7.f, 1.f / 7.f), base * 0.125f - lo * 0.125f);
     step = __uint_as_float((__float_as_uint(step) + 0xFFFFu) & 0xFFFF0000u);  // (>= 0: up)
     if (!finite) {
         base = __uint_as_float(0x7FC00000u);
         step = 0.f;
     }
     base_step = (__float_as_uint(base) >> 16) | (__float_as_uint(step) & 0xFFFF0000u);
+}
+
+// Values of a group for q4_code: those of a step of 2^100 and more are scaled by 2^-64, so that no difference to the base
+// overflows. Nothing but the codes may be taken from them then.
+template <int N> __device__ __forceinline__ void q4_in_range(float (&v)[N], float &base, float &step)
+{
+    if (step < 1.2676506e30f) return;
+    constexpr float by = 5.4210109e-20f;
+    base *= by;
+    step *= by;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= by;
 }
 
 // 1 / step, 0 for none. (Of steps below 2^-126, 2^126: their codes end at 0 or 15.)

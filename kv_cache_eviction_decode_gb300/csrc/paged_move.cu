@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kPagedThreads) append_q4_kernel(const __grid_c
                 char *const to = s_codes[w][t];
                 if (tk[u] < nt && to) {
                     const long long head = (ha + hd[u]) * head_bytes;
+                    q4_in_range(v, base, step);
                     const float inverse = q4_inverse(step);
                     *reinterpret_cast<uint16_t *>(to + head + byte) = q4_codes(v, base, step, inverse);
                     *reinterpret_cast<uint16_t *>(to + head + byte + D / 16) = q4_codes(v + 4, base, step, inverse);
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const __grid_cons
                 float base, step;
                 q4_group(lo, hi, all == 0xffu, params, base, step);
                 const int g = lane & 7, j = lane >> 3;
+                q4_in_range(v, base, step);
                 *reinterpret_cast<uint16_t *>(block + slot * (D / 2) + (D / 16) * g + 2 * j) = q4_codes(v, base, step, q4_inverse(step));
                 if (g == 0) *reinterpret_cast<uint32_t *>(block + c.S * (D / 2) + slot * (D / 8) + 4 * j) = params;
             } else {
