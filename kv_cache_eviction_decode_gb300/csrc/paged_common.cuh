@@ -111,19 +111,21 @@ __device__ __forceinline__ void q4_group(float lo, float hi, bool finite, uint32
 }
 
 // Values of a group for q4_code: those of a step of 2^100 and more are scaled by 2^-64, so that no difference to the base
-// overflows. Nothing but the codes may be taken from them then.
+// overflows, those of a step below 2^-64 by 2^64, so that the step has a reciprocal and a quotient's remainder its bits
+// (they are no larger than 2^-35: a difference to the base below 2^-61 needs such neighbours). Nothing but the codes
+// may be taken from them then.
 template <int N> __device__ __forceinline__ void q4_in_range(float (&v)[N], float &base, float &step)
 {
-    if (step < 1.2676506e30f) return;
-    constexpr float by = 5.4210109e-20f;
+    if ((step >= 5.4210109e-20f && step < 1.2676506e30f) || step == 0.f) return;
+    const float by = step < 1.f ? 1.8446744e19f : 5.4210109e-20f;
     base *= by;
     step *= by;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] *= by;
 }
 
-// 1 / step, 0 for none. (Of steps below 2^-126, 2^126: their codes end at 0 or 15.)
-__device__ __forceinline__ float q4_inverse(float step) { return step > 0.f ? fminf(__fdividef(1.f, step), 8.507059173e37f) : 0.f; }
+// 1 / step, 0 for none.
+__device__ __forceinline__ float q4_inverse(float step) { return step > 0.f ? __fdividef(1.f, step) : 0.f; }
 
 // A code in the low bits of 2^23 + 2^22 + code, where fp32's step is 1: the sum rounds
 // (k + 1/2 to the even code).

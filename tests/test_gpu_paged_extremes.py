@@ -59,3 +59,19 @@ def test_far_apart(cuda_device, d, dtype, R):
     x = (x * torch.linspace(0.8, 1, x.shape[0], device="cuda", dtype=torch.float64)[:, None, None] * most).to(dtype)
     for codes, params in appended(x, R):
         check(x[:, 0].double(), codes, params)
+
+
+@pytest.mark.parametrize("R", [None, 64, 6])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_close_together(cuda_device, d, dtype, R):
+    """Groups whose steps are below the smallest normal value, down to nothing but zeros; a few around it; and values of one
+    size with such steps between them and without."""
+    x = values(dtype, d, 60)
+    x = x * torch.exp2(torch.linspace(-149, -115, 60, device="cuda", dtype=torch.float64).round())[:, None, None]
+    for codes, params in appended(x.to(dtype), R):
+        check(x.to(dtype)[:, 0].double(), codes, params)
+    x = torch.full_like(x, 2.0 ** -110) * (1 + 2.0 ** -7 * (values(dtype, d, 60) > 0))
+    x[::3] = torch.tensor([3.0e38, -1.5, 2.0 ** -126, 0.0], device="cuda", dtype=torch.float64).repeat(5)[:, None, None]
+    for codes, params in appended(x.to(dtype), R):
+        check(x.to(dtype)[:, 0].double(), codes, params)
