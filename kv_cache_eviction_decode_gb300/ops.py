@@ -83,8 +83,8 @@ def _ints(t, n: int, q: torch.Tensor, name: str) -> int:
 def _scale(scale) -> float:
     if scale is None:
         return 0.0
-    if not (scale > 0 and math.isfinite(scale)):
-        raise ValueError("scale: need a positive finite number")
+    if not (2.0 ** -150 < scale < 2.0 ** 128 - 2.0 ** 103):  # (0 in fp32 would be the default)
+        raise ValueError("scale: need a positive finite number in fp32's range")
     return float(scale)
 
 
