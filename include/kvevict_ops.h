@@ -70,9 +70,10 @@ extern "C" {
  *              sequence b owns the token rows q_starts[b] .. q_starts[b + 1] - 1
  *              of q, out and lse (q_rows of them in all) and k_starts[b] .. of
  *              k and v (k_rows in all); the sequence strides are ignored. No
- *              sequence has more than max_q queries; max_k, the most keys, only
- *              steers the launch. Rows outside every sequence are left as they
- *              were. lse is dense [q_rows][n_q_heads].
+ *              sequence has more than max_q queries (0: nothing is launched, and
+ *              no start looked at); max_k, the most keys, only steers the launch.
+ *              Rows outside every sequence are left as they were. lse is dense
+ *              [q_rows][n_q_heads].
  *   out and lse must not overlap q, k or v.
  *   V rows that no query of the sequence sees may hold anything, infinities
  *              and NaN included; K likewise. Rows that one query sees and

@@ -137,9 +137,9 @@ int kvevict_paged_gather(const kvevict_paged_gather_args *a, void *cuda_stream);
  *              the probabilities (4 bits: times the step) rounded to bf16 for the
  *              product with V (steps of V below 2^-50 lose precision, bases above
  *              2^60 may overflow); fp32 ones the CUDA cores, in fp32.
- *   max_q:     with starts: no sequence has more new tokens. max_k: the most keys
- *              of a sequence, or 0: as many as the table holds; it only steers the
- *              launch.
+ *   max_q:     with starts: no sequence has more new tokens (0: nothing is launched,
+ *              and no start looked at). max_k: the most keys of a sequence, or 0:
+ *              as many as the table holds; it only steers the launch.
  *   V rows that no query of the sequence sees may hold anything; of bf16 and fp32
  *              pages, rows that one query sees and another does not must be finite
  *              for the other's sake.

@@ -194,9 +194,9 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, n_sin
     Returns out (as q), or (out, lse) with return_lse or an lse tensor: fp32
     [B][Hq][N], or [T][Hq] packed. A row that sees nothing gives 0 and -inf.
     Rows behind q_lens, outside the starts or beyond max_q are not written (in
-    an output made here they hold anything). Lengths and starts out of range are
-    clamped and set DEV_BAD_LENGTH in error_word (int32 on the device; None: see
-    operator_errors).
+    an output made here they hold anything). Lengths and starts out of range, and
+    sequences of more than max_q queries (0 counts as 1), are clamped and set
+    DEV_BAD_LENGTH in error_word (int32 on the device; None: see operator_errors).
     """
     if q.requires_grad or k.requires_grad or v.requires_grad or (out is not None and out.requires_grad):
         _forward_only("window_attention", q, k, v, out)
@@ -250,7 +250,7 @@ def _window_layout(q, k, v, n_sink, window, scale, q_starts, max_q, max_k) -> _L
             raise ValueError("packed: give q_starts, k_starts, max_q and max_k, and no lengths")
         if max_q < 0 or max_k < 0:
             raise ValueError("max_q, max_k: need 0 or more")
-        max_q, max_k = min(max_q, _INT_MAX), min(max_k, _INT_MAX)
+        max_q, max_k = min(max(max_q, 1), _INT_MAX), min(max_k, _INT_MAX)
         B = q_starts.shape[0] - 1
         N, Hq, M, Hkv = q.shape[0], q.shape[1], k.shape[0], k.shape[1]
         strides = [(0, t.stride(1), t.stride(0)) for t in (q, k, v)]

@@ -206,11 +206,12 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     query at position p sees the keys up to p that are among the first n_sink or the
     newest `window` (None: all), as in window_attention(). T / B tokens of every
     sequence (one: a decode step; a few: drafted ones), or with q_starts (and max_q,
-    the longest) any number. max_k, the most keys of a sequence, only steers the
-    launch (None: as many as the table holds). Returns out (as q), or (out, lse
-    [T][Hq]) with return_lse or an lse tensor; a row that sees nothing gives 0 and
-    -inf. For the many tokens of a prompt's chunk paged_gather() and
-    window_attention() are faster."""
+    the longest; 0 counts as 1) any number: of a sequence with more than max_q the
+    first ones are taken, and DEV_BAD_LENGTH is set in error_word. max_k, the most
+    keys of a sequence, only steers the launch (None: as many as the table holds).
+    Returns out (as q), or (out, lse [T][Hq]) with return_lse or an lse tensor; a row
+    that sees nothing gives 0 and -inf. For the many tokens of a prompt's chunk
+    paged_gather() and window_attention() are faster."""
     if q.requires_grad or k_pages.requires_grad or v_pages.requires_grad or (out is not None and out.requires_grad):
         _forward_only("paged_attention", q, k_pages, v_pages, out)
     key = ("attention", q.dtype, q.get_device(), q.shape, q.stride(), *_pages_key(k_pages, v_pages, block_table, kv_lens), n_sink, window,
@@ -248,7 +249,8 @@ def _attention_layout(q, k_pages, v_pages, block_table, q_starts, max_q, max_k, 
         raise ValueError(f"q: {Hq} heads, the pages have {shape[3]}")
     _per_sequence(T, q_starts, lay.batch, "q")
     lay.head = struct.pack("@8i", *shape)
-    lay.tail = _ATTENTION_HEAD.pack(Hq, min(n_sink, _INT_MAX), min(window, _INT_MAX), min(max_q or 0, _INT_MAX), min(max_k or 0, _INT_MAX),
+    # (a call that launches nothing would not report sequences with new tokens that max_q = 0 denies)
+    lay.tail = _ATTENTION_HEAD.pack(Hq, min(n_sink, _INT_MAX), min(window, _INT_MAX), min(max(max_q or 0, 1), _INT_MAX), min(max_k or 0, _INT_MAX),
                                     _scale(scale), T)
     lay.lse_shape = q.shape[:2]
     lay.out_shape = (d, Hq * d)  # a dense output's strides
