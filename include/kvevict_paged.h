@@ -131,8 +131,9 @@ int kvevict_paged_gather(const kvevict_paged_gather_args *a, void *cuda_stream);
  * the query's own place), which also says what a row without keys gives.
  *   q, out:    [tokens][n_q_heads][head_dim], strides (head, token) positive
  *              multiples of 16 bytes; n_q_heads a multiple of n_kv_heads, at most
- *              64 times it. lse: dense fp32 [tokens][n_q_heads] or NULL. out and
- *              lse must not overlap q or the pages.
+ *              64 times it. A sequence's new tokens times n_q_heads / n_kv_heads:
+ *              fewer than 2^31 - 16. lse: dense fp32 [tokens][n_q_heads] or NULL.
+ *              out and lse must not overlap q or the pages.
  *   Sums, softmax statistics and lse are fp32. bf16 queries take the tensor cores,
  *              the probabilities (4 bits: times the step) rounded to bf16 for the
  *              product with V (steps of V below 2^-50 lose precision, bases above

@@ -1,6 +1,7 @@
 // api_paged.cu -- host side of the operators on a paged cache
 // (include/kvevict_paged.h): argument checks, how the work is cut, launches.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "api_internal.h"
@@ -169,6 +170,7 @@ int plan_attention(const kvevict_paged_attention_args *a, Plan &w)
     p.mask.q_starts = a->q_starts;
     const bool tensor = a->c.dtype == KVEVICT_BF16, q4 = a->c.page_dtype == KVEVICT_Q4;
     const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
+    if (rows > INT_MAX - 16) return KVEVICT_ERR_INVALID_ARG;  // a unit's rows are ints in the kernels
     w.rows = tensor ? (rows <= 8 ? 8 : 16) : rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
     p.q_tiles = static_cast<int>((rows + w.rows - 1) / w.rows);
     const int64_t units = static_cast<int64_t>(a->c.batch) * a->c.n_kv_heads * p.q_tiles;
