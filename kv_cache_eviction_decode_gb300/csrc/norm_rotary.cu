@@ -15,6 +15,7 @@
 #include <cmath>
 
 #include "launch.h"
+#include "norm_rotary.h"
 #include "rotary_common.cuh"
 
 namespace kvevict {
@@ -35,10 +36,6 @@ __device__ __forceinline__ void copy16(uint4 *dst, const void *src)
 }
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-constexpr int kNormStages = 4;
-constexpr int kNormPairs = 256;  // of a head of 64 chunks at most
-
 
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, 4) norm_rotary_kernel(const __grid_constant__ NormParams np)
@@ -234,37 +231,21 @@ __global__ void __launch_bounds__(kRotThreads) norm_rotary_any_kernel(const __gr
     }
 }
 
-// A CTA's share of tokens (all heads), or of one token's heads where there are few
-// tokens: what lets whole waves of four CTAs an SM end soonest, a CTA taking what
-// its rows take and as much as kStart times its 256 threads' rows to find its way
-// and its cosines. (16384 tokens, 64 + 8 heads of 128: 108 us, 82% of the copy
-// bandwidth, 111 with 4 tokens a CTA; 3 x 2049 tokens, 12 + 4 heads, 48 of 128 in
-// fp32: 26 us, 30 with ten tokens a CTA.)
-constexpr int kStart = 5;
-
 long long norm_shares(NormParams &np)
 {
     RotParams &p = np.r;
-    const long long heads = p.heads[0] + p.heads[1], step = kRotThreads / np.lanes, slots = 4 * 152;
+    const long long heads = p.heads[0] + p.heads[1], step = kRotThreads / np.lanes;
     p.heads_per = static_cast<uint32_t>(heads);
     p.head_blocks = 1;
     p.tokens_per = 1;
-    if (p.total < slots / 2) {
+    if (p.total < kNormSlots / 2) {
         // few tokens: two trips of a CTA's threads at most
-        const long long want = std::max(step, p.total * heads / (slots / 2));
+        const long long want = std::max(step, p.total * heads / (kNormSlots / 2));
         p.heads_per = static_cast<uint32_t>(std::min(heads, want));
         p.head_blocks = static_cast<uint32_t>((heads + p.heads_per - 1) / p.heads_per);
         return p.total * p.head_blocks;
     }
-    double least = 0;
-    for (long long t = 1; t <= std::min<long long>(64, 8192 / std::max(p.R, 2)); ++t) {
-        const long long waves = ((p.total + t - 1) / t + slots - 1) / slots;
-        const double cost = static_cast<double>(waves) * (static_cast<double>(t * heads) / static_cast<double>(step) + kStart);
-        if (t == 1 || cost < least * 0.995) {
-            least = cost;
-            p.tokens_per = static_cast<uint32_t>(t);
-        }
-    }
+    p.tokens_per = static_cast<uint32_t>(norm_tokens(p.total, heads, step, p.R));
     return (p.total + p.tokens_per - 1) / p.tokens_per;
 }
 
@@ -279,10 +260,9 @@ template <typename T> cudaError_t launch_norm(NormParams &np, bool chunks, uint3
             rc = KVEVICT_ERR_INVALID_ARG;
             return cudaSuccess;
         }
-        constexpr int kOwn = kNormStages * 2 * kRotThreads * 16;
-        const size_t smem = static_cast<size_t>(p.tokens_per) * (p.R / 2) * sizeof(float2) + kOwn;
+        const size_t smem = static_cast<size_t>(p.tokens_per) * (p.R / 2) * sizeof(float2) + kNormOwn;
         auto kern = p.interleaved ? norm_rotary_kernel<T, true> : norm_rotary_kernel<T, false>;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwn + 8192 * static_cast<int>(sizeof(float2)) / 2);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormOwn + kNormTable);
         if (e != cudaSuccess) return e;
         return launch_dependent(kern, static_cast<unsigned>(blocks), kRotThreads, smem, st, np);
     }
