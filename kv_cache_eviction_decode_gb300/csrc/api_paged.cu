@@ -178,8 +178,8 @@ int plan_attention(const kvevict_paged_attention_args *a, Plan &w)
     // (with starts only the mean of the new tokens is known here)
     const int64_t mean = a->c.batch ? (a->tokens + a->c.batch - 1) / a->c.batch * p.G : 0;
     const int64_t busy = static_cast<int64_t>(a->c.batch) * a->c.n_kv_heads * std::min<int64_t>(p.q_tiles, (mean + w.rows - 1) / w.rows);
-    p.splits = parts(busy, tiles, kSMs * (!tensor || (q4 && w.rows == 8) ? 3 : 2), q4 && tensor ? 1 : tensor || q4 ? 0.5 : 0.25, p.mask.window > 0,
-                     p.clusters);
+    const int ctas = tensor ? paged_mma_ctas(q4, w.rows) : paged_simt_ctas(q4, a->c.head_dim, w.rows);
+    p.splits = parts(busy, tiles, kSMs * ctas, q4 && tensor ? 1 : tensor || q4 ? 0.5 : 0.25, p.mask.window > 0, p.clusters);
     w.items = units * p.splits;
     if (w.items >= (int64_t{1} << 31)) return KVEVICT_ERR_INVALID_ARG;
     const size_t slots = static_cast<size_t>(p.splits) * a->tokens * p.Hq;

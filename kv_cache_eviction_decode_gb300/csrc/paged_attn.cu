@@ -6,8 +6,9 @@
 // holds eight channels of up to eight query rows and of their outputs, D / 8 lanes a key.
 // The partial products of a key are added up so that each lane ends with one row's
 // logit (halving exchanges), which is also how softmax is spread. 8 sequences to 8000
-// tokens, 8 heads of 128, one token each: 78 us (4.9 TB/s), 233 with items of eight
-// rows whatever there are and nothing read ahead; 32 heads over 8: 95 (237).
+// tokens, 8 heads of 128, one token each: 74 us (5.2 TB/s; with items of eight rows
+// whatever there are and nothing read ahead the first version took 233); 32 heads over
+// 8: 88 (237).
 #include <cmath>
 
 #include "launch.h"
@@ -78,7 +79,7 @@ template <bool Q4> struct Raw {
 // one of eight. With up to four, V's rows and the next tile's K are on their way
 // while a tile's logits and products are made.
 template <bool Q4, int D, int R>
-__global__ void __launch_bounds__(kSimtWarps * 32) paged_simt_kernel(const __grid_constant__ PagedAttnParams p)
+__global__ void __launch_bounds__(kSimtWarps * 32, paged_simt_ctas(Q4, D, R)) paged_simt_kernel(const __grid_constant__ PagedAttnParams p)
 {
     constexpr int kLanes = D / 8, kKeys = 32 / kLanes, U = kPagedTile / kKeys;  // lanes a key, keys at once, steps a tile
     constexpr int kShift = R == 8 ? (D == 128 ? 1 : 0) : R == 4 ? (D == 128 ? 2 : 1) : R == 2 ? (D == 128 ? 3 : 2) : (D == 128 ? 4 : 3);

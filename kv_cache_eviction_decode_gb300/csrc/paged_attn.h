@@ -86,6 +86,16 @@ __device__ __forceinline__ float paged_join_peers(const float *o, const float *m
     return total;
 }
 
+// CTAs that an SM holds, by their registers (which the launch bounds hold to this) and,
+// bf16 pages, their rings. What the planner counts on: with three of every fp32 kernel,
+// where some have room for two and others for five, clusters ran in waves, 26 us for 8
+// sequences of 1008 tokens, 8 heads of 128, instead of 17.
+constexpr int paged_simt_ctas(bool q4, int head_dim, int rows)
+{
+    return rows == 8 ? 2 : !q4 ? (head_dim == 128 ? 2 : rows == 1 ? 4 : 3) : head_dim == 128 ? (rows == 4 ? 3 : 4) : rows == 4 ? 4 : 5;
+}
+constexpr int paged_mma_ctas(bool q4, int rows) { return q4 && rows == 8 ? 3 : 2; }
+
 // fp32 queries on the CUDA cores; rows: 1, 2, 4 or 8 of an item.
 cudaError_t launch_paged_simt(const PagedAttnParams &p, int head_dim, bool q4, int rows, cudaStream_t st);
 // bf16 queries on the tensor cores; rows: 8 or 16 of an item.
