@@ -113,7 +113,7 @@ int kvevict_paged_append(const kvevict_paged_append_args *a, void *cuda_stream);
  *              ascending); strides (sequence, head, token) positive multiples of 16
  *              bytes. Rows behind a sequence's kv_lens, or outside the starts, are
  *              left as they were; a sequence longer than its rows or its table is
- *              cut (BAD_LENGTH).
+ *              cut (BAD_LENGTH; rows = 0: nothing is launched, and no length looked at).
  */
 typedef struct {
     kvevict_paged_cache c;

@@ -433,6 +433,10 @@ __global__ void __launch_bounds__(kPagedThreads) gather_kernel(const __grid_cons
     const int row0 = tile * kGatherRows, count = min(kGatherRows, p.rows - row0);
     uint32_t bits = 0;
     if (p.k_starts) paged_owners<kPagedThreads>(p.k_starts, c.batch, p.rows, row0, count, s_seq, &s_fall, bits);
+    if (p.k_starts && blockIdx.x == 0) {  // (what has no rows is in no CTA's share)
+        for (int j = tid; j < c.batch; j += kPagedThreads)
+            if (paged_rows(p.k_starts, j, 0, p.rows).n == 0 && c.kv_lens[j] != 0) bits |= KVEVICT_DEV_BAD_LENGTH;
+    }
     if (tid < count) {
         const int b = p.k_starts ? s_seq[tid] : b0;
         int page = -1;
