@@ -28,6 +28,8 @@ extern "C" {
  *   base = bf16(8/15 hi + 7/15 lo), hi and lo the group's largest and smallest;
  *   step = max((hi - base) / 7, (base - lo) / 8), rounded up to bf16;
  *   code = round((x - base) / step) + 8, ties to even, in 0 .. 15 (8 where step is 0).
+ * (The ends of a group that reaches within a 64th of the type's largest number may
+ * stand for an infinity, as the step is rounded up.)
  * A page's block for one head, [page_size * 5 head_dim / 8] bytes, contiguous:
  * first the codes [page_size][head_dim / 2], then [page_size][head_dim / 32]
  * groups of (base, step). Channel 32 j + 4 g + i of a row (j the group, g 0 .. 7,
@@ -85,9 +87,9 @@ typedef struct {
  *              none of them is looked at.
  * Tokens before the first place or behind the table (BAD_LENGTH) and in no page
  * (BAD_PAGE) are dropped, and so is every sequence of starts that go back from the
- * first such on. k and v must not overlap the pages. Two tokens that the tables put in one place, or a call that reads
- * the pages at the same time, give undefined contents there. Other rows of the
- * pages are left as they were.
+ * first such on. k and v must not overlap the pages. Two tokens that the tables put
+ * in one place, or a call that reads the pages at the same time, give undefined
+ * contents there. Other rows of the pages are left as they were.
  */
 typedef struct {
     kvevict_paged_cache c;
@@ -136,8 +138,9 @@ int kvevict_paged_gather(const kvevict_paged_gather_args *a, void *cuda_stream);
  *              out and lse must not overlap q or the pages.
  *   Sums, softmax statistics and lse are fp32. bf16 queries take the tensor cores,
  *              the probabilities (4 bits: times the step) rounded to bf16 for the
- *              product with V (steps of V below 2^-50 lose precision, bases above
- *              2^60 may overflow); fp32 ones the CUDA cores, in fp32.
+ *              product with V; over 4 bits steps of V below 2^-50 lose precision,
+ *              and bases of V above 2^60 or queries of 2^118 may overflow. fp32 ones
+ *              take the CUDA cores, in fp32.
  *   max_q:     with starts: no sequence has more new tokens (0: nothing is launched,
  *              and no start looked at). max_k: the most keys of a sequence, or 0:
  *              as many as the table holds; it only steers the launch.

@@ -6,8 +6,11 @@
 // (cp.async), keeps its own softmax, and only at the end are a CTA's warps joined.
 // The products are transposed, S^T = K Q^T and O^T = V^T P^T, with keys and then
 // channels on the 16-wide axis of mma.m16n8k16 and query rows on the 8-wide one:
-// eight query heads of a KV head fill an instruction. (tcgen05 would want 64 or 128
-// rows.) P^T comes from S^T by transposing 8 x 8 blocks in registers (movmatrix).
+// eight query heads of a KV head fill an instruction. (tcgen05 could have the keys on
+// its long axis in the same way, but takes them from shared or tensor memory as bf16:
+// four times the bytes of 4-bit codes, written there first. bf16 pages are at their
+// bytes without it.) P^T comes from S^T by transposing 8 x 8 blocks in registers
+// (movmatrix).
 //
 // 4 bits: a code needs a mask and nothing else to be a matrix operand. bf16's bit
 // patterns 0 .. 255 are the values 0 .. 255 times 2^-133 (its subnormals and, with
@@ -32,7 +35,8 @@
 // words), 19 products at eight, ten transposes at four, 340 in all, against 437 cycles
 // for the bytes; 580 are taken, because three warps a quarter (168 registers) do not
 // cover a warp's chain. Two tiles at a time give it a second one (252 us with one); four
-// spill (272 at that stage), and four CTAs of 128 registers with one tile, 223.
+// spill (272 at that stage), and four CTAs of 128 registers with one tile gained nothing
+// (250).
 #include <cfloat>
 #include <cmath>
 
@@ -556,8 +560,6 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 3 : 2)) paged_mma_kern
                     for (int a = 0; a < NT; ++a) {
                         const uint32_t b0 = transpose8x8(pack_bf16x2(z[h][a][0] * st0, z[h][a][1] * st0));
                         const uint32_t b1 = transpose8x8(pack_bf16x2(z[h][a][2] * st1, z[h][a][3] * st1));
-                        
-                        
                         mma_next(o[a][2 * j], less<8>(code(v0)), less<136>(v0), less<8>(code(v1)), less<136>(v1), b0, b1);
                         mma_next(o[a][2 * j + 1], less<8>(code(y0)), less<136>(y0), less<8>(code(y1)), less<136>(y1), b0, b1);
                     }

@@ -123,7 +123,7 @@ def _error_word(t, q: torch.Tensor) -> int:
 
 def operator_errors(device=None) -> int:
     """Waits for the device (None: the current one); returns the error bits that calls without an error_word have set
-    on it since the last time (0: clean; DEV_BAD_LENGTH, DEV_WAIT_TIMEOUT), and clears them."""
+    on it since the last time (0: clean; DEV_BAD_LENGTH, DEV_BAD_PAGE, DEV_WAIT_TIMEOUT), and clears them."""
     if device is not None and torch.device(device).type != "cuda":
         raise ValueError(f"operator_errors: need a CUDA device, got {device}")
     w = ctypes.c_uint32(0)

@@ -208,10 +208,13 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     sequence (one: a decode step; a few: drafted ones), or with q_starts (and max_q,
     the longest; 0 counts as 1) any number: of a sequence with more than max_q the
     first ones are taken, and DEV_BAD_LENGTH is set in error_word. max_k, the most
-    keys of a sequence, only steers the launch (None: as many as the table holds).
+    keys of a sequence, only steers the launch (None: as many as the table holds,
+    which a table much wider than its sequences makes a slower plan of).
     Returns out (as q), or (out, lse [T][Hq]) with return_lse or an lse tensor; a row
-    that sees nothing gives 0 and -inf. For the many tokens of a prompt's chunk
-    paged_gather() and window_attention() are faster."""
+    that sees nothing gives 0 and -inf. bf16 queries round the probabilities to bf16
+    for the product with V, and over 4 bits want V's steps above 2^-50, its bases
+    below 2^60 and queries below 2^118; fp32 ones are computed in fp32. For the many
+    tokens of a prompt's chunk paged_gather() and window_attention() are faster."""
     if q.requires_grad or k_pages.requires_grad or v_pages.requires_grad or (out is not None and out.requires_grad):
         _forward_only("paged_attention", q, k_pages, v_pages, out)
     key = ("attention", q.dtype, q.get_device(), q.shape, q.stride(), *_pages_key(k_pages, v_pages, block_table, kv_lens), n_sink, window,

@@ -1,11 +1,12 @@
-"""4-bit groups at the ends of fp32's range. The bounds of check_groups in tests/paged_reference.py with the absolute term
-of fp32's own grid instead of one that hides these groups: differences and products below 2^-126 are off by 2^-150 each,
-eight of them at most (2^-147), and a base or a step is rounded on bf16's grid, 2^-133 there."""
+"""4-bit groups, and queries over them, at the ends of fp32's range. The bounds of check_groups in tests/paged_reference.py
+with the absolute term of fp32's own grid instead of one that hides these groups: differences and products below 2^-126 are
+off by 2^-150 each, eight of them at most (2^-147), and a base or a step is rounded on bf16's grid, 2^-133 there."""
 import pytest
 import torch
 
 import kv_cache_eviction_decode_gb300 as kv
 from tests.paged_reference import Pool, parts, unpack
+from tests.test_gpu_paged_attention import check_sequence
 
 pytestmark = pytest.mark.gpu
 GRID = 2.0 ** -133
@@ -75,3 +76,19 @@ def test_close_together(cuda_device, d, dtype, R):
     x[::3] = torch.tensor([3.0e38, -1.5, 2.0 ** -126, 0.0], device="cuda", dtype=torch.float64).repeat(5)[:, None, None]
     for codes, params in appended(x.to(dtype), R):
         check(x.to(dtype)[:, 0].double(), codes, params)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", [(4, 1), (8, 2)])
+@pytest.mark.parametrize("up", [-100, -30, 30, 90, 114])
+def test_queries_of_any_size(cuda_device, up, G, n, d):
+    """Queries up to 2^118 and keys as much smaller, and the other way around: the same logits."""
+    lens = [300, 40]
+    pool = Pool(lens, 2, 16, d, torch.bfloat16, True, seed=3)
+    parts(pool.k, d)[1].mul_(2.0 ** -up)
+    q = torch.randn(2 * n, 2 * G, d, device="cuda", dtype=torch.bfloat16, generator=torch.Generator(device="cuda").manual_seed(8)) * 2.0 ** up
+    assert float(q.abs().max()) < 2.0 ** 118
+    out, lse = kv.paged_attention(q, pool.k, pool.v, pool.table, pool.kv_lens, return_lse=True)
+    for b, m in enumerate(lens):
+        rows = slice(b * n, b * n + n)
+        check_sequence(pool, b, q[rows], out[rows], lse[rows], m, 0, None, d ** -0.5)
